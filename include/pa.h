@@ -185,7 +185,8 @@ int pa_reshape_and_cache_opt(const pa_tensor *key, const pa_tensor *value, pa_te
  * Head sizes built: 64, 128, 256 (FP8 caches: 128, 256).
  * Uses a library-held workspace on the current device (grown on demand with
  * cudaMallocAsync and zero-filled on `stream`); calls that use it on different
- * streams must not overlap.  FP8 scales are 1.0 here; use pa_decode_ex for scales, a caller-owned
+ * streams must not overlap.  A stream capture cannot grow it (PA_ERR_WORKSPACE): run a call
+ * of the shape once before capturing it.  FP8 scales are 1.0 here; use pa_decode_ex for scales, a caller-owned
  * workspace, an explicit partition size or a device error word.
  */
 int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
@@ -224,7 +225,9 @@ int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, cons
  *                     Zero-fill it once before its first use: it holds per-unit
  *                     arrival counters that every call leaves at zero again.  The
  *                     library owns its contents between calls, and calls that
- *                     share one workspace must not run concurrently.
+ *                     share one workspace must not run concurrently.  Calls with
+ *                     other numbers of sequences or heads place their counters and
+ *                     their states elsewhere in it: zero-fill it again between those.
  *   device_error      device int to OR error bits into, or NULL.
  * Split-KV runs in the one decode launch: each partition's CTA stores its
  * (max, exp-sum, partial output) state and the last CTA of a (sequence, kv head)

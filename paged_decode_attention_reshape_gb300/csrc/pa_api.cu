@@ -296,12 +296,52 @@ WsLayout workspace_layout(int S, int Hq, int Hkv, int D, int maxNB, int P, int f
 
 // ------------------------------------------------------ internal workspace
 
+// One growing allocation per device: an arrival-counter region, then the partial states of
+// the call.  The counter region keeps its size between calls (and is zero between them), so
+// a call of one shape never leaves its partial states where a call of another shape, with
+// more units, looks for its counters.
 struct DevWorkspace {
   void *ptr = nullptr;
-  size_t bytes = 0;
+  size_t bytes = 0;     // the whole allocation
+  size_t counters = 0;  // its counter region
+  bool captured = false;  // a captured graph holds the address: the allocation outlives its use here
 };
 std::mutex g_ws_mu;
 DevWorkspace g_ws[64];
+
+// The current device's workspace with room for `counters` bytes of arrival counters and `data`
+// bytes behind them.  Growing it allocates and clears, which a stream capture would turn into
+// memory of that graph, so a capture must find it large enough (PA_ERR_WORKSPACE): run the
+// call once before capturing it.
+int internal_workspace(size_t counters, size_t data, cudaStream_t st, DevWorkspace *out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return PA_ERR_CUDA;
+  std::lock_guard<std::mutex> g(g_ws_mu);
+  DevWorkspace &w = g_ws[dev];
+  if (w.counters < counters || w.bytes - w.counters < data) {
+    if (cap != cudaStreamCaptureStatusNone) return PA_ERR_WORKSPACE;
+    const size_t nc = std::max(w.counters, counters), nd = std::max(w.bytes - w.counters, data);
+    if (w.ptr && !w.captured) cudaFreeAsync(w.ptr, st);
+    w = DevWorkspace{};
+    void *ptr = nullptr;
+    if (cudaMallocAsync(&ptr, nc + nd, st) != cudaSuccess) {
+      (void)cudaGetLastError();  // the failed allocation is reported here, not by a later launch
+      return PA_ERR_CUDA;
+    }
+    if (cudaMemsetAsync(ptr, 0, nc, st) != cudaSuccess) {
+      cudaFreeAsync(ptr, st);
+      return PA_ERR_CUDA;
+    }
+    w.ptr = ptr;
+    w.bytes = nc + nd;
+    w.counters = nc;
+  }
+  if (cap != cudaStreamCaptureStatusNone) w.captured = true;
+  *out = w;
+  return PA_OK;
+}
 
 // ------------------------------------------------------------- validation
 
@@ -633,27 +673,19 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   }
   if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0) {
     const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, maxNB, P, pl.flat);
+    size_t ml_off = lay.ml_off;
     if (internal_ws) {
-      int dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
-      std::lock_guard<std::mutex> g(g_ws_mu);
-      DevWorkspace &w = g_ws[dev];
-      if (w.bytes < lay.total) {
-        if (w.ptr) cudaFreeAsync(w.ptr, st);
-        w.ptr = nullptr;
-        w.bytes = 0;
-        if (cudaMallocAsync(&w.ptr, lay.total, st) != cudaSuccess) return PA_ERR_CUDA;
-        if (cudaMemsetAsync(w.ptr, 0, lay.total, st) != cudaSuccess) return PA_ERR_CUDA;
-        w.bytes = lay.total;
-      }
+      DevWorkspace w;
+      if ((r = internal_workspace(lay.ml_off, lay.total - lay.ml_off, st, &w))) return r;
       workspace = w.ptr;
-      workspace_bytes = w.bytes;
+      ml_off = w.counters;
+    } else {
+      if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+      if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
     }
-    if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
     p.counters = static_cast<int *>(workspace);
-    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + lay.ml_off);
-    p.part_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + lay.acc_off);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ml_off);
+    p.part_acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + ml_off + (lay.acc_off - lay.ml_off));
   }
 
   cudaError_t e;
