@@ -8,6 +8,7 @@
  *                          ("Inside vLLM CUDA Kernels: KV-Cache Writes and Paged
  *                          Attention", Part 2; "How vLLM CUDA Kernels Write and
  *                          Read the Paged KV Cache", "Writing K and V into the cache")
+ *   pa_gather_cache        the rows of given slots read back as values
  *   pa_decode / _ex        single-query paged decode attention with GQA, online
  *                          softmax and split-KV partitions merged by a
  *                          log-sum-exp reduce ("Inside vLLM CUDA Kernels", Part 3;
@@ -35,6 +36,14 @@
  *    16 x head_size elements; with the default contiguous strides it is one
  *    contiguous run of memory.  Other strides for the two outer dimensions are
  *    accepted (for instance K and V as views of one [num_blocks, 2, ...] tensor).
+ *  - 4-bit caches (PA_FP4_E2M1): k_cache and v_cache are each [num_blocks, num_kv_heads,
+ *    9 * head_size] BYTES (strides in bytes, innermost 1, head_size 64, 128 or 256), a
+ *    page of 9 * head_size bytes per (block, kv head): first 16 x head_size / 2 bytes of
+ *    E2M1 codes, then 16 x head_size / 16 E4M3 scales.  Byte b of token t's codes holds
+ *    elements 2b (low half) and 2b + 1, and lies, with r = min(64, head_size / 2) and
+ *    lin = t * r + b % 64, at (b / 64) * 1024 + (lin ^ (((lin >> 7) & 3) << 5)); scale j of
+ *    token t (elements 16 j .. 16 j + 15) lies at 8 * head_size + t * head_size / 16 + j.
+ *    The element's value is code * scale * k_scale (v_scale).
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *    default stream) and never synchronise, except pa_check_device_error and
  *    pa_profile_read.
@@ -63,12 +72,16 @@ typedef enum {
     PA_F16 = 2,
     PA_FP8_E4M3 = 3, /* OCP OFP8 E4M3: bias 7, no infinities, max 448 */
     PA_I32 = 4,
-    PA_I64 = 5
+    PA_I64 = 5,
+    PA_FP4_E2M1 = 6  /* 4-bit cache pages: OCP E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and
+                        their negatives) with an E4M3 scale per 16 elements; caches only,
+                        given as page bytes (see below) */
 } pa_dtype;
 
 typedef enum {
     PA_KV_AUTO = 0,     /* cache element type == key/value element type: bit copy */
-    PA_KV_FP8_E4M3 = 1  /* quantise to E4M3 with a per-tensor scale */
+    PA_KV_FP8_E4M3 = 1, /* quantise to E4M3 with a per-tensor scale */
+    PA_KV_FP4_E2M1 = 2  /* quantise to 4-bit pages: E2M1 codes, an E4M3 scale per 16 elements */
 } pa_kv_dtype;
 
 typedef enum {
@@ -111,7 +124,8 @@ typedef struct {
  *   key, value    [T, Hkv, D], PA_F32 / PA_BF16 / PA_F16 (same type for both);
  *                 innermost stride 1; the token and head strides are free.
  *   k_cache,      [num_blocks, Hkv, 16, D]; element type == key's for PA_KV_AUTO,
- *   v_cache       PA_FP8_E4M3 for PA_KV_FP8_E4M3.  Written in place.
+ *   v_cache       PA_FP8_E4M3 for PA_KV_FP8_E4M3; [num_blocks, Hkv, 9 D] PA_FP4_E2M1
+ *                 for PA_KV_FP4_E2M1.  Written in place.
  *   slot_mapping  PA_I64 [T].  Row t goes to cache slot slot_mapping[t];
  *                 a negative entry writes nothing for row t.  Entries
  *                 >= num_blocks * 16 write nothing and set PA_DEVERR_SLOT_RANGE.
@@ -120,6 +134,10 @@ typedef struct {
  *                 stored as E4M3(fp32(x) / scale) -- one IEEE fp32 division
  *                 rounded to nearest, then round-to-nearest-even to E4M3 with
  *                 saturation to +-448 and NaN -> 0x7F.
+ *                 PA_KV_FP4_E2M1: per group of 16 elements, y = fp32(x) / scale,
+ *                 sg = E4M3(max(max |y| / 6, 2^-9)), code = E2M1(y / sg): IEEE fp32
+ *                 divisions rounded to nearest, conversions to nearest even with
+ *                 saturation.  A group with a NaN gets sg = NaN (0x7F) and codes 0.
  *   k_scale,      device pointers to one fp32 scale each (per tensor); NULL means
  *   v_scale       1.0.  Ignored for PA_KV_AUTO.
  *   device_error  device int to OR error bits into, or NULL.
@@ -141,7 +159,7 @@ int pa_reshape_and_cache(const pa_tensor *key, const pa_tensor *value, pa_tensor
  * scale, otherwise head h uses scale[h * kv_scale_stride]).
  */
 typedef struct {
-    const float *k_scale;  /* device fp32 scale(s) of an FP8 cache; NULL = 1.0 */
+    const float *k_scale;  /* device fp32 scale(s) of an FP8 or 4-bit cache; NULL = 1.0 */
     const float *v_scale;
     int64_t scale_stride;  /* 0: one scale for every KV head; > 0: KV head h uses
                               k_scale[h * scale_stride] and v_scale[h * scale_stride];
@@ -160,6 +178,26 @@ typedef struct {
 int pa_reshape_and_cache_opt(const pa_tensor *key, const pa_tensor *value, pa_tensor *k_cache,
                              pa_tensor *v_cache, const pa_tensor *slot_mapping, int kv_dtype,
                              const pa_write_options *opt, pa_stream_t stream);
+
+/*
+ * pa_gather_cache -- read rows of the paged cache back as values: the inverse of
+ * pa_reshape_and_cache (a cached prefix handed to an attention that wants 16-bit K / V, a
+ * sequence moved to another cache).
+ *
+ *   key, value    [T, Hkv, D], PA_F32 / PA_BF16 / PA_F16 (same type for both), D a multiple
+ *                 of 16; innermost stride 1; may not overlap the caches.  Row t is read from
+ *                 slot slot_mapping[t]; a negative entry, or one >= num_blocks * 16 (which
+ *                 sets PA_DEVERR_SLOT_RANGE), leaves row t as it was.
+ *   k_cache,      [num_blocks, Hkv, 16, D] of key's type (bit copies) or PA_FP8_E4M3, or
+ *   v_cache       [num_blocks, Hkv, 9 D] PA_FP4_E2M1.
+ *   opt           scales, scale_stride and device_error as pa_reshape_and_cache_opt; NULL =
+ *                 defaults.  A value is code * k_scale_h (E4M3) or code * sg * k_scale_h
+ *                 (E2M1), one fp32 product rounded to nearest, then converted to key's type
+ *                 (nearest even).
+ * Alignment as pa_reshape_and_cache.  T == 0 is a no-op.
+ */
+int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                    const pa_tensor *slot_mapping, const pa_write_options *opt, pa_stream_t stream);
 
 /*
  * pa_decode -- single-query paged decode attention (one query token per sequence).
@@ -458,8 +496,8 @@ int pa_bm_export(const pa_block_manager *m, const int *seqs, int n, int row_stri
 
 /* Copy whole cache blocks on the device: for each row (src, dst) of block_pairs
  * (PA_I64 [n, 2], contiguous, device), every (kv head, token) row of block src of
- * k_cache and v_cache ([num_blocks, Hkv, 16, D], any 16-byte-aligned strides, any cache
- * type) is copied to block dst.  Pairs naming a block outside [0, num_blocks) copy
+ * k_cache and v_cache ([num_blocks, Hkv, 16, D] or 4-bit pages, any 16-byte-aligned strides,
+ * any cache type) is copied to block dst.  Pairs naming a block outside [0, num_blocks) copy
  * nothing and set PA_DEVERR_BLOCK_RANGE.  Asynchronous on `stream`. */
 int pa_copy_blocks(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *block_pairs, int *device_error,
                    pa_stream_t stream);

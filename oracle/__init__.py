@@ -216,3 +216,72 @@ def cache_values(cache_flat: np.ndarray, cache_dtype: str, scale=1.0) -> np.ndar
         sc = np.asarray(scale, dtype=np.float32).astype(np.float64)
         return table[cache_flat] * sc.reshape((1, -1) + (1,) * (cache_flat.ndim - 2))
     raise ValueError(cache_dtype)
+
+
+# ------------------------------------------------------------------ 4-bit cache
+
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _nearest_even(mag: np.ndarray, values: np.ndarray) -> np.ndarray:
+    """Index of the nearest entry of the ascending `values`, ties to the even index, saturating
+    (both formats' codes count up with the value, so an even code is an even significand)."""
+    mid = (values[1:] + values[:-1]) / 2
+    lo = np.searchsorted(mid, mag, side="left")    # mid < mag: a tie stays below
+    hi = np.searchsorted(mid, mag, side="right")   # mid <= mag: a tie goes up
+    return np.where(lo % 2 == 0, lo, hi)
+
+
+def fp4_quantize(x: np.ndarray, scale) -> tuple:
+    """fp32 rows x [T, Hkv, D] -> (codes uint8 [T, Hkv, D], scales uint8 [T, Hkv, D/16]).
+
+    y = x / scale, sg = E4M3(max(max16 |y| / 6, 2^-9)), code = E2M1(y / sg), each quotient
+    rounded to fp32 (computed in fp64 and then rounded, which for a quotient of fp32 numbers
+    is the correctly rounded one).  scale: one value or Hkv."""
+    x = np.asarray(x, dtype=np.float32)
+    T, H, D = x.shape
+    s = np.broadcast_to(np.asarray(scale, dtype=np.float32).astype(np.float64).reshape(1, -1, 1), (1, H, 1))
+    with np.errstate(all="ignore"):
+        y = (x.astype(np.float64) / s).astype(np.float32).astype(np.float64)
+        g = np.abs(y).reshape(T, H, D // 16, 16)
+        bad = np.isnan(g).any(-1)
+        top = (g.max(-1) / 6).astype(np.float32).astype(np.float64)
+        e4m3 = e4m3_decode(np.arange(0x7F, dtype=np.uint8))
+        sg = _nearest_even(np.clip(np.where(bad, 1.0, top), 2.0 ** -9, 448.0), e4m3).astype(np.uint8)
+        q = (g / e4m3[sg][..., None]).astype(np.float32).astype(np.float64)
+        code = _nearest_even(np.where(bad[..., None], 0.0, q), E2M1_VALUES).astype(np.uint8)
+    neg = np.signbit(x) ^ (s < 0)
+    code = code.reshape(T, H, D) | (neg.astype(np.uint8) << 3)
+    code[np.repeat(bad, 16, -1)] = 0
+    sg[bad] = 0x7F
+    return code, sg
+
+
+def fp4_values(code: np.ndarray, sg: np.ndarray, scale=1.0) -> np.ndarray:
+    """fp64 values code * sg * scale of codes [..., Hkv, D], scales [..., Hkv, D/16]."""
+    e4m3 = e4m3_decode(np.arange(256, dtype=np.uint8))
+    v = np.where(code & 8, -1.0, 1.0) * E2M1_VALUES[code & 7] * np.repeat(e4m3[sg], 16, -1)
+    sc = np.asarray(scale, dtype=np.float32).astype(np.float64)
+    return v * (sc if sc.ndim == 0 else sc[:, None])
+
+
+def fp4_place(D: int) -> np.ndarray:
+    """int64 [16, D/2 + D/16]: the place in a page of each token's code bytes, then of its scales."""
+    out = np.zeros((16, D // 2 + D // 16), dtype=np.int64)
+    for t in range(16):
+        for b in range(D // 2):
+            lin = t * min(64, D // 2) + b % 64
+            out[t, b] = (b // 64) * 1024 + (lin ^ (((lin >> 7) & 3) << 5))
+        for j in range(D // 16):
+            out[t, D // 2 + j] = 8 * D + t * (D // 16) + j
+    return out
+
+
+def fp4_store(pages: np.ndarray, slots, code: np.ndarray, sg: np.ndarray) -> None:
+    """Place rows (codes [T, Hkv, D], scales) at `slots` of pages uint8 [NB, Hkv, 9 D]; slots < 0 skipped."""
+    D = code.shape[2]
+    place = fp4_place(D)
+    rows = np.concatenate([code[..., 0::2] | (code[..., 1::2] << 4), sg], -1)
+    for t, slot in enumerate(np.asarray(slots)):
+        if slot >= 0:
+            pages[slot // 16][:, place[slot % 16]] = rows[t]

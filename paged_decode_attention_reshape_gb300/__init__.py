@@ -7,7 +7,8 @@ there is no fallback: if the library is not built, importing works but the
 first call raises ``RuntimeError``.
 
 Element types: float32, bfloat16, float16; E4M3 caches as torch.uint8 (raw
-codes) or torch.float8_e4m3fn; block tables and sequence lengths int32;
+codes) or torch.float8_e4m3fn; 4-bit caches as torch.uint8 page bytes
+[NB, Hkv, 9 D] (see include/pa.h); block tables and sequence lengths int32;
 slot_mapping int64.
 """
 from __future__ import annotations
@@ -21,8 +22,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpa_gb300.so")
 
-PA_F32, PA_BF16, PA_F16, PA_FP8_E4M3, PA_I32, PA_I64 = range(6)
-PA_KV_AUTO, PA_KV_FP8_E4M3 = 0, 1
+PA_F32, PA_BF16, PA_F16, PA_FP8_E4M3, PA_I32, PA_I64, PA_FP4_E2M1 = range(7)
+PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_FP4_E2M1 = 0, 1, 2
 PA_KERNEL_WRITE, PA_KERNEL_DECODE = 0, 1
 PA_DEVERR_SLOT_RANGE, PA_DEVERR_BLOCK_RANGE, PA_DEVERR_SEQLEN_RANGE, PA_DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
 STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", -3: "PA_ERR_ALIGNMENT",
@@ -30,6 +31,7 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", 
           -8: "PA_ERR_DEVICE_TIMEOUT", -9: "PA_ERR_NO_BLOCKS"}
 
 EXPORTS = ("pa_reshape_and_cache", "pa_reshape_and_cache_opt", "pa_decode", "pa_decode_ex", "pa_decode_opt",
+           "pa_gather_cache",
            "pa_attention_varlen", "pa_decode_step", "pa_decode_noalloc", "pa_decode_plan", "pa_decode_workspace_size", "pa_check_device_error",
            "pa_status_string", "pa_profile_enable", "pa_profile_read", "pa_bm_create", "pa_bm_destroy",
            "pa_bm_num_free", "pa_bm_block_refs", "pa_bm_seq_len", "pa_bm_append", "pa_bm_fork", "pa_bm_free",
@@ -89,6 +91,8 @@ def lib() -> ctypes.CDLL:
             L.pa_reshape_and_cache.argtypes = [T, T, T, T, T, i32, P, P, P, P]
             L.pa_reshape_and_cache_opt.restype = i32
             L.pa_reshape_and_cache_opt.argtypes = [T, T, T, T, T, i32, ctypes.POINTER(PaWriteOptions), P]
+            L.pa_gather_cache.restype = i32
+            L.pa_gather_cache.argtypes = [T, T, T, T, T, ctypes.POINTER(PaWriteOptions), P]
             L.pa_decode_opt.restype = i32
             L.pa_decode_opt.argtypes = [T, T, T, T, T, T, f32, i32, ctypes.POINTER(PaDecodeOptions), P]
             L.pa_decode_step.restype = i32
@@ -160,6 +164,11 @@ def desc(t: torch.Tensor, dtype_code: int | None = None) -> PaTensor:
     return d
 
 
+def _cache(t: torch.Tensor) -> PaTensor:
+    """pa_tensor of a cache: a rank-3 uint8 tensor [NB, Hkv, 9 D] is a 4-bit cache's pages."""
+    return desc(t, PA_FP4_E2M1 if t.dim() == 3 and t.dtype is torch.uint8 else None)
+
+
 def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -178,8 +187,9 @@ def _check(rc: int, where: str):
 def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, kv_dtype: int = PA_KV_AUTO,
                          k_scale=None, v_scale=None, device_error=None, stream=None) -> None:
     """Scatter key/value [T, Hkv, D] rows into k_cache/v_cache [NB, Hkv, 16, D] at slot_mapping [T] (int64).
-    kv_dtype PA_KV_FP8_E4M3 quantises with the device fp32 scales k_scale/v_scale (1-element tensors)."""
-    args = (desc(key), desc(value), desc(k_cache), desc(v_cache), desc(slot_mapping))
+    kv_dtype PA_KV_FP8_E4M3 (PA_KV_FP4_E2M1: into 4-bit pages) quantises with the device fp32 scales
+    k_scale/v_scale (1-element tensors)."""
+    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
     rc = lib().pa_reshape_and_cache(*[ctypes.byref(a) for a in args], int(kv_dtype), _ptr(k_scale), _ptr(v_scale),
                                     _ptr(device_error), _stream(stream))
     _check(rc, "pa_reshape_and_cache")
@@ -192,10 +202,21 @@ def pa_reshape_and_cache_opt(key, value, k_cache, v_cache, slot_mapping, kv_dtyp
     (scale_stride 0: one scale for every head).  The cache may be a strided view (an NHD cache
     [NB, 16, Hkv, D] passed as .permute(0, 2, 1, 3))."""
     o = PaWriteOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(device_error))
-    args = (desc(key), desc(value), desc(k_cache), desc(v_cache), desc(slot_mapping))
+    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
     rc = lib().pa_reshape_and_cache_opt(*[ctypes.byref(a) for a in args], int(kv_dtype), ctypes.byref(o),
                                         _stream(stream))
     _check(rc, "pa_reshape_and_cache_opt")
+
+
+def pa_gather_cache(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_scale=None, scale_stride: int = 0,
+                    device_error=None, stream=None) -> None:
+    """Rows of the cache at slot_mapping [T] (int64) back as values into key/value [T, Hkv, D]: bit copies
+    from a cache of key's type, code * scale from an E4M3 or 4-bit cache (scales as
+    pa_reshape_and_cache_opt).  A negative slot leaves its row as it was."""
+    o = PaWriteOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(device_error))
+    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
+    rc = lib().pa_gather_cache(*[ctypes.byref(a) for a in args], ctypes.byref(o), _stream(stream))
+    _check(rc, "pa_gather_cache")
 
 
 def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num_kv_heads: int,
@@ -208,7 +229,7 @@ def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float,
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
                         _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    args = (desc(out), desc(q), desc(k_cache), desc(v_cache), desc(block_table), desc(seq_lens))
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
     rc = lib().pa_decode_opt(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), ctypes.byref(o),
                              _stream(stream))
     _check(rc, "pa_decode_opt")
@@ -227,7 +248,7 @@ def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_tab
     o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
                         _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
     nrs = None if new_rows_start is None else ctypes.byref(desc(new_rows_start))
-    args = (desc(out), desc(q), desc(key), desc(value), desc(k_cache), desc(v_cache), desc(slot_mapping))
+    args = (desc(out), desc(q), desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
     rc = lib().pa_decode_step(*[ctypes.byref(a) for a in args], nrs, ctypes.byref(desc(block_table)),
                               ctypes.byref(desc(seq_lens)), float(scale), int(num_kv_heads), ctypes.byref(o),
                               _stream(stream))
@@ -245,7 +266,7 @@ def pa_attention_varlen(out, q, k_cache, v_cache, query_start_loc, block_table, 
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
                         _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    args = (desc(out), desc(q), desc(k_cache), desc(v_cache), desc(query_start_loc), desc(block_table),
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(query_start_loc), desc(block_table),
             desc(seq_lens))
     rc = lib().pa_attention_varlen(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads),
                                    int(max_query_len), ctypes.byref(o), _stream(stream))
@@ -256,7 +277,7 @@ def pa_decode(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num
               stream=None) -> None:
     """Paged decode attention: out/q [S, Hq, D], caches [NB, Hkv, 16, D], block_table [S, maxNB] int32,
     seq_lens [S] int32."""
-    args = (desc(out), desc(q), desc(k_cache), desc(v_cache), desc(block_table), desc(seq_lens))
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
     rc = lib().pa_decode(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _stream(stream))
     _check(rc, "pa_decode")
 
@@ -266,7 +287,7 @@ def pa_decode_ex(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, 
                  stream=None) -> None:
     """pa_decode with FP8 scales, explicit partition size (0 heuristic, -1 unsplit), caller workspace
     (a zero-filled uint8 CUDA tensor, see pa_decode_workspace_size) and device error word (int32)."""
-    args = (desc(out), desc(q), desc(k_cache), desc(v_cache), desc(block_table), desc(seq_lens))
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().pa_decode_ex(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _ptr(k_scale),
                             _ptr(v_scale), int(partition_size), _ptr(workspace), ws_bytes, _ptr(device_error),
@@ -280,7 +301,7 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_table, seq_lens, scale: fl
     where they run decode.  Split-KV scratch comes from a fixed 32 MiB buffer inside the library,
     shared by all calls on a device (calls that overlap on the GPU race on it); a problem needing
     more than that raises PAError(PA_ERR_WORKSPACE)."""
-    args = (desc(out), desc(q), desc(k_cache), desc(v_cache), desc(block_table), desc(seq_lens))
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
     rc = lib().pa_decode_noalloc(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _ptr(k_scale),
                                  _ptr(v_scale), int(partition_size), _ptr(device_error), _stream(stream))
     _check(rc, "pa_decode_noalloc")
@@ -389,6 +410,6 @@ class BlockManager:
 def pa_copy_blocks(k_cache, v_cache, block_pairs, device_error=None, stream=None) -> None:
     """Copy whole cache blocks: for each row (src, dst) of block_pairs (int64 [n, 2] on the
     device), block src of k_cache / v_cache is copied to block dst."""
-    args = (desc(k_cache), desc(v_cache), desc(block_pairs))
+    args = (_cache(k_cache), _cache(v_cache), desc(block_pairs))
     rc = lib().pa_copy_blocks(*[ctypes.byref(a) for a in args], _ptr(device_error), _stream(stream))
     _check(rc, "pa_copy_blocks")

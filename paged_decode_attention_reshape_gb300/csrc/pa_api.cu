@@ -10,45 +10,12 @@
 #include <vector>
 
 #include "pa_internal.h"
+#include "pa_validate.h"
 
 #define PA_API extern "C" __attribute__((visibility("default")))
 
 namespace pa {
 namespace {
-
-// ------------------------------------------------------------------ helpers
-
-int elem_bytes(int dt) {
-  switch (dt) {
-    case PA_F32: case PA_I32: return 4;
-    case PA_BF16: case PA_F16: return 2;
-    case PA_FP8_E4M3: return 1;
-    case PA_I64: return 8;
-    default: return 0;
-  }
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Descriptor sanity: non-null, rank, element type, positive extents.
-int check_desc(const pa_tensor *t, int ndim) {
-  if (!t || t->ndim != ndim) return PA_ERR_INVALID_ARG;
-  for (int i = 0; i < ndim; ++i)
-    if (t->shape[i] < 0 || t->stride[i] < 0) return PA_ERR_INVALID_ARG;
-  if (elem_bytes(t->dtype) == 0) return PA_ERR_UNSUPPORTED_DTYPE;
-  return PA_OK;
-}
-
-int device_sm_count() {
-  static int cache[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) cache[dev] = n;
-  return n;
-}
 
 // --------------------------------------------------------------- profiling
 
@@ -343,28 +310,6 @@ int internal_workspace(size_t counters, size_t data, cudaStream_t st, DevWorkspa
   return PA_OK;
 }
 
-// ------------------------------------------------------------- validation
-
-int validate_cache_pair(const pa_tensor *kc, const pa_tensor *vc, int *NB, int *Hkv, int *D) {
-  int r;
-  if ((r = check_desc(kc, 4)) || (r = check_desc(vc, 4))) return r;
-  for (int i = 0; i < 4; ++i)
-    if (kc->shape[i] != vc->shape[i]) return PA_ERR_INVALID_ARG;
-  if (kc->dtype != vc->dtype) return PA_ERR_INVALID_ARG;
-  if (kc->shape[2] != kBlock) return PA_ERR_UNSUPPORTED_SHAPE;
-  if (kc->stride[3] != 1 || vc->stride[3] != 1) return PA_ERR_INVALID_ARG;
-  if (!kc->data || !vc->data) return PA_ERR_INVALID_ARG;
-  const int eb = elem_bytes(kc->dtype);
-  if (!aligned16(kc->data) || !aligned16(vc->data)) return PA_ERR_ALIGNMENT;
-  for (int i = 0; i < 3; ++i)
-    if ((kc->stride[i] * eb) % 16 || (vc->stride[i] * eb) % 16) return PA_ERR_ALIGNMENT;
-  if (kc->shape[0] > INT32_MAX || kc->shape[1] > 65535) return PA_ERR_UNSUPPORTED_SHAPE;
-  *NB = static_cast<int>(kc->shape[0]);
-  *Hkv = static_cast<int>(kc->shape[1]);
-  *D = static_cast<int>(kc->shape[3]);
-  return PA_OK;
-}
-
 }  // namespace
 }  // namespace pa
 
@@ -407,6 +352,8 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
     if (k_cache->dtype != in_dt) return PA_ERR_UNSUPPORTED_DTYPE;
   } else if (kv_dtype == PA_KV_FP8_E4M3) {
     if (k_cache->dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED_DTYPE;
+  } else if (kv_dtype == PA_KV_FP4_E2M1) {
+    if (k_cache->dtype != PA_FP4_E2M1) return PA_ERR_UNSUPPORTED_DTYPE;
   } else {
     return PA_ERR_INVALID_ARG;
   }
@@ -422,6 +369,34 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
   if (!aligned16(key->data) || !aligned16(value->data)) return PA_ERR_ALIGNMENT;
   for (int i = 0; i < 2; ++i)
     if ((key->stride[i] * ib) % 16 || (value->stride[i] * ib) % 16) return PA_ERR_ALIGNMENT;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (kv_dtype == PA_KV_FP4_E2M1) {
+    Fp4WriteParams f{};
+    f.key = key->data;
+    f.value = value->data;
+    f.k_cache = static_cast<char *>(k_cache->data);
+    f.v_cache = static_cast<char *>(v_cache->data);
+    f.slot_mapping = static_cast<const int64_t *>(slot_mapping->data);
+    f.T = T;
+    f.Hkv = Hkv;
+    f.D = D;
+    f.key_ts = key->stride[0];
+    f.key_hs = key->stride[1];
+    f.val_ts = value->stride[0];
+    f.val_hs = value->stride[1];
+    f.kc_s0 = k_cache->stride[0];
+    f.kc_s1 = k_cache->stride[1];
+    f.vc_s0 = v_cache->stride[0];
+    f.vc_s1 = v_cache->stride[1];
+    f.num_slots = static_cast<int64_t>(NB) * kBlock;
+    f.k_scale = o.k_scale;
+    f.v_scale = o.v_scale;
+    f.scale_stride = o.scale_stride;
+    f.err = o.device_error;
+    ProfScope ps(PA_KERNEL_WRITE, st);
+    return launch_write_fp4(f, in_dt, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
 
   WriteParams p;
   p.key = key->data;
@@ -460,7 +435,6 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
   }
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   {
     ProfScope ps(PA_KERNEL_WRITE, st);
@@ -483,6 +457,59 @@ PA_API int pa_reshape_and_cache(const pa_tensor *key, const pa_tensor *value, pa
   o.v_scale = v_scale;
   o.device_error = device_error;
   return pa_reshape_and_cache_opt(key, value, k_cache, v_cache, slot_mapping, kv_dtype, &o, stream);
+}
+
+PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                           const pa_tensor *slot_mapping, const pa_write_options *opt, pa_stream_t stream) {
+  const pa_write_options o = opt ? *opt : pa_write_options{};
+  if (o.scale_stride < 0) return PA_ERR_INVALID_ARG;
+  int r;
+  if ((r = check_desc(key, 3)) || (r = check_desc(value, 3)) || (r = check_desc(slot_mapping, 1))) return r;
+  int NB, Hkv, D;
+  if ((r = validate_cache_pair(k_cache, v_cache, &NB, &Hkv, &D))) return r;
+  const int out_dt = key->dtype, cache_dt = k_cache->dtype;
+  if (value->dtype != out_dt) return PA_ERR_INVALID_ARG;
+  if (out_dt != PA_F32 && out_dt != PA_BF16 && out_dt != PA_F16) return PA_ERR_UNSUPPORTED_DTYPE;
+  const bool quantised = cache_dt == PA_FP8_E4M3 || cache_dt == PA_FP4_E2M1;
+  if (!quantised && cache_dt != out_dt) return PA_ERR_UNSUPPORTED_DTYPE;
+  if (slot_mapping->dtype != PA_I64) return PA_ERR_UNSUPPORTED_DTYPE;
+  const int64_t T = key->shape[0];
+  if (value->shape[0] != T || slot_mapping->shape[0] != T) return PA_ERR_INVALID_ARG;
+  if (key->shape[1] != Hkv || key->shape[2] != D || value->shape[1] != Hkv || value->shape[2] != D)
+    return PA_ERR_INVALID_ARG;
+  if (key->stride[2] != 1 || value->stride[2] != 1 || slot_mapping->stride[0] != 1) return PA_ERR_INVALID_ARG;
+  if (D <= 0 || D % 16) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || Hkv == 0) return PA_OK;
+  if (!key->data || !value->data || !slot_mapping->data) return PA_ERR_INVALID_ARG;
+  const int ob = elem_bytes(out_dt), cb = elem_bytes(cache_dt);
+  if (!aligned16(key->data) || !aligned16(value->data)) return PA_ERR_ALIGNMENT;
+  for (int i = 0; i < 2; ++i)
+    if ((key->stride[i] * ob) % 16 || (value->stride[i] * ob) % 16) return PA_ERR_ALIGNMENT;
+  GatherParams p{};
+  p.key = static_cast<char *>(key->data);
+  p.value = static_cast<char *>(value->data);
+  p.k_cache = static_cast<const char *>(k_cache->data);
+  p.v_cache = static_cast<const char *>(v_cache->data);
+  p.slot_mapping = static_cast<const int64_t *>(slot_mapping->data);
+  p.T = T;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.key_ts = key->stride[0];
+  p.key_hs = key->stride[1];
+  p.val_ts = value->stride[0];
+  p.val_hs = value->stride[1];
+  p.kc_s0 = k_cache->stride[0] * cb;
+  p.kc_s1 = k_cache->stride[1] * cb;
+  p.kc_s2 = cache_dt == PA_FP4_E2M1 ? 0 : k_cache->stride[2] * cb;
+  p.vc_s0 = v_cache->stride[0] * cb;
+  p.vc_s1 = v_cache->stride[1] * cb;
+  p.vc_s2 = cache_dt == PA_FP4_E2M1 ? 0 : v_cache->stride[2] * cb;
+  p.num_slots = static_cast<int64_t>(NB) * kBlock;
+  p.k_scale = quantised ? o.k_scale : nullptr;
+  p.v_scale = quantised ? o.v_scale : nullptr;
+  p.scale_stride = o.scale_stride;
+  p.err = o.device_error;
+  return launch_gather(p, cache_dt, out_dt, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API int pa_decode_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_blocks_per_seq,

@@ -155,10 +155,10 @@ namespace pa {
 namespace {
 
 // One CTA per (pair, cache): copies every (kv head, token) row of block src to block dst,
-// 16 bytes per thread and step.
+// 16 bytes per thread and step (a 4-bit cache: one row, the whole page, per kv head).
 __global__ void __launch_bounds__(256) copy_blocks_kernel(char *kc, char *vc, int64_t kc_s0, int64_t kc_s1,
                                                           int64_t kc_s2, int64_t vc_s0, int64_t vc_s1, int64_t vc_s2,
-                                                          int Hkv, int row_bytes, const int64_t *pairs, int n,
+                                                          int Hkv, int rows, int row_bytes, const int64_t *pairs, int n,
                                                           int num_blocks, int *err) {
   const int i = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
@@ -170,9 +170,9 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(char *kc, char *vc, in
   }
   char *base = is_v ? vc : kc;
   const int64_t s0 = is_v ? vc_s0 : kc_s0, s1 = is_v ? vc_s1 : kc_s1, s2 = is_v ? vc_s2 : kc_s2;  // bytes
-  const int packs = row_bytes / 16, per_block = Hkv * kBlock * packs;
+  const int packs = row_bytes / 16, per_block = Hkv * rows * packs;
   for (int j = threadIdx.x; j < per_block; j += blockDim.x) {
-    const int pk = j % packs, r = j / packs, t = r % kBlock, h = r / kBlock;
+    const int pk = j % packs, r = j / packs, t = r % rows, h = r / rows;
     const int64_t off = h * s1 + t * s2 + static_cast<int64_t>(pk) * 16;
     *reinterpret_cast<uint4 *>(base + dst * s0 + off) = *reinterpret_cast<const uint4 *>(base + src * s0 + off);
   }
@@ -184,28 +184,30 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(char *kc, char *vc, in
 PA_API int pa_copy_blocks(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *block_pairs, int *device_error,
                           pa_stream_t stream) {
   using namespace pa;
-  if (!k_cache || !v_cache || !block_pairs || k_cache->ndim != 4 || v_cache->ndim != 4 || block_pairs->ndim != 2)
-    return PA_ERR_INVALID_ARG;
-  for (int i = 0; i < 4; ++i)
+  if (!k_cache || !v_cache || !block_pairs || block_pairs->ndim != 2) return PA_ERR_INVALID_ARG;
+  const bool fp4 = k_cache->dtype == PA_FP4_E2M1;
+  const int rank = fp4 ? 3 : 4;
+  if (k_cache->ndim != rank || v_cache->ndim != rank) return PA_ERR_INVALID_ARG;
+  for (int i = 0; i < rank; ++i)
     if (k_cache->shape[i] != v_cache->shape[i]) return PA_ERR_INVALID_ARG;
-  if (k_cache->dtype != v_cache->dtype || k_cache->shape[2] != kBlock) return PA_ERR_INVALID_ARG;
+  if (k_cache->dtype != v_cache->dtype || (!fp4 && k_cache->shape[2] != kBlock)) return PA_ERR_INVALID_ARG;
   if (block_pairs->dtype != PA_I64 || block_pairs->shape[1] != 2 || block_pairs->stride[1] != 1 ||
       block_pairs->stride[0] != 2)
     return PA_ERR_INVALID_ARG;
   const int64_t n = block_pairs->shape[0];
   if (n == 0) return PA_OK;
   if (n > (1 << 30) || !k_cache->data || !v_cache->data || !block_pairs->data) return PA_ERR_INVALID_ARG;
-  const int eb = k_cache->dtype == PA_F32 ? 4 : (k_cache->dtype == PA_FP8_E4M3 ? 1 : 2);
-  const int row_bytes = static_cast<int>(k_cache->shape[3]) * eb;
-  if (k_cache->stride[3] != 1 || v_cache->stride[3] != 1 || row_bytes % 16) return PA_ERR_INVALID_ARG;
+  const int eb = k_cache->dtype == PA_F32 ? 4 : (k_cache->dtype == PA_FP8_E4M3 || fp4 ? 1 : 2);
+  const int row_bytes = static_cast<int>(k_cache->shape[rank - 1]) * eb;
+  if (k_cache->stride[rank - 1] != 1 || v_cache->stride[rank - 1] != 1 || row_bytes % 16) return PA_ERR_INVALID_ARG;
   const uintptr_t kb = reinterpret_cast<uintptr_t>(k_cache->data), vb = reinterpret_cast<uintptr_t>(v_cache->data);
   if (kb % 16 || vb % 16) return PA_ERR_ALIGNMENT;
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < rank - 1; ++i)
     if ((k_cache->stride[i] * eb) % 16 || (v_cache->stride[i] * eb) % 16) return PA_ERR_ALIGNMENT;
   copy_blocks_kernel<<<static_cast<unsigned>(2 * n), 256, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<char *>(k_cache->data), static_cast<char *>(v_cache->data), k_cache->stride[0] * eb,
-      k_cache->stride[1] * eb, k_cache->stride[2] * eb, v_cache->stride[0] * eb, v_cache->stride[1] * eb,
-      v_cache->stride[2] * eb, static_cast<int>(k_cache->shape[1]), row_bytes,
+      k_cache->stride[1] * eb, fp4 ? 0 : k_cache->stride[2] * eb, v_cache->stride[0] * eb, v_cache->stride[1] * eb,
+      fp4 ? 0 : v_cache->stride[2] * eb, static_cast<int>(k_cache->shape[1]), fp4 ? 1 : kBlock, row_bytes,
       static_cast<const int64_t *>(block_pairs->data), static_cast<int>(n), static_cast<int>(k_cache->shape[0]),
       device_error);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

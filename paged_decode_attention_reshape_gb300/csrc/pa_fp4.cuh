@@ -1,0 +1,60 @@
+// pa_fp4.cuh -- the 4-bit (E2M1) cache page: where its bytes are, and how codes become f16.
+//
+// One page, of one (block, kv head), is 9 D contiguous bytes: 8 D bytes of E2M1 codes (16
+// tokens x D / 2 bytes; byte b of a token holds elements 2b, low half, and 2b + 1), then D
+// bytes of E4M3 scales (16 tokens x D / 16; scale j belongs to elements 16 j .. 16 j + 15).
+// One contiguous run per page means one bulk copy per page and tensor, and a page size that
+// is a multiple of 64 bytes for every head size.
+//
+// Code bytes lie in sections of 16 x min(64, D / 2) bytes (head size 256: two, elements
+// 0..127 and 128..255), token by token, with bits 5 and 6 of the offset XORed by bits 7 and
+// 8.  Both readers of a page in shared memory are then free of bank conflicts: the score
+// fragments (lane (r, c) reads a run of token r, 16 bytes at D >= 128, 8 at D = 64) and the
+// P.V fragments (lane (r, c) reads run r, 8 or 4 bytes, of token 2c + {0, 1, 8, 9}), which
+// without the XOR would meet in one quarter of the banks (4-way).
+#pragma once
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+__host__ __device__ constexpr int fp4_page_bytes(int D) { return 9 * D; }
+
+// Offset in its page of code byte `b` of token `t`.
+__host__ __device__ __forceinline__ int fp4_code_off(int D, int t, int b) {
+  const int row = D >= 128 ? 64 : D / 2;
+  const int lin = t * row + (b & 63);
+  return (b >> 6) * 1024 + (lin ^ (((lin >> 7) & 3) << 5));
+}
+// Offset in its page of the scale of elements 16 j .. 16 j + 15 of token `t`.
+__host__ __device__ __forceinline__ int fp4_scale_off(int D, int t, int j) { return 8 * D + t * (D / 16) + j; }
+
+// Four code bytes (byte 0 first) -> four f16x2, each with its byte's low code in the low
+// half.  Exact: every E2M1 value is an f16.
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t eight_codes, uint32_t &a, uint32_t &b, uint32_t &c,
+                                                  uint32_t &d) {
+  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\t"
+      "mov.b32 {x0, x1, x2, x3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, x0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, x1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, x2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, x3;\n\t}"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(eight_codes));
+}
+
+// Two E4M3 codes (low byte first) -> f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(two_codes));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+}  // namespace pa

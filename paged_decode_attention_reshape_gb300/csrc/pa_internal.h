@@ -39,6 +39,37 @@ struct WriteParams {
                                                     // within a block below 2^31 bytes
 };
 
+// The 4-bit cache write (pa_fp4.cu): source strides in elements, cache strides in bytes.
+struct Fp4WriteParams {
+  const void *key, *value;
+  char *k_cache, *v_cache;
+  const int64_t *slot_mapping;
+  int64_t T;
+  int Hkv, D;
+  int64_t key_ts, key_hs, val_ts, val_hs;
+  int64_t kc_s0, kc_s1, vc_s0, vc_s1;
+  int64_t num_slots;
+  const float *k_scale, *v_scale;  // nullable (1.0)
+  int64_t scale_stride;
+  int *err;
+};
+
+// The read back of cache rows (pa_fp4.cu): output strides in elements, cache strides in bytes
+// (s2, the token stride, is not used by the 4-bit cache).
+struct GatherParams {
+  char *key, *value;
+  const char *k_cache, *v_cache;
+  const int64_t *slot_mapping;
+  int64_t T;
+  int Hkv, D;
+  int64_t key_ts, key_hs, val_ts, val_hs;
+  int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
+  int64_t num_slots;
+  const float *k_scale, *v_scale;  // nullable (1.0)
+  int64_t scale_stride;
+  int *err;
+};
+
 struct DecodeParams {
   void *out;
   const void *q;
@@ -121,6 +152,9 @@ int decode_ex_requirements(pa_tensor *out, const pa_tensor *q, const pa_tensor *
 // ctas_per_sm: the grid's CTAs per SM (1 .. 4; 0 = the standalone write's choice).
 cudaError_t launch_write(const WriteParams &p, int in_dtype, int cache_dtype, int sm_count, int ctas_per_sm,
                          cudaStream_t st);
+
+cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st);
+cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, cudaStream_t st);
 
 // Tensor-core kernel shape per (kind, head size): warps per CTA and pipeline
 // stages per warp.  Shared memory = W * STAGES * 2 pages (+ alignment, barriers).

@@ -1,0 +1,111 @@
+"""The oracle's 4-bit codec on the host, and the refusals of the calls that take 4-bit caches (no
+kernel is launched here)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+from test_abi import _decode, _t, _write
+
+import paged_decode_attention_reshape_gb300 as pa
+
+
+@pytest.fixture(scope="module")
+def L():
+    from paged_decode_attention_reshape_gb300 import _build
+    _build.build()
+    return pa.lib()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_page_places_cover_the_page_once(D):
+    assert np.array_equal(np.sort(oracle.fp4_place(D).ravel()), np.arange(9 * D))
+
+
+def test_codes_are_the_nearest_values():
+    rng = np.random.RandomState(1)
+    x = (rng.randn(40, 2, 64) * np.exp(rng.randn(40, 2, 1) * 3)).astype(np.float32)
+    code, sg = oracle.fp4_quantize(x, 1.0)
+    v = oracle.fp4_values(code, sg)
+    s = np.repeat(oracle.e4m3_decode(sg), 16, -1)
+    cand = np.concatenate([-oracle.E2M1_VALUES[::-1], oracle.E2M1_VALUES]) * s[..., None]
+    best = np.abs(cand - x[..., None].astype(np.float64)).min(-1)
+    assert (np.abs(v - x) <= best * (1 + 1e-6)).all()
+    # the group's largest element is within one sixth of a step of the scale's rounding of 6 sg
+    top = np.abs(x).reshape(40, 2, 4, 16).max(-1)
+    e = oracle.e4m3_decode(sg)
+    ok = (np.abs(e - top / 6) <= np.maximum(e / 16, 2.0 ** -10)) | (top / 6 < 2.0 ** -9) | (top / 6 > 448)
+    assert ok.all()
+
+
+def test_special_groups():
+    x = np.zeros((1, 1, 64), dtype=np.float32)
+    x[0, 0, 3] = np.nan
+    x[0, 0, 16] = np.inf
+    x[0, 0, 33] = -1e-6
+    code, sg = oracle.fp4_quantize(x, 1.0)
+    assert sg[0, 0].tolist() == [0x7F, 0x7E, 0x01, 0x01]
+    assert not code[0, 0, :16].any() and code[0, 0, 16] == 7 and code[0, 0, 33] == 8 and not code[0, 0, 48:].any()
+
+
+def test_write_refusals(L):
+    T, H, D, NB = 4, 2, 64, 8
+    key, sm = _t([T, H, D], pa.PA_BF16), _t([T], pa.PA_I64)
+    page = _t([NB, H, 9 * D], pa.PA_FP4_E2M1)
+    kv = pa.PA_KV_FP4_E2M1
+    empty = _t([0, H, D], pa.PA_BF16)
+    assert _write(L, empty, empty, page, page, _t([0], pa.PA_I64), kv) == 0
+    assert _write(L, key, key, page, page, sm, pa.PA_KV_AUTO) == -2                    # mode and cache differ
+    assert _write(L, key, key, page, page, sm, pa.PA_KV_FP8_E4M3) == -2
+    assert _write(L, key, key, _t([NB, H, 16, D], pa.PA_BF16), _t([NB, H, 16, D], pa.PA_BF16), sm, kv) == -2
+    assert _write(L, key, key, _t([NB, H, 16, D], pa.PA_FP4_E2M1), page, sm, kv) == -1  # pages have rank 3
+    assert _write(L, key, key, _t([NB, H, 9 * 96], pa.PA_FP4_E2M1), _t([NB, H, 9 * 96], pa.PA_FP4_E2M1), sm, kv) == -7
+    assert _write(L, key, key, _t([NB, H, 9 * 128], pa.PA_FP4_E2M1), _t([NB, H, 9 * 128], pa.PA_FP4_E2M1), sm, kv) == -1
+    assert _write(L, key, key, page, _t([NB, H + 1, 9 * D], pa.PA_FP4_E2M1), sm, kv) == -1
+    assert _write(L, key, key, _t([NB, H, 9 * D], pa.PA_FP4_E2M1, ptr=0x10008), page, sm, kv) == -3
+    assert _write(L, key, key, _t([NB, H, 9 * D], pa.PA_FP4_E2M1, strides=[H * 9 * D + 8, 9 * D, 1]), page, sm, kv) == -3
+    assert _write(L, key, key, _t([NB, H, 9 * D], pa.PA_FP4_E2M1, strides=[H * 18 * D, 18 * D, 2]), page, sm, kv) == -1
+    assert _write(L, _t([T, H, D], pa.PA_FP4_E2M1), _t([T, H, D], pa.PA_FP4_E2M1), page, page, sm, kv) == -2
+    f8 = _t([T, H, D], pa.PA_FP8_E4M3)
+    assert _write(L, f8, f8, page, page, sm, kv) == -2
+
+
+def _gather(L, key, val, kc, vc, sm, opt=None):
+    return L.pa_gather_cache(ctypes.byref(key), ctypes.byref(val), ctypes.byref(kc), ctypes.byref(vc),
+                             ctypes.byref(sm), opt, None)
+
+
+def test_gather_refusals(L):
+    T, H, D, NB = 4, 2, 64, 8
+    key, sm = _t([T, H, D], pa.PA_BF16), _t([T], pa.PA_I64)
+    page = _t([NB, H, 9 * D], pa.PA_FP4_E2M1)
+    bf = _t([NB, H, 16, D], pa.PA_BF16)
+    empty = _t([0, H, D], pa.PA_BF16)
+    assert _gather(L, empty, empty, page, page, _t([0], pa.PA_I64)) == 0
+    assert _gather(L, key, _t([T, H, D], pa.PA_F16), page, page, sm) == -1
+    assert _gather(L, _t([T, H, D], pa.PA_FP8_E4M3), _t([T, H, D], pa.PA_FP8_E4M3), page, page, sm) == -2
+    assert _gather(L, _t([T, H, D], pa.PA_F16), _t([T, H, D], pa.PA_F16), bf, bf, sm) == -2   # no conversion
+    assert _gather(L, key, key, page, page, _t([T], pa.PA_I32)) == -2
+    assert _gather(L, key, key, page, page, _t([T + 1], pa.PA_I64)) == -1
+    assert _gather(L, _t([T, H + 1, D], pa.PA_BF16), _t([T, H + 1, D], pa.PA_BF16), page, page, sm) == -1
+    assert _gather(L, _t([T, H, D], pa.PA_BF16, ptr=0x10004), key, page, page, sm) == -3
+    assert _gather(L, _t([T, H, D], pa.PA_BF16, strides=[H * D + 4, D, 1]), key, page, page, sm) == -3
+    assert _gather(L, _t([T, H, D], pa.PA_BF16, ptr=0), key, page, page, sm) == -1
+    b24 = _t([NB, H, 16, 24], pa.PA_BF16)
+    assert _gather(L, _t([T, H, 24], pa.PA_BF16), _t([T, H, 24], pa.PA_BF16), b24, b24, sm) == -7
+    o = pa.PaWriteOptions()
+    o.scale_stride = -1
+    assert _gather(L, key, key, page, page, sm, ctypes.byref(o)) == -1
+
+
+def test_copy_blocks_refusals(L):
+    NB, H, D = 4, 2, 64
+    pairs = _t([1, 2], pa.PA_I64)
+
+    def copy(k, v):
+        return L.pa_copy_blocks(ctypes.byref(k), ctypes.byref(v), ctypes.byref(pairs), None, None)
+    page = _t([NB, H, 9 * D], pa.PA_FP4_E2M1)
+    assert copy(_t([NB, H, 16, D], pa.PA_FP4_E2M1), _t([NB, H, 16, D], pa.PA_FP4_E2M1)) == -1
+    assert copy(page, _t([NB, H, 16, D], pa.PA_BF16)) == -1
+    assert copy(page, _t([NB, H, 9 * D], pa.PA_FP4_E2M1, ptr=0x10008)) == -3
