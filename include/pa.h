@@ -212,7 +212,8 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  *   out           [S, Hq, D], same element type as q (may be the same memory as q).
  *   q             [S, Hq, D], PA_F32 / PA_BF16 / PA_F16, innermost stride 1.
  *   k_cache,      [num_blocks, Hkv, 16, D]; element type == q's, or PA_FP8_E4M3
- *   v_cache       with a PA_BF16 / PA_F16 query.
+ *   v_cache       with a PA_BF16 / PA_F16 query; or [num_blocks, Hkv, 9 D] 4-bit pages
+ *                 (PA_FP4_E2M1) with a PA_BF16 / PA_F16 query.
  *   block_table   PA_I32 [S, max_blocks_per_seq], innermost stride 1.  Only the
  *                 first ceil(seq_lens[s] / 16) entries of row s are used; the
  *                 rest may hold any value (padding).
@@ -220,7 +221,7 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  *                 token written in this step.  0 gives an all-zero output row.
  *   scale         softmax scale (usually 1 / sqrt(D)).
  *   num_kv_heads  Hkv; must equal k_cache->shape[1] and divide Hq.
- * Head sizes built: 64, 128, 256 (FP8 caches: 128, 256).
+ * Head sizes built: 64, 128, 256 (E4M3 caches: 128, 256).
  * Uses a library-held workspace on the current device (grown on demand with
  * cudaMallocAsync and zero-filled on `stream`); calls that use it on different
  * streams must not overlap.  A stream capture cannot grow it (PA_ERR_WORKSPACE): run a call
@@ -241,8 +242,9 @@ int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, cons
  * softmax identity).  The pages' fixed 512-token partition and 8192-token V1/V2 switch are
  * replaced by a plan measured on GB300 (pa_decode_plan).
  *
- *   k_scale, v_scale  device fp32 per-tensor dequantisation scales for an FP8 cache
- *                     (K and V element values are code_value * scale); NULL = 1.0.
+ *   k_scale, v_scale  device fp32 per-tensor dequantisation scales for an FP8 or 4-bit
+ *                     cache (K and V element values are code_value * scale, 4-bit ones
+ *                     also times their group's scale); NULL = 1.0.
  *   partition_size    how the KV range of a sequence is split: 0 = chosen by the
  *                     library's measured heuristic (pa_decode_plan); -1 = never split;
  *                     > 0 = partitions of that many tokens (rounded up to a multiple of
@@ -288,7 +290,7 @@ int pa_decode_ex(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, c
  * h for key token t is scale * q.k_t + alibi_slopes[h] * (t - (seq_len - 1)).
  */
 typedef struct {
-    const float *k_scale;        /* as pa_write_options: FP8 dequantisation scales, */
+    const float *k_scale;        /* as pa_write_options: FP8 / 4-bit dequantisation scales, */
     const float *v_scale;        /* NULL = 1.0; element value = code value * scale_h */
     int64_t scale_stride;        /* 0: one scale; > 0: KV head h uses [h * scale_stride] */
     const float *alibi_slopes;   /* device fp32 [Hq], contiguous, or NULL (no bias) */
@@ -336,7 +338,7 @@ int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, 
  * query columns as Hq * max_query_len heads: pa_decode_plan / pa_decode_workspace_size
  * with num_heads = Hq * max_query_len give them.  PA_PARTITION_BALANCED is refused
  * (PA_ERR_UNSUPPORTED_SHAPE).  Kernels: with fewer than 64 query columns per KV head
- * (max_query_len * Hq / Hkv; 32 at head size 64), an fp8 or fp32 cache, D other than 64 / 128, or a split
+ * (max_query_len * Hq / Hkv; 32 at head size 64), an fp8, 4-bit or fp32 cache, D other than 64 / 128, or a split
  * asked for (partition_size > 0 or a cluster split), the decode kernels run with 8
  * columns per CTA, each CTA reading the pages its columns see.  Otherwise (bf16 / f16
  * cache, partition_size 0 or -1) a query-tile kernel runs on the tcgen05 tensor cores:
@@ -364,9 +366,9 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  *
  *   out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, opt: as
  *                    pa_decode_opt (one query token per sequence; opt's scales and
- *                    scale_stride also quantise the rows written to an FP8 cache).
+ *                    scale_stride also quantise the rows written to an FP8 or 4-bit cache).
  *   key, value       [T, Hkv, D] new rows, slot_mapping int64 [T]: as pa_reshape_and_cache
- *                    (kv dtype: E4M3 when the cache is E4M3, else the cache keeps q's dtype).
+ *                    (kv dtype: E4M3 or E2M1 when the cache is, else the cache keeps q's dtype).
  *   new_rows_start   NULL: T == S and row s is sequence s's newest token.  Else int32 [S + 1]
  *                    (device): rows new_rows_start[s] .. new_rows_start[s+1]-1 are sequence
  *                    s's newest n_s tokens, row i at position seq_lens[s] - n_s + i.

@@ -137,6 +137,11 @@ int kind_of(int q_dtype, int cache_dtype) {
     if (q_dtype == PA_F16) return KIND_FP8_F16Q;
     return -1;
   }
+  if (cache_dtype == PA_FP4_E2M1) {
+    if (q_dtype == PA_BF16) return KIND_FP4_BF16Q;
+    if (q_dtype == PA_F16) return KIND_FP4_F16Q;
+    return -1;
+  }
   if (q_dtype != cache_dtype) return -1;
   if (q_dtype == PA_BF16) return KIND_BF16;
   if (q_dtype == PA_F16) return KIND_F16;
@@ -154,11 +159,13 @@ bool longest_first(int kind, int S) { return kind != KIND_F32 && S <= 128; }
 int ctas_per_sm(int kind, int D, bool device) {
   if (kind == KIND_F32) return 4;
   if (device) {
-    static std::atomic<int> cache[5][3];
+    static std::atomic<int> cache[7][3];
     const int di = D == 64 ? 0 : D == 128 ? 1 : 2;
     int n = cache[kind][di].load(std::memory_order_relaxed);
     if (n == 0) {
-      n = (kind == KIND_BF16 || kind == KIND_F16) ? occupancy_decode_mma_16(kind, D) : occupancy_decode_mma_fp8(kind, D);
+      n = (kind == KIND_BF16 || kind == KIND_F16) ? occupancy_decode_mma_16(kind, D)
+          : mma_fp4(kind)                         ? occupancy_decode_mma_fp4(kind, D)
+                                                  : occupancy_decode_mma_fp8(kind, D);
       if (n > 0) cache[kind][di].store(n, std::memory_order_relaxed);
     }
     if (n > 0) return n;
@@ -521,6 +528,7 @@ PA_API int pa_decode_plan(int num_seqs, int num_heads, int num_kv_heads, int hea
   int kind;
   switch (kv_dtype_code) {
     case PA_FP8_E4M3: kind = KIND_FP8_BF16Q; break;
+    case PA_FP4_E2M1: kind = KIND_FP4_BF16Q; break;
     case PA_BF16: kind = KIND_BF16; break;
     case PA_F16: kind = KIND_F16; break;
     case PA_F32: kind = KIND_F32; break;
@@ -547,12 +555,13 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
       max_blocks_per_seq < 0)
     return 0;
   if (partition_size == PA_PARTITION_BALANCED) {
-    // enough for any cache type on the current device: the E4M3 kernel's shared-memory
-    // bound admits the most CTAs per SM
+    // enough for any cache type on the current device: the shared-memory bounds of the
+    // quantised kernels admit the most CTAs per SM
     const int sm = device_sm_count();
     if (sm <= 0 || num_seqs > kFlatMaxSeqs) return 0;
     const int kind = head_size >= 128 ? KIND_FP8_BF16Q : KIND_BF16;
-    const int flat = balanced_ctas(num_heads, num_kv_heads, head_size, kind, sm, false);
+    const int flat = std::max(balanced_ctas(num_heads, num_kv_heads, head_size, kind, sm, false),
+                              balanced_ctas(num_heads, num_kv_heads, head_size, KIND_FP4_BF16Q, sm, false));
     return workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, 0, flat).total;
   }
   const int P = partition_size > 0 ? (partition_size + kBlock - 1) / kBlock * kBlock : 0;
@@ -683,7 +692,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
                 ? 1
                 : 0;
   }
-  if (kind != KIND_FP8_BF16Q && kind != KIND_FP8_F16Q) p.k_scale = p.v_scale = nullptr;
+  if (!mma_fp8(kind) && !mma_fp4(kind)) p.k_scale = p.v_scale = nullptr;
   if (static_cast<int64_t>(p.Hkv) * p.HG > 65535) return PA_ERR_UNSUPPORTED_SHAPE;
 
   if (dry) {  // validation only (pa_decode_step checks everything before its first launch)
@@ -727,6 +736,15 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     p.vc_s2 = v_cache->stride[2];
     ProfScope ps(PA_KERNEL_DECODE, st);
     e = launch_decode_f32(p, st);
+  } else if (mma_fp4(kind)) {
+    p.k4 = static_cast<const char *>(k_cache->data);
+    p.v4 = static_cast<const char *>(v_cache->data);
+    p.kc_s0 = k_cache->stride[0];
+    p.kc_s1 = k_cache->stride[1];
+    p.vc_s0 = v_cache->stride[0];
+    p.vc_s1 = v_cache->stride[1];
+    ProfScope ps(PA_KERNEL_DECODE, st);
+    e = launch_decode_mma_fp4(p, kind, st);
   } else {
     CUtensorMap tmK, tmV;
     int nhd_k = 0, nhd_v = 0;
@@ -812,7 +830,7 @@ PA_API int pa_decode_step(pa_tensor *out, const pa_tensor *q, const pa_tensor *k
   const pa_decode_options o = opt ? *opt : pa_decode_options{};
   const bool internal = !o.workspace && o.workspace_bytes == 0;
   int r;
-  if ((r = check_desc(q, 3)) || (r = check_desc(key, 3)) || (r = check_desc(k_cache, 4))) return r;
+  if ((r = check_desc(q, 3)) || (r = check_desc(key, 3)) || !k_cache) return r ? r : PA_ERR_INVALID_ARG;
   if (!new_rows_start && key->shape[0] != q->shape[0]) return PA_ERR_INVALID_ARG;  // one new row per sequence
   if (new_rows_start && ((r = check_desc(new_rows_start, 1)) || new_rows_start->shape[0] != q->shape[0] + 1))
     return r ? r : PA_ERR_INVALID_ARG;
@@ -821,7 +839,9 @@ PA_API int pa_decode_step(pa_tensor *out, const pa_tensor *q, const pa_tensor *k
                        nullptr, 1, new_rows_start, true, true)))
     return r;
   const pa_write_options wo{o.k_scale, o.v_scale, o.scale_stride, o.device_error};
-  const int kv = k_cache->dtype == PA_FP8_E4M3 ? PA_KV_FP8_E4M3 : PA_KV_AUTO;
+  const int kv = k_cache->dtype == PA_FP8_E4M3   ? PA_KV_FP8_E4M3
+                 : k_cache->dtype == PA_FP4_E2M1 ? PA_KV_FP4_E2M1
+                                                 : PA_KV_AUTO;
   // Early reads pay when the write is long (several new rows per sequence: measured 202.8 ->
   // 198.7 us on 128 sequences x 64 rows into an E4M3 cache); a one-row write is over before
   // they help, and the early variant's in-loop wait costs more (c2: 33.3 vs 33.5 us).  With

@@ -1,4 +1,4 @@
-// pa_decode_mma.cuh -- paged decode attention on tensor cores (bf16 / f16 / e4m3 caches).
+// pa_decode_mma.cuh -- paged decode attention on tensor cores (bf16 / f16 / e4m3 / e2m1 caches).
 //
 // What it computes ("Inside vLLM CUDA Kernels", Part 3; "vLLM 源码完全拆解（七）"):
 // for each sequence s and query head h, o = sum_t softmax_t(scale * q . k_t) v_t
@@ -44,6 +44,12 @@
 // head-dimension order (each lane reads 32 contiguous bytes of a row) and the
 // query uses the same permutation, which leaves q . k unchanged.
 //
+// 4-bit (E2M1) caches: the same, with bulk copies of whole pages (pa_fp4.cuh) and every
+// widened pair multiplied by its group's E4M3 scale before the tensor-core products, which is
+// exact.  A lane's K run is whole scale groups and its V run lies inside one, so a page costs
+// a lane 4 + 4 scales; per element that is half a conversion and half a product (K), and a
+// quarter of a nibble exchange more (V).
+//
 // After the last page, each warp writes its (m, l, acc) to its own shared-memory
 // region; the CTA merges the W warp states with max/LSE rescaling and writes
 // either the normalised output (a sequence with a single partition) or the
@@ -60,6 +66,7 @@
 #pragma once
 
 #include "pa_device.cuh"
+#include "pa_fp4.cuh"
 #include "pa_internal.h"
 #include "pa_merge.cuh"
 
@@ -74,19 +81,23 @@ constexpr float kEmptyMax = -1e30f;         // running max of a column with no v
 template <int KIND, int D, int W, int STAGES>
 struct MmaCfg {
   static constexpr bool FP8 = KIND == KIND_FP8_BF16Q || KIND == KIND_FP8_F16Q;
-  static constexpr bool QBF16 = KIND == KIND_BF16 || KIND == KIND_FP8_BF16Q;  // query/output bf16
+  static constexpr bool FP4 = KIND == KIND_FP4_BF16Q || KIND == KIND_FP4_F16Q;
+  static constexpr bool WIDEN = FP8 || FP4;  // codes widened to f16, the query scaled to f16
+  static constexpr bool QBF16 = KIND == KIND_BF16 || KIND == KIND_FP8_BF16Q || KIND == KIND_FP4_BF16Q;  // query/output bf16
   static constexpr bool MMA_BF16 = KIND == KIND_BF16;
   static constexpr int ELEM = FP8 ? 1 : 2;     // cache element bytes
   static constexpr int ROWB = D * ELEM;        // bytes of one token row of a page
   static constexpr int NBOX = ROWB / 128;      // 128-byte TMA boxes across a row
   static constexpr int BOXE = 128 / ELEM;      // elements per box row
-  static constexpr int PAGEB = kBlock * ROWB;  // one (block, kv head) page
+  static constexpr int PAGEB = FP4 ? fp4_page_bytes(D) : kBlock * ROWB;  // one (block, kv head) page
+  // widened caches: lane (r, c) of a fragment covers elements 128 b + QE c + [0, QE) of a row
+  static constexpr int QB = D >= 128 ? D / 128 : 1, QE = D >= 128 ? 32 : D / 4;
   static constexpr int STAGEB = 2 * PAGEB;     // K page + V page
   static constexpr int KT = D / 16;            // k-steps of Q.K^T = d-tiles of P.V
   static constexpr int THREADS = W * 32;
   static constexpr size_t SCRATCH_OFF = static_cast<size_t>(W) * STAGES * STAGEB + W * STAGES * 8;
   static constexpr size_t SMEM = 1024 + SCRATCH_OFF + kMmaScratch;
-  static_assert(ROWB % 128 == 0, "page rows must be whole 128-byte swizzle spans");
+  static_assert(FP4 || ROWB % 128 == 0, "page rows must be whole 128-byte swizzle spans");
   static_assert(STAGES * STAGEB >= 64 + 8 * D * 4, "warp region must hold the merge state");
   static_assert(static_cast<size_t>(W) * STAGES * STAGEB >= 8 * kMergeSmemParts * 4, "merge weights");
   static_assert(kMmaScratch >= kLptScratchBytes, "ranking scratch");
@@ -141,6 +152,11 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
       const uint32_t bar = bar0 + 8 * st;
       const uint32_t kdst = stage0 + st * C::STAGEB;
       mbar_arrive_expect_tx(bar, C::STAGEB);
+      if constexpr (C::FP4) {  // a page is one contiguous run: one bulk copy each
+        bulk_load(kdst, p.k4 + pid * p.kc_s0 + g * p.kc_s1, C::PAGEB, bar, pol);
+        bulk_load(kdst + C::PAGEB, p.v4 + pid * p.vc_s0 + g * p.vc_s1, C::PAGEB, bar, pol);
+        return;
+      }
       const int c1 = p.nhd ? g : 0, c2 = p.nhd ? 0 : g;  // (token, head) or (head, token) order
 #pragma unroll
       for (int b = 0; b < C::NBOX; ++b) tma_load_4d(kdst + b * 2048, tmK, bar, b * C::BOXE, c1, c2, pid, pol);
@@ -159,7 +175,7 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
   const char *qrow = static_cast<const char *>(p.q) + cm.q_off(p, qvalid ? qh : 0) * 2;
   uint32_t qf[C::KT][2];
   float sc0, sc1;  // score scale (log2 units) of this lane's two head columns 2qc, 2qc+1
-  if constexpr (!C::FP8) {
+  if constexpr (!C::WIDEN) {
 #pragma unroll
     for (int j = 0; j < C::KT; ++j) {
       const uint32_t lo = __ldg(reinterpret_cast<const uint32_t *>(qrow + (16 * j + 2 * qc) * 2));
@@ -169,14 +185,14 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     }
     sc0 = sc1 = p.scale_log2;
   } else {
-    // lane covers d = 128 b + 32 qc + [0, 32) of head qh, box b
-    uint4 raw[C::NBOX][4];
+    // lane covers d = 128 b + QE qc + [0, QE) of head qh
+    uint4 raw[C::QB][C::QE / 8];
     float mx = 0.f;
 #pragma unroll
-    for (int b = 0; b < C::NBOX; ++b) {
+    for (int b = 0; b < C::QB; ++b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        raw[b][i] = __ldg(reinterpret_cast<const uint4 *>(qrow + (128 * b + 32 * qc + 8 * i) * 2));
+      for (int i = 0; i < C::QE / 8; ++i) {
+        raw[b][i] = __ldg(reinterpret_cast<const uint4 *>(qrow + (128 * b + C::QE * qc + 8 * i) * 2));
         const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -195,11 +211,11 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     const int sh = max(-120, min(120, 14 - ex));
     const float sfac = ldexpf(1.f, sh);  // max |q| * sfac in [2^14, 2^15)
 #pragma unroll
-    for (int b = 0; b < C::NBOX; ++b) {
+    for (int b = 0; b < C::QB; ++b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < C::QE / 8; ++i) {
         const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
-        // elements 8i .. 8i+7 of the lane's 32 = k-steps j = 2i, 2i+1 (4 elements each)
+        // elements 8i .. 8i+7 of the lane's QE = k-steps j = 2i, 2i+1 (4 elements each)
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
           const float2 f0 = C::QBF16 ? unpack_bf16(w4[2 * jj]) : unpack_f16(w4[2 * jj]);
@@ -263,7 +279,33 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
 
     // ---- scores: two accumulation chains over the k-steps
     float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (!C::FP8) {
+    if constexpr (C::FP4) {
+      // lane (ra, qc) holds elements QE qc .. of tokens ra and ra + 8: whole scale groups, so
+      // each f16x2 of codes takes one product with its own token's and group's scale (exact:
+      // at most 6 significant bits, magnitudes 2^-10 .. 2688)
+#pragma unroll
+      for (int b = 0; b < C::QB; ++b) {
+        uint32_t wa[C::QE / 8], wb[C::QE / 8], sa[C::QE / 16], sb[C::QE / 16];
+        fp4_lane_codes<D>(kb, ra, b, qc, wa);
+        fp4_lane_codes<D>(kb, ra + 8, b, qc, wb);
+        fp4_lane_scales<D>(kb, ra, b, qc, sa);
+        fp4_lane_scales<D>(kb, ra + 8, b, qc, sb);
+#pragma unroll
+        for (int i = 0; i < C::QE / 8; ++i) {
+          uint32_t a0[4], a1[4];  // k-steps 2i and 2i + 1
+          e2m1x8_to_f16x2x4(wa[i], a0[0], a0[2], a1[0], a1[2]);
+          e2m1x8_to_f16x2x4(wb[i], a0[1], a0[3], a1[1], a1[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a0[e] = mul_f16x2(a0[e], (e & 1) ? sb[i >> 1] : sa[i >> 1]);
+            a1[e] = mul_f16x2(a1[e], (e & 1) ? sb[i >> 1] : sa[i >> 1]);
+          }
+          const int j = b * (C::QE / 4) + 2 * i;
+          mma_f16(c0, a0, qf[j][0], qf[j][1]);
+          mma_f16(c1, a1, qf[j + 1][0], qf[j + 1][1]);
+        }
+      }
+    } else if constexpr (!C::FP8) {
       const int lrow = (lane & 7) | (lane & 8);
       const int lhi = lane >> 4;
 #pragma unroll
@@ -362,7 +404,48 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     }
 
     // ---- O^T += V^T . P^T (tail rows of the last page zeroed first)
-    if constexpr (!C::FP8) {
+    if constexpr (C::FP4) {
+      // lane (ra, qc) holds codes of one run of D / 8 (at most 16) elements, inside one scale
+      // group, of tokens 2qc, 2qc+1 | 2qc+8, 2qc+9.  Nibbles of two tokens are brought
+      // together so that one conversion gives the pair the product contracts over: bytes
+      // (token t0 | token t1 << 4) of the even elements, then of the odd ones.  A hidden
+      // token's scale becomes 0 (its codes are finite), so nothing stale reaches the sum.
+      constexpr int VW = D >= 128 ? 2 : 1;  // words of eight codes per token and section
+      const int t0 = 2 * qc, t1 = t0 + 1, t2 = t0 + 8, t3 = t0 + 9;
+#pragma unroll
+      for (int b = 0; b < C::QB; ++b) {
+        uint32_t w[4][VW];
+        fp4_run_codes<D>(vb, t0, b, ra, w[0]);
+        fp4_run_codes<D>(vb, t1, b, ra, w[1]);
+        fp4_run_codes<D>(vb, t2, b, ra, w[2]);
+        fp4_run_codes<D>(vb, t3, b, ra, w[3]);
+        const int sj = D == 64 ? ra >> 1 : 8 * b + ra;  // the run's scale group
+        const uint32_t z0 = t0 < nv ? lds_u8(vb + fp4_scale_off(D, t0, sj)) : 0u;
+        const uint32_t z1 = t1 < nv ? lds_u8(vb + fp4_scale_off(D, t1, sj)) : 0u;
+        const uint32_t z2 = t2 < nv ? lds_u8(vb + fp4_scale_off(D, t2, sj)) : 0u;
+        const uint32_t z3 = t3 < nv ? lds_u8(vb + fp4_scale_off(D, t3, sj)) : 0u;
+        const uint32_t s01 = e4m3x2_to_f16x2(z0 | (z1 << 8)), s23 = e4m3x2_to_f16x2(z2 | (z3 << 8));
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
+          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd elements of the word
+          const uint32_t xe = (w[0][i] & kLow) | ((w[1][i] << 4) & ~kLow), xo = ((w[0][i] >> 4) & kLow) | (w[1][i] & ~kLow);
+          const uint32_t ye = (w[2][i] & kLow) | ((w[3][i] << 4) & ~kLow), yo = ((w[2][i] >> 4) & kLow) | (w[3][i] & ~kLow);
+          e2m1x8_to_f16x2x4(xe, e01[0], e01[1], e01[2], e01[3]);
+          e2m1x8_to_f16x2x4(xo, o01[0], o01[1], o01[2], o01[3]);
+          e2m1x8_to_f16x2x4(ye, e23[0], e23[1], e23[2], e23[3]);
+          e2m1x8_to_f16x2x4(yo, o23[0], o23[1], o23[2], o23[3]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {  // fragment rows ra: element 2m of the word, ra + 8: 2m + 1
+            const uint32_t a[4] = {mul_f16x2(e01[m], s01), mul_f16x2(o01[m], s01), mul_f16x2(e23[m], s23),
+                                   mul_f16x2(o23[m], s23)};
+            const int t = b * 8 + 4 * i + m;
+            mma_f16(acc[t], a, bh0, bh1);
+            mma_f16(acc[t], a, bl0, bl1);
+          }
+        }
+      }
+    } else if constexpr (!C::FP8) {
       const uint32_t mA = (2 * qc < nv ? 0x0000FFFFu : 0u) | (2 * qc + 1 < nv ? 0xFFFF0000u : 0u);
       const uint32_t mB = (2 * qc + 8 < nv ? 0x0000FFFFu : 0u) | (2 * qc + 9 < nv ? 0xFFFF0000u : 0u);
       const int vtok = (lane & 7) | ((lane >> 4) << 3);
@@ -448,7 +531,8 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     for (int i = 0; i < 4; ++i) {
       const int head = 2 * qc + (i & 1);
       int d;
-      if constexpr (!C::FP8) d = 16 * t + ra + 8 * (i >> 1);
+      if constexpr (!C::WIDEN) d = 16 * t + ra + 8 * (i >> 1);
+      else if constexpr (D == 64) d = 8 * ra + 2 * t + (i >> 1);
       else d = 128 * (t >> 3) + 16 * ra + 2 * (t & 7) + (i >> 1);
       wacc[head * D + d] = acc[t][i];
     }
@@ -526,8 +610,10 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     const uint32_t bar0 = sbase + static_cast<uint32_t>(W * STAGES * C::STAGEB + warp * STAGES * 8);
     for (int st = 0; st < STAGES; ++st) mbar_init(bar0 + 8 * st, 1);
     fence_barrier_init();
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
+    if constexpr (!C::FP4) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
   }
   __syncwarp();
   // Warm L2 with the metadata this launch reads on its critical path.  A prefetch
@@ -571,7 +657,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   // head reading the same pages, evict-normal measured 3 % slower on GB300: 4 query tokens
   // x 256 sequences x 32/8 heads, 395.6 vs 384.3 us.)
   const uint64_t pol = policy_evict_first();
-  const float vs = (C::FP8 && p.v_scale) ? __ldg(p.v_scale + g * p.scale_stride) : 1.f;
+  const float vs = (C::WIDEN && p.v_scale) ? __ldg(p.v_scale + g * p.scale_stride) : 1.f;
   float *const smem_w = reinterpret_cast<float *>(sgen);  // merge weights (stage buffers, free by then)
   int used = 0;
   bool stalled = false;

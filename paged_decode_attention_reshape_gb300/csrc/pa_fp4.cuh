@@ -57,4 +57,45 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Lane (r, c)'s codes of token t in section b of the page at shared address `page`: elements
+// 128 b + 32 c .. + 31 in four words (head size 64: 16 c .. + 15 in two).
+template <int D>
+__device__ __forceinline__ void fp4_lane_codes(uint32_t page, int t, int b, int c, uint32_t (&w)[D >= 128 ? 4 : 2]) {
+  if constexpr (D >= 128) {
+    const uint4 v = lds128(page + fp4_code_off(D, t, 64 * b + 16 * c));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    const uint2 v = lds64(page + fp4_code_off(D, t, 8 * c));
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+// The scales of those elements, each in both halves of an f16x2.
+template <int D>
+__device__ __forceinline__ void fp4_lane_scales(uint32_t page, int t, int b, int c, uint32_t (&s)[D >= 128 ? 2 : 1]) {
+  if constexpr (D >= 128) {
+    const uint32_t two = e4m3x2_to_f16x2(lds_u16(page + fp4_scale_off(D, t, 8 * b + 2 * c)));
+    s[0] = __byte_perm(two, two, 0x1010);
+    s[1] = __byte_perm(two, two, 0x3232);
+  } else {
+    const uint32_t one = lds_u8(page + fp4_scale_off(D, t, c));
+    s[0] = e4m3x2_to_f16x2(one | (one << 8));
+  }
+}
+// Run r of token t in section b: elements 128 b + 16 r .. + 15 in two words (head size 64:
+// 8 r .. + 7 in one).
+template <int D>
+__device__ __forceinline__ void fp4_run_codes(uint32_t page, int t, int b, int r, uint32_t (&w)[D >= 128 ? 2 : 1]) {
+  if constexpr (D >= 128) {
+    const uint2 v = lds64(page + fp4_code_off(D, t, 64 * b + 8 * r));
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = lds32(page + fp4_code_off(D, t, 4 * r));
+  }
+}
+
 }  // namespace pa

@@ -20,7 +20,9 @@ enum DecodeKind : int {
   KIND_F16 = 1,       // f16 cache [f16 q]
   KIND_FP8_BF16Q = 2, // e4m3 cache [bf16 q]
   KIND_FP8_F16Q = 3,  // e4m3 cache [f16 q]
-  KIND_F32 = 4        // fp32 cache [fp32 q], CUDA-core path
+  KIND_F32 = 4,       // fp32 cache [fp32 q], CUDA-core path
+  KIND_FP4_BF16Q = 5, // e2m1 page cache [bf16 q]
+  KIND_FP4_F16Q = 6   // e2m1 page cache [f16 q]
 };
 
 struct WriteParams {
@@ -112,8 +114,9 @@ struct DecodeParams {
   // first K/V group): 0 = the normal limit, > 0 = that many polls, < 0 = give up at once.
   // Tests use it to make a bounded wait run out; every later wait and drain keeps the normal limit.
   int first_wait_limit;
-  // fp32 path only: direct cache pointers and strides (elements)
+  // fp32 and 4-bit paths: direct cache pointers and strides (fp32: elements; 4-bit: bytes, no s2)
   const float *kc, *vc;
+  const char *k4, *v4;
   int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
 };
 
@@ -156,6 +159,7 @@ cudaError_t launch_write(const WriteParams &p, int in_dtype, int cache_dtype, in
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st);
 cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, cudaStream_t st);
 
+constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND_FP4_F16Q; }
 // Tensor-core kernel shape per (kind, head size): warps per CTA and pipeline
 // stages per warp.  Shared memory = W * STAGES * 2 pages (+ alignment, barriers).
 // A CTA's loads are served at a bounded rate for each warp's stages in flight
@@ -166,18 +170,21 @@ cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype,
 constexpr int mma_warps(int kind, int D) { return (void)kind, D == 64 ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
-constexpr int mma_stages(int kind, int D) { return (void)kind, (void)D, 2; }
+constexpr int mma_stages(int kind, int D) { return (void)D, mma_fp4(kind) ? 4 : 2; }
 // Resident CTAs per SM the register allocation must allow (ptxas launch bound): as
 // many as the shared memory admits, so registers never cut the occupancy, except
 // for the E4M3 head-size-128 kernel (6 by shared memory; held at 4 to avoid spills).
 constexpr bool mma_fp8(int kind) { return kind == KIND_FP8_BF16Q || kind == KIND_FP8_F16Q; }
 constexpr int mma_min_ctas(int kind, int D) {
+  if (mma_fp4(kind)) return D == 64 ? 2 : D == 128 ? 4 : 3;
   return D == 64 ? 3 : D == 128 ? (mma_fp8(kind) ? 4 : 3) : (mma_fp8(kind) ? 3 : 1);
+}
+constexpr int mma_page_bytes(int kind, int D) {
+  return mma_fp4(kind) ? 9 * D : kBlock * D * (mma_fp8(kind) ? 1 : 2);
 }
 constexpr size_t kMmaScratch = 2048;  // sequence-order ranking scratch (after the barriers)
 constexpr size_t mma_smem(int kind, int D) {
-  return 1024 + static_cast<size_t>(mma_warps(kind, D)) * mma_stages(kind, D) *
-                    (2 * kBlock * D * ((kind == KIND_FP8_BF16Q || kind == KIND_FP8_F16Q) ? 1 : 2) + 8) +
+  return 1024 + static_cast<size_t>(mma_warps(kind, D)) * mma_stages(kind, D) * (2 * mma_page_bytes(kind, D) + 8) +
          kMmaScratch;
 }
 
@@ -185,6 +192,7 @@ cudaError_t launch_decode_mma_16(const DecodeParams &p, int kind, const CUtensor
                                  cudaStream_t st);  // KIND_BF16, KIND_F16
 cudaError_t launch_decode_mma_fp8(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   cudaStream_t st);  // KIND_FP8_*
+cudaError_t launch_decode_mma_fp4(const DecodeParams &p, int kind, cudaStream_t st);  // KIND_FP4_*
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st);
 // Query-tile kernel for chunks of query tokens (pa_attention_varlen) on tcgen05 tensor
 // cores: bf16 / f16 caches, head sizes 64 and 128; never splits the page range.
@@ -202,6 +210,7 @@ constexpr int kChunkTwoTileColumns = 128;
 // shared memory, registers and threads); 0 when it cannot be queried.
 int occupancy_decode_mma_16(int kind, int D);
 int occupancy_decode_mma_fp8(int kind, int D);
+int occupancy_decode_mma_fp4(int kind, int D);
 
 // Launch `kern` as a programmatic dependent of the previous work on `st`, in
 // thread-block clusters of `cluster_x` CTAs along x when cluster_x > 1.
