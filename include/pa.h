@@ -15,6 +15,7 @@
  *                          "vLLM 源码完全拆解（七）", 参数与内存布局 through V1 与 V2)
  *
  *   pa_decode_step         the cache write and the decode of one step in one call
+ *   pa_decode_accumulate   the decode that also adds up every token's attention weight
  *   pa_attention_varlen    several new query tokens per sequence, causal
  *                          ("Inside vLLM CUDA Kernels", Part 3, the varlen read path);
  *                          long chunks run on a tcgen05 query-tile kernel
@@ -315,6 +316,32 @@ typedef struct {
 int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
                   const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads,
                   const pa_decode_options *opt, pa_stream_t stream);
+
+/*
+ * pa_decode_accumulate -- pa_decode_opt that also adds the attention weight of every cached
+ * token to an array: the statistics by which pa_evict shortens a sequence.
+ *
+ *   weights          PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16, innermost stride 1.  For
+ *                    every sequence s, KV head g and token t < seq_lens[s], weights[s, g, t]
+ *                    grows by the sum over the Hq / Hkv query heads of g of their softmax
+ *                    weight of t (so by Hq / Hkv over the whole row).  Other entries are not
+ *                    touched.  A sequence that sets an error bit adds nothing.
+ *   other arguments  as pa_decode_opt, and the same outputs.  partition_size: 0, -1 or > 0
+ *                    (the cluster and balanced splits give PA_ERR_UNSUPPORTED_SHAPE).  The
+ *                    workspace (pa_decode_accumulate_workspace_size bytes, used by every
+ *                    call, split or not) holds one fp32 score per (query head, token):
+ *                    4 bytes against the 2 head_size * (element bytes) of a token's K and V.
+ * Two kernels: the decode, which stores its scores, and a second one that turns them into
+ * weights once every head's softmax sum is known.
+ */
+int pa_decode_accumulate(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                         const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads,
+                         pa_tensor *weights, const pa_decode_options *opt, pa_stream_t stream);
+
+/* Bytes of pa_decode_accumulate's workspace for the partition size the call ends up using (0 =
+ * unsplit; arguments as pa_decode_workspace_size).  Host-only; invalid arguments give 0. */
+size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                           int max_blocks_per_seq, int partition_size);
 
 /*
  * pa_attention_varlen -- paged attention for several new query tokens per sequence

@@ -31,7 +31,7 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", 
           -8: "PA_ERR_DEVICE_TIMEOUT", -9: "PA_ERR_NO_BLOCKS"}
 
 EXPORTS = ("pa_reshape_and_cache", "pa_reshape_and_cache_opt", "pa_decode", "pa_decode_ex", "pa_decode_opt",
-           "pa_gather_cache",
+           "pa_gather_cache", "pa_decode_accumulate", "pa_decode_accumulate_workspace_size",
            "pa_attention_varlen", "pa_decode_step", "pa_decode_noalloc", "pa_decode_plan", "pa_decode_workspace_size", "pa_check_device_error",
            "pa_status_string", "pa_profile_enable", "pa_profile_read", "pa_bm_create", "pa_bm_destroy",
            "pa_bm_num_free", "pa_bm_block_refs", "pa_bm_seq_len", "pa_bm_append", "pa_bm_fork", "pa_bm_free",
@@ -95,6 +95,10 @@ def lib() -> ctypes.CDLL:
             L.pa_gather_cache.argtypes = [T, T, T, T, T, ctypes.POINTER(PaWriteOptions), P]
             L.pa_decode_opt.restype = i32
             L.pa_decode_opt.argtypes = [T, T, T, T, T, T, f32, i32, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_decode_accumulate.restype = i32
+            L.pa_decode_accumulate.argtypes = [T, T, T, T, T, T, f32, i32, T, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_decode_accumulate_workspace_size.restype = ctypes.c_size_t
+            L.pa_decode_accumulate_workspace_size.argtypes = [i32] * 6
             L.pa_decode_step.restype = i32
             L.pa_decode_step.argtypes = [T, T, T, T, T, T, T, T, T, T, f32, i32, ctypes.POINTER(PaDecodeOptions), P]
             L.pa_attention_varlen.restype = i32
@@ -233,6 +237,29 @@ def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float,
     rc = lib().pa_decode_opt(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), ctypes.byref(o),
                              _stream(stream))
     _check(rc, "pa_decode_opt")
+
+
+def pa_decode_accumulate(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num_kv_heads: int, weights,
+                         k_scale=None, v_scale=None, scale_stride: int = 0, alibi_slopes=None,
+                         partition_size: int = 0, workspace=None, device_error=None, stream=None,
+                         first_wait_limit: int = 0) -> None:
+    """pa_decode_opt that also adds every cached token's attention weight, summed over the query heads of
+    its KV head, to weights (fp32 [S, Hkv, W >= max blocks * 16]).  Options as pa_decode_opt (no cluster
+    or balanced split); the workspace size is pa_decode_accumulate_workspace_size."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
+                        _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
+    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
+    rc = lib().pa_decode_accumulate(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads),
+                                    ctypes.byref(desc(weights)), ctypes.byref(o), _stream(stream))
+    _check(rc, "pa_decode_accumulate")
+
+
+def pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,
+                                        partition_size) -> int:
+    """Bytes of pa_decode_accumulate's workspace; zero-fill it once before first use (torch.zeros)."""
+    return int(lib().pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size,
+                                                         max_blocks_per_seq, partition_size))
 
 
 def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_table, seq_lens, scale: float,

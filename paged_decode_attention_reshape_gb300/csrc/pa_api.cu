@@ -268,6 +268,21 @@ WsLayout workspace_layout(int S, int Hq, int Hkv, int D, int maxNB, int P, int f
   return L;
 }
 
+// pa_decode_accumulate's part of the workspace, behind the split-KV part: log2 of every
+// head's softmax sum, then one score per (sequence, KV head, head group, token, column).
+struct ScoreLayout {
+  int cols;  // columns per token: the group's query heads rounded up to 1, 2, 4 or 8
+  size_t scores_off, total;
+};
+ScoreLayout score_layout(int S, int Hq, int Hkv, int maxNB) {
+  const int G = Hq / Hkv, HG = (G + 7) / 8;
+  ScoreLayout L;
+  L.cols = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8;
+  L.scores_off = round256(static_cast<size_t>(S) * Hq * sizeof(float));
+  L.total = L.scores_off + static_cast<size_t>(S) * Hkv * HG * maxNB * kBlock * L.cols * sizeof(float);
+  return L;
+}
+
 // ------------------------------------------------------ internal workspace
 
 // One growing allocation per device: an arrival-counter region, then the partial states of
@@ -569,6 +584,16 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
   return workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, P, 0).total;
 }
 
+PA_API size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                                  int max_blocks_per_seq, int partition_size) {
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_size < 0 ||
+      max_blocks_per_seq < 0 || partition_size < -1)
+    return 0;
+  return round256(pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,
+                                           partition_size)) +
+         score_layout(num_seqs, num_heads, num_kv_heads, max_blocks_per_seq).total;
+}
+
 namespace {
 
 // Decode (query_start_loc == NULL: one query token per sequence, q [S, Hq, D]) or varlen
@@ -579,7 +604,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
                 const pa_decode_options &o, bool internal_ws, pa_stream_t stream,
                 const pa_tensor *query_start_loc = nullptr, int max_query_len = 1,
                 const pa_tensor *new_rows_start = nullptr, bool early = false, bool dry = false,
-                size_t *ws_need = nullptr, size_t *ws_counters = nullptr) {
+                size_t *ws_need = nullptr, size_t *ws_counters = nullptr, pa_tensor *weights = nullptr) {
   const float *k_scale = o.k_scale, *v_scale = o.v_scale;
   const int partition_size = o.partition_size;
   void *workspace = o.workspace;
@@ -623,7 +648,17 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     if (new_rows_start->shape[0] != S64 + 1 || new_rows_start->stride[0] != 1) return PA_ERR_INVALID_ARG;
     if (S64 > 0 && !new_rows_start->data) return PA_ERR_INVALID_ARG;
   }
+  if (weights) {
+    if ((r = check_desc(weights, 3))) return r;
+    if (weights->dtype != PA_F32) return PA_ERR_UNSUPPORTED_DTYPE;
+    if (weights->shape[0] != S64 || weights->shape[1] != Hkv || weights->shape[2] < block_table->shape[1] * kBlock ||
+        weights->stride[2] != 1)
+      return PA_ERR_INVALID_ARG;
+    if (o.partition_size < -1) return PA_ERR_UNSUPPORTED_SHAPE;  // cluster and balanced splits
+  }
   if (S64 == 0 || q->shape[0] == 0) return PA_OK;
+  if (weights && block_table->shape[1] > 0 && !weights->data) return PA_ERR_INVALID_ARG;
+  if (weights && reinterpret_cast<uintptr_t>(weights->data) % 4) return PA_ERR_ALIGNMENT;
   if (!q->data || !out->data || !block_table->data || !seq_lens->data) return PA_ERR_INVALID_ARG;
   const int qb = elem_bytes(q->dtype);
   if (!aligned16(q->data) || !aligned16(out->data)) return PA_ERR_ALIGNMENT;
@@ -707,17 +742,25 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     }
     return PA_OK;
   }
-  if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0) {
-    const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, maxNB, P, pl.flat);
+  if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0 || weights) {
+    const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, maxNB, max_parts > 1 ? P : 0, pl.flat);
+    const ScoreLayout sc = weights ? score_layout(S, Hq, Hkv, maxNB) : ScoreLayout{0, 0, 0};
+    const size_t total = weights ? round256(lay.total) + sc.total : lay.total;
     size_t ml_off = lay.ml_off;
     if (internal_ws) {
       DevWorkspace w;
-      if ((r = internal_workspace(lay.ml_off, lay.total - lay.ml_off, st, &w))) return r;
+      if ((r = internal_workspace(lay.ml_off, total - lay.ml_off, st, &w))) return r;
       workspace = w.ptr;
       ml_off = w.counters;
     } else {
-      if (!workspace || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+      if (!workspace || workspace_bytes < total) return PA_ERR_WORKSPACE;
       if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
+    }
+    if (weights) {
+      char *base = static_cast<char *>(workspace) + ml_off + (round256(lay.total) - lay.ml_off);
+      p.lse = reinterpret_cast<float *>(base);
+      p.scores = reinterpret_cast<float *>(base + sc.scores_off);
+      p.score_cols = sc.cols;
     }
     p.counters = static_cast<int *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ml_off);
@@ -761,6 +804,22 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     } else {
       e = launch_decode_mma_fp8(p, kind, tmK, tmV, st);
     }
+  }
+  if (e == cudaSuccess && weights) {
+    WeightsParams w{};
+    w.seq_lens = p.seq_lens;
+    w.scores = p.scores;
+    w.lse = p.lse;
+    w.weights = static_cast<float *>(weights->data);
+    w.w_ss = weights->stride[0];
+    w.w_hs = weights->stride[1];
+    w.S = S;
+    w.Hkv = Hkv;
+    w.G = p.G;
+    w.HG = p.HG;
+    w.max_tokens = maxNB * kBlock;
+    ProfScope ps(PA_KERNEL_DECODE, st);
+    e = launch_weights(w, p.score_cols, st);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -810,6 +869,16 @@ PA_API int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_
   const pa_decode_options o = opt ? *opt : pa_decode_options{};
   const bool internal = !o.workspace && o.workspace_bytes == 0;
   return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream);
+}
+
+PA_API int pa_decode_accumulate(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                                const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads,
+                                pa_tensor *weights, const pa_decode_options *opt, pa_stream_t stream) {
+  if (!weights) return PA_ERR_INVALID_ARG;
+  const pa_decode_options o = opt ? *opt : pa_decode_options{};
+  const bool internal = !o.workspace && o.workspace_bytes == 0;
+  return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
+                     nullptr, 1, nullptr, false, false, nullptr, nullptr, weights);
 }
 
 PA_API int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,

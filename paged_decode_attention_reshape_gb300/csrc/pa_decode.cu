@@ -1,4 +1,4 @@
-// pa_decode.cu -- the fp32 decode path (CUDA cores).
+// pa_decode.cu -- the fp32 decode path (CUDA cores), and the accumulation of attention weights.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_merge.cuh"
@@ -13,7 +13,8 @@ namespace pa {
 // (coalesced 128-byte loads), one butterfly reduction per (token, head) gives
 // the score, and the per-head online-softmax state is kept in registers.
 
-template <int D, int W>
+// ACC: scores and softmax sums kept for pa_decode_accumulate.
+template <int D, int W, bool ACC>
 __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p) {
   constexpr int PER = D / 32;
   __shared__ float sm[W][8][D + 2];
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
           z = fmaf(ab[hh], static_cast<float>(tt - pos[hh]), z * p.scale_log2);
+          if (ACC && lane == 0)
+            p.scores[((static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * p.max_blocks * kBlock + tt) * p.score_cols + hh] = z;
           const float mn = fmaxf(m[hh], z);
           const float al = ex2(m[hh] - mn);
           const float pz = ex2(z - mn);
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
       }
       if (direct) {
         static_cast<float *>(p.out)[cm.out_off(p, hh) + d] = den > 0.f ? num / den : 0.f;
+        if (ACC && d == 0) p.lse[cm.row(hh) * p.Hq + cm.head(hh)] = log_total(M, den);
       } else {
         const int64_t row = rows(hh, part);
         p.part_acc[row * D + d] = num;
@@ -172,22 +176,87 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
       }
     }
   }
+  if (ACC && any_bad && direct) drop_lse(p, cm, ng);
   static_assert(sizeof(sm) >= 8 * kMergeSmemParts * 4, "merge weights reuse sm");
   if (!direct)
-    merge_if_last<float, D>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * s, ng, nparts, 1.f, any_bad,
+    merge_if_last<float, D, ACC>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * s, ng, nparts, 1.f, any_bad,
                             W * 32, &sm[0][0][0], rows);
 }
 
-cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
+namespace {
+template <bool ACC>
+cudaError_t launch_f32(const DecodeParams &p, cudaStream_t st) {
   const dim3 grid(p.max_parts, p.Hkv * p.HG, p.S);
   cudaError_t e;
   switch (p.D) {
-    case 64: e = launch_pdl(decode_f32_kernel<64, 4>, grid, dim3(128), 0, st, p.cluster, p); break;
-    case 128: e = launch_pdl(decode_f32_kernel<128, 4>, grid, dim3(128), 0, st, p.cluster, p); break;
-    case 256: e = launch_pdl(decode_f32_kernel<256, 2>, grid, dim3(64), 0, st, p.cluster, p); break;
+    case 64: e = launch_pdl(decode_f32_kernel<64, 4, ACC>, grid, dim3(128), 0, st, p.cluster, p); break;
+    case 128: e = launch_pdl(decode_f32_kernel<128, 4, ACC>, grid, dim3(128), 0, st, p.cluster, p); break;
+    case 256: e = launch_pdl(decode_f32_kernel<256, 2, ACC>, grid, dim3(64), 0, st, p.cluster, p); break;
     default: return cudaErrorInvalidValue;
   }
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
+  return p.scores ? launch_f32<true>(p, st) : launch_f32<false>(p, st);
+}
+
+// ------------------------------------------------- accumulated attention weights
+//
+// weights[s, g, t] += sum over the query heads h of KV head g of 2^(score_h,t - lse_h), the
+// attention weight of token t: the decode kernels have left every score (log2 units) and
+// every head's log2 of the softmax sum, which is known only after the last page, in the
+// workspace.  Scores are stored token by token, the group's columns together, so a thread
+// reads one 16- or 32-byte run per token and adjacent threads adjacent runs.  Keeping the
+// scores costs 4 bytes a (query head, token) each way, mostly served by L2, against a second
+// read of every K page (2 D bytes a (KV head, token) for a 16-bit cache).
+template <int CW>
+__global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
+  const int s = blockIdx.z, g = blockIdx.y;
+  grid_dependency_wait();
+  const int len = __ldg(p.seq_lens + s);
+  if (len < 0 || len > p.max_tokens) return;  // reported by the decode
+  float *w = p.weights + s * p.w_ss + g * p.w_hs;
+  for (int t = blockIdx.x * 256 + threadIdx.x; t < len; t += gridDim.x * 256) {
+    float sum = 0.f;
+    for (int hg = 0; hg < p.HG; ++hg) {
+      const float *sc = p.scores + ((static_cast<int64_t>(s) * p.Hkv + g) * p.HG + hg) * static_cast<int64_t>(p.max_tokens) * CW +
+                        static_cast<int64_t>(t) * CW;
+      const float *lse = p.lse + static_cast<int64_t>(s) * p.Hkv * p.G + g * p.G + hg * 8;
+      const int n = min(CW, p.G - hg * 8);
+      float v[CW];
+      if constexpr (CW >= 4) {
+#pragma unroll
+        for (int i = 0; i < CW / 4; ++i) {
+          const float4 f = __ldcg(reinterpret_cast<const float4 *>(sc) + i);
+          v[4 * i] = f.x;
+          v[4 * i + 1] = f.y;
+          v[4 * i + 2] = f.z;
+          v[4 * i + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CW; ++i) v[i] = __ldcg(sc + i);
+      }
+#pragma unroll
+      for (int i = 0; i < CW; ++i)
+        if (i < n) sum += ex2(v[i] - __ldcg(lse + i));
+    }
+    w[t] += sum;
+  }
+}
+
+cudaError_t launch_weights(const WeightsParams &p, int cols, cudaStream_t st) {
+  const int64_t blocks = (static_cast<int64_t>(p.max_tokens) + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), p.Hkv, p.S);
+  switch (cols) {
+    case 1: return launch_pdl(weights_kernel<1>, grid, dim3(256), 0, st, 1, p);
+    case 2: return launch_pdl(weights_kernel<2>, grid, dim3(256), 0, st, 1, p);
+    case 4: return launch_pdl(weights_kernel<4>, grid, dim3(256), 0, st, 1, p);
+    case 8: return launch_pdl(weights_kernel<8>, grid, dim3(256), 0, st, 1, p);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pa

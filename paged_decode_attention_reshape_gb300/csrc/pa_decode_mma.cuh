@@ -59,8 +59,8 @@
 //
 // The kernel is launched as a programmatic dependent of the previous grid on the
 // stream: it waits for that grid before its first global read, so its launch
-// overlaps the previous kernel's tail.  Three variants per shape: the general one
-// (several query tokens, ALiBi), PLAIN (one query token, no ALiBi: one compare per score
+// overlaps the previous kernel's tail.  Four variants per shape: the general one
+// (several query tokens, ALiBi), the same storing its scores (pa_decode_accumulate), PLAIN (one query token, no ALiBi: one compare per score
 // for the page tail), and PLAIN + EARLY for pa_decode_step's multi-row steps, which reads
 // everything but the pages with new positions before that wait.
 #pragma once
@@ -113,7 +113,8 @@ struct MmaCfg {
 // already holds lane i's table entry for the warp's i-th page (read early by the
 // caller).  Returns true after a bad block id or a timed-out wait; `stalled` is set
 // on a timeout, after which the CTA must not issue into its stages again.
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY>
+// ACC: every score goes to p.scores too (log2 units; -inf where a column does not see the token).
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
 __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
                                           const uint32_t sbase, uint8_t *const sgen, int &used, bool &stalled,
                                           const int s, const int len, const Cols &cm, const int pos0,
@@ -254,6 +255,11 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     if (2 * qc + 1 < ng) ab1 = __ldg(p.alibi + cm.head(2 * qc + 1)) * kLog2e;
   }
 
+  float *score_lane = nullptr;  // ACC: this lane's place in the unit's first page of scores
+  if constexpr (ACC)
+    score_lane = p.scores + ((static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * p.max_blocks * kBlock + ra) * p.score_cols +
+                 2 * qc;
+
   for (int k = 0; k < nmine; ++k) {
     const int u = u0 + k;  // this page's use of the warp's stages
     const int st = u % STAGES;
@@ -354,6 +360,18 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
       s1 = ta <= posB ? fmaf(ab1, static_cast<float>(ta - posB), (c0[1] + c1[1]) * sc1) : -INFINITY;
       s2 = tb <= posA ? fmaf(ab0, static_cast<float>(tb - posA), (c0[2] + c1[2]) * sc0) : -INFINITY;
       s3 = tb <= posB ? fmaf(ab1, static_cast<float>(tb - posB), (c0[3] + c1[3]) * sc1) : -INFINITY;
+    }
+    if constexpr (ACC) {
+      if (2 * qc < p.score_cols) {
+        float *d = score_lane + static_cast<int64_t>(page) * (kBlock * p.score_cols);
+        if (p.score_cols > 1) {
+          *reinterpret_cast<float2 *>(d) = make_float2(s0, s1);
+          *reinterpret_cast<float2 *>(d + 8 * p.score_cols) = make_float2(s2, s3);
+        } else {
+          d[0] = s0;
+          d[8] = s2;
+        }
+      }
     }
     // The running max of a head moves only when a score exceeds it by more than
     // kMaxSlack (log2 units); otherwise the page is weighted against the stale max,
@@ -543,7 +561,7 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
 // Merges the W warp states of the CTA (max / log-sum-exp rescaling) and, for every
 // (head, element) of the group, writes the normalised output (direct) or stores the
 // CTA's state (m, l, unnormalised acc) in workspace row rows(hh).
-template <int KIND, int D, int W, int STAGES, typename OutT, typename RowFn>
+template <int KIND, int D, int W, int STAGES, bool ACC, typename OutT, typename RowFn>
 __device__ __forceinline__ void write_cta_state(const DecodeParams &p, const uint8_t *sgen, const Cols &cm, int ng,
                                                 float vs, bool direct, RowFn rows) {
   using C = MmaCfg<KIND, D, W, STAGES>;
@@ -567,6 +585,9 @@ __device__ __forceinline__ void write_cta_state(const DecodeParams &p, const uin
     if (direct) {
       OutT *o = static_cast<OutT *>(p.out) + cm.out_off(p, hh) + d;
       *o = OutT(den > 0.f ? num / den * vs : 0.f);
+      if constexpr (ACC) {
+        if (d == 0) p.lse[cm.row(hh) * p.Hq + cm.head(hh)] = log_total(M, den);
+      }
     } else {
       const int64_t r = rows(hh);
       p.part_acc[r * D + d] = num;
@@ -587,7 +608,8 @@ __device__ __forceinline__ void zero_rows(const DecodeParams &p, const Cols &cm,
 // per-column causal limits and the bias.  EARLY (with PLAIN only): the early reads of
 // pa_decode_step (DecodeParams::early); a wait inside the page loop costs the other
 // variants about 1.4 us on a 30 us decode, so only this one carries it.
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY>
+// ACC (general variant only): scores stored for pa_decode_accumulate.
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
 __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
@@ -736,20 +758,20 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
       const int zlen = __ldg(p.seq_lens + z);
       bool bad = true;
       if (!dead)
-        bad = run_pages<KIND, D, W, STAGES, PLAIN, false>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
+        bad = run_pages<KIND, D, W, STAGES, PLAIN, false, false>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
                                             x - ps, y - ps, 0, false, pol, kNoWaitPage);
       const bool any_bad = __syncthreads_or(bad);
       if (any_bad) dead = __syncthreads_or(stalled) || dead;
       if (x == ps && y == pn) {
-        if (!any_bad) write_cta_state<KIND, D, W, STAGES, OutT>(p, sgen, cm, ng, vs, true, [](int) { return int64_t{0}; });
+        if (!any_bad) write_cta_state<KIND, D, W, STAGES, false, OutT>(p, sgen, cm, ng, vs, true, [](int) { return int64_t{0}; });
       } else {
         const int j = x == a ? 0 : 1;  // this CTA's first or last range
         if (!any_bad)
-          write_cta_state<KIND, D, W, STAGES, OutT>(p, sgen, cm, ng, vs, false,
+          write_cta_state<KIND, D, W, STAGES, false, OutT>(p, sgen, cm, ng, vs, false,
                                                     [&](int hh) { return (my_row * 2 + j) * 8 + hh; });
         // a CTA with an error still counts itself, so the unit's counter returns to zero
         const int c0 = owner(ps);
-        merge_if_last<OutT, D>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * z, ng, owner(pn - 1) - c0 + 1,
+        merge_if_last<OutT, D, false>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * z, ng, owner(pn - 1) - c0 + 1,
                                vs, any_bad, C::THREADS, smem_w,
                                FlatRows{static_cast<int64_t>(blockIdx.y) * p.flat + c0, range_start(c0) < ps ? 1 : 0});
       }
@@ -825,7 +847,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     wait_page = nnew <= 0 ? kNoWaitPage : max(0, len - nnew) / kBlock;
   }
 
-  const bool bad = run_pages<KIND, D, W, STAGES, PLAIN, EARLY>(p, &tmK, &tmV, sbase, sgen, used, stalled, s, len, cm, pos0, ng,
+  const bool bad = run_pages<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, &tmK, &tmV, sbase, sgen, used, stalled, s, len, cm, pos0, ng,
                                                  pb, pe, pid_reg, true, pol, wait_page);
   if (early) grid_dependency_wait();  // before any output or workspace write
   const bool any_bad = __syncthreads_or(bad);
@@ -862,11 +884,13 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   const bool direct = nparts == 1;  // this CTA holds the whole sequence: write the output
   const FixedRows rows{(static_cast<int64_t>(s) * p.Hkv + g) * p.VH + v0, p.max_parts};
   if (!any_bad)
-    write_cta_state<KIND, D, W, STAGES, OutT>(p, sgen, cm, ng, vs, direct, [&](int hh) { return rows(hh, part); });
+    write_cta_state<KIND, D, W, STAGES, ACC, OutT>(p, sgen, cm, ng, vs, direct, [&](int hh) { return rows(hh, part); });
+  else if (ACC && direct)
+    drop_lse(p, cm, ng);
   // a CTA with an error still counts itself (so the unit's counter returns to zero) and marks
   // the unit, whose merge then writes nothing
   if (!direct)
-    merge_if_last<OutT, D>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * s, ng, nparts, vs, any_bad,
+    merge_if_last<OutT, D, ACC>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * s, ng, nparts, vs, any_bad,
                            C::THREADS, smem_w, rows);
 }
 
@@ -878,31 +902,34 @@ struct MmaLaunch {
   using C = MmaCfg<KIND, D, W, ST>;
   static_assert(C::SMEM == mma_smem(KIND, D), "shape table out of sync");
 
-  template <bool PLAIN, bool EARLY>
+  template <bool PLAIN, bool EARLY, bool ACC>
   static cudaError_t attrs() {
-    auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY>;
+    auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     // same shared/L1 split as the cache write that usually precedes it (no reconfiguration)
     return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   }
-  static cudaError_t launch(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
-    const bool plain = !p.qsl && !p.alibi;
-    const bool early = plain && p.early;  // (the general variant ignores p.early: it waits first)
-    cudaError_t e = early ? attrs<true, true>() : plain ? attrs<true, false>() : attrs<false, false>();
+  template <bool PLAIN, bool EARLY, bool ACC>
+  static cudaError_t launch_variant(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                    cudaStream_t st) {
+    cudaError_t e = attrs<PLAIN, EARLY, ACC>();
     if (e != cudaSuccess) return e;
     const dim3 grid = p.flat > 0 ? dim3(p.flat, p.Hkv * p.HG, 1) : dim3(p.max_parts, p.Hkv * p.HG, p.S);
-    const dim3 block(C::THREADS);
-    e = early   ? launch_pdl(decode_mma_kernel<KIND, D, W, ST, true, true>, grid, block, C::SMEM, st, p.cluster, p, tmK, tmV)
-        : plain ? launch_pdl(decode_mma_kernel<KIND, D, W, ST, true, false>, grid, block, C::SMEM, st, p.cluster, p, tmK, tmV)
-                : launch_pdl(decode_mma_kernel<KIND, D, W, ST, false, false>, grid, block, C::SMEM, st, p.cluster, p, tmK,
-                             tmV);
+    e = launch_pdl(decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>, grid, dim3(C::THREADS), C::SMEM, st, p.cluster,
+                   p, tmK, tmV);
     return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  static cudaError_t launch(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    if (p.scores) return launch_variant<false, false, true>(p, tmK, tmV, st);
+    const bool plain = !p.qsl && !p.alibi;
+    if (!plain) return launch_variant<false, false, false>(p, tmK, tmV, st);  // (ignores p.early: it waits first)
+    return p.early ? launch_variant<true, true, false>(p, tmK, tmV, st) : launch_variant<true, false, false>(p, tmK, tmV, st);
   }
   static int occupancy() {  // 0 when it cannot be queried
     int n = 0;
-    if (attrs<false, false>() != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<KIND, D, W, ST, false, false>, C::THREADS,
+    if (attrs<false, false, false>() != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<KIND, D, W, ST, false, false, false>, C::THREADS,
                                                       C::SMEM) !=
             cudaSuccess)
       return 0;

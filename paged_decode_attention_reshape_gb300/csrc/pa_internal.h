@@ -117,7 +117,21 @@ struct DecodeParams {
   // fp32 and 4-bit paths: direct cache pointers and strides (fp32: elements; 4-bit: bytes, no s2)
   const float *kc, *vc;
   const char *k4, *v4;
+  // pa_decode_accumulate (nullable): scores [S, Hkv, HG, max_blocks * 16, score_cols], the log2
+  // of every head's softmax sum [S, Hq]; score_cols = G rounded up to 1, 2, 4 or 8.
+  float *scores, *lse;
+  int score_cols;
   int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
+};
+
+// The second kernel of pa_decode_accumulate.
+struct WeightsParams {
+  const int32_t *seq_lens;
+  const float *scores;  // [S, Hkv, HG, max_tokens, cols]
+  const float *lse;     // [S, Hq]
+  float *weights;
+  int64_t w_ss, w_hs;   // strides of weights, elements
+  int S, Hkv, G, HG, max_tokens;
 };
 
 // The query columns of one CTA: virtual heads v0 .. v0+7 of KV head g (see DecodeParams).
@@ -193,6 +207,7 @@ cudaError_t launch_decode_mma_16(const DecodeParams &p, int kind, const CUtensor
 cudaError_t launch_decode_mma_fp8(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   cudaStream_t st);  // KIND_FP8_*
 cudaError_t launch_decode_mma_fp4(const DecodeParams &p, int kind, cudaStream_t st);  // KIND_FP4_*
+cudaError_t launch_weights(const WeightsParams &p, int cols, cudaStream_t st);
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st);
 // Query-tile kernel for chunks of query tokens (pa_attention_varlen) on tcgen05 tensor
 // cores: bf16 / f16 caches, head sizes 64 and 128; never splits the page range.

@@ -52,9 +52,19 @@ struct FlatRows {
 constexpr int kUnitBad = 0x40000000;
 constexpr int kArrivalMask = kUnitBad - 1;
 
+// log2 of a column's whole softmax sum, sum_t 2^score_t = 2^M den, for pa_decode_accumulate;
+// +inf (every weight 2^(score - inf) = 0) for a column without any weight.
+__device__ __forceinline__ float log_total(float M, float den) { return den > 0.f ? M + log2f(den) : INFINITY; }
+// The same for the columns of a unit that wrote nothing after an error.
+__device__ __forceinline__ void drop_lse(const DecodeParams &p, const Cols &cm, int ng) {
+  if (threadIdx.x < static_cast<unsigned>(ng))
+    p.lse[cm.row(threadIdx.x) * p.Hq + cm.head(threadIdx.x)] = INFINITY;
+}
+
 // smem_w: shared memory for 8 * kMergeSmemParts floats, free for reuse by now.
 // rows(hh, i): workspace row of column hh in the unit's i-th part; cm maps columns to outputs.
-template <typename OutT, int D, typename Rows>
+// ACC: the columns' log2 of the softmax sum goes to p.lse.
+template <typename OutT, int D, bool ACC, typename Rows>
 __device__ __forceinline__ void merge_if_last(const DecodeParams &p, const Cols &cm, int unit, int ng, int nparts,
                                               float vs, bool bad, int threads, float *smem_w, Rows rows) {
   __shared__ int s_last;
@@ -68,10 +78,13 @@ __device__ __forceinline__ void merge_if_last(const DecodeParams &p, const Cols 
     asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.counters + unit) : "memory");
     const int last = (old & kArrivalMask) == nparts - 1;
     if (last) atomicExch(p.counters + unit, 0);
-    s_last = last && !(old & kUnitBad) && !bad;
+    s_last = !last ? 0 : (!(old & kUnitBad) && !bad) ? 1 : 2;
   }
   __syncthreads();
-  if (!s_last) return;
+  if constexpr (ACC) {
+    if (s_last == 2) drop_lse(p, cm, ng);
+  }
+  if (s_last != 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = threads >> 5;
   const bool in_smem = nparts <= kMergeSmemParts;
   for (int hh = warp; hh < ng; hh += nw) {
@@ -89,6 +102,9 @@ __device__ __forceinline__ void merge_if_last(const DecodeParams &p, const Cols 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     const float inv = den > 0.f ? vs / den : 0.f;
+    if constexpr (ACC) {
+      if (lane == 0) p.lse[cm.row(hh) * p.Hq + cm.head(hh)] = log_total(M, den);
+    }
     if (in_smem) {
       __syncwarp();
       for (int i = lane; i < nparts; i += 32) s_w[hh][i] *= inv;

@@ -109,3 +109,52 @@ def test_copy_blocks_refusals(L):
     assert copy(_t([NB, H, 16, D], pa.PA_FP4_E2M1), _t([NB, H, 16, D], pa.PA_FP4_E2M1)) == -1
     assert copy(page, _t([NB, H, 16, D], pa.PA_BF16)) == -1
     assert copy(page, _t([NB, H, 9 * D], pa.PA_FP4_E2M1, ptr=0x10008)) == -3
+
+
+def _accumulate(L, out, q, kc, vc, bt, sl, hkv, w, opt=None):
+    return L.pa_decode_accumulate(ctypes.byref(out), ctypes.byref(q), ctypes.byref(kc), ctypes.byref(vc),
+                                  ctypes.byref(bt), ctypes.byref(sl), 0.1, hkv, None if w is None else ctypes.byref(w),
+                                  None if opt is None else ctypes.byref(opt), None)
+
+
+def test_decode_and_accumulate_refusals(L):
+    S, Hq, H, D, NB, MB = 3, 8, 2, 128, 16, 4
+    q, out = _t([S, Hq, D], pa.PA_BF16), _t([S, Hq, D], pa.PA_BF16, ptr=0x20000)
+    page, bt, sl = _t([NB, H, 9 * D], pa.PA_FP4_E2M1), _t([S, MB], pa.PA_I32), _t([S], pa.PA_I32)
+    assert _decode(L, _t([S, Hq, D], pa.PA_F32), _t([S, Hq, D], pa.PA_F32), page, page, bt, sl, H) == -2
+    assert _decode(L, _t([S, Hq, 64], pa.PA_BF16), _t([S, Hq, 64], pa.PA_BF16), page, page, bt, sl, H) == -1
+    assert _decode(L, out, q, page, _t([NB, H, 16, D], pa.PA_BF16), bt, sl, H) == -1
+    assert _decode(L, out, q, _t([NB, H, 16, D], pa.PA_FP4_E2M1), page, bt, sl, H) == -1
+    assert _decode(L, out, q, page, page, bt, sl, 3) == -1
+    w = _t([S, H, MB * 16], pa.PA_F32)
+    none = pa.PaDecodeOptions()
+    assert _accumulate(L, out, q, page, page, bt, sl, H, None) == -1
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_BF16)) == -2
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16 - 1], pa.PA_F32)) == -1
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H + 1, MB * 16], pa.PA_F32)) == -1
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, ptr=0)) == -1
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, ptr=0x10002)) == -3
+    assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, strides=[999, 99, 2])) == -1
+    for P in (-2, -8, pa.PA_PARTITION_BALANCED):
+        none.partition_size = P
+        assert _accumulate(L, out, q, page, page, bt, sl, H, w, none) == -7
+    empty = _t([0, Hq, D], pa.PA_BF16)
+    assert _accumulate(L, empty, empty, page, page, _t([0, MB], pa.PA_I32), _t([0], pa.PA_I32), H,
+                       _t([0, H, MB * 16], pa.PA_F32)) == 0
+
+
+def test_accumulate_workspace_size(L):
+    size = pa.pa_decode_accumulate_workspace_size
+    # unsplit: one log-sum per (sequence, head), one score per (sequence, KV head, token, column)
+    assert size(4, 32, 8, 128, 64, -1) == size(4, 32, 8, 128, 64, 0) == 4 * 32 * 4 + 4 * 8 * 64 * 16 * 4 * 4
+    assert size(1, 3, 1, 64, 2, 0) == 256 + 2 * 16 * 4 * 4                   # 3 columns are kept as 4
+    assert size(1, 9, 1, 64, 2, 0) == 256 + 2 * 2 * 16 * 8 * 4               # 9 heads: two groups of 8
+    split = pa.pa_decode_workspace_size(4, 32, 8, 128, 64, 256)
+    assert size(4, 32, 8, 128, 64, 256) == (split + 255) // 256 * 256 + size(4, 32, 8, 128, 64, 0)
+    assert size(4, 30, 8, 128, 64, 0) == 0 and size(4, 32, 8, 128, 64, -2) == 0
+
+
+def test_plan_of_a_4_bit_cache(L):
+    assert pa.pa_decode_plan(128, 64, 8, 128, 512, pa.PA_FP4_E2M1, 152, 0) == (0, 1)
+    P, n = pa.pa_decode_plan(4, 32, 8, 128, 8192, pa.PA_FP4_E2M1, 152, 0)
+    assert P >= 1024 and P % 16 == 0 and n == -(-8192 * 16 // P)
