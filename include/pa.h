@@ -16,6 +16,7 @@
  *
  *   pa_decode_step         the cache write and the decode of one step in one call
  *   pa_decode_accumulate   the decode that also adds up every token's attention weight
+ *   pa_evict               a sequence shortened to its recent and heaviest tokens, in place
  *   pa_attention_varlen    several new query tokens per sequence, causal
  *                          ("Inside vLLM CUDA Kernels", Part 3, the varlen read path);
  *                          long chunks run on a tcgen05 query-tile kernel
@@ -344,6 +345,42 @@ size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_
                                            int max_blocks_per_seq, int partition_size);
 
 /*
+ * pa_evict -- shorten sequences to a budget of tokens, keeping the most recent ones and those
+ * of largest accumulated attention weight (pa_decode_accumulate), in place.
+ *
+ * For every sequence s with L = seq_lens[s] > budget and every KV head g: the last
+ * R = min(recent, budget) tokens stay and, of the L - R others, the budget - R of largest
+ * weights[s, g, t] (equal weights by lowest t; NaN counts below everything).  Each KV head
+ * keeps its own tokens.  They keep their order and move to positions 0 .. budget - 1 of the
+ * sequence's blocks, in this head's rows of both caches, bit for bit; what lies behind is
+ * left as it was.  A sequence of at most `budget` tokens stays as it is.
+ *
+ *   k_cache, v_cache  any cache type (as pa_reshape_and_cache); rows of at most 4096 bytes.
+ *   block_table       PA_I32 [S, max_blocks_per_seq]; the first ceil(L / 16) entries of a row
+ *   seq_lens          are used.  PA_I32 [S].
+ *   weights           PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16.  Read only.
+ *   kept              PA_I32 [S, Hkv, budget], written: the positions kept, ascending, then
+ *                     -1 where the sequence is shorter than the budget.
+ *   new_seq_lens      PA_I32 [S], written: min(L, budget).  Not the memory of seq_lens.
+ *   new_weights       PA_F32 [S, Hkv, W], written: the kept tokens' weights at their new
+ *                     positions, then zeros, ready for the next pa_decode_accumulate.  Not
+ *                     the memory of weights.
+ *   device_error      device int to OR error bits into, or NULL.
+ * Innermost strides 1, the others free (caches: the alignment of pa_reshape_and_cache).
+ * A sequence with a length or a used table entry out of range (PA_DEVERR_SEQLEN_RANGE,
+ * PA_DEVERR_BLOCK_RANGE) keeps its rows: its kept entries are all -1, its length and weights are
+ * copied as they are.
+ * Precondition (not checked): no block of a shortened sequence belongs to another sequence too
+ * (pa_bm_block_refs 1), or appears twice in its row.  Afterwards pa_bm_truncate gives the
+ * blocks behind the budget back.
+ * Keys keep the positions they were written with (rotary positions stay in the values);
+ * ALiBi and causal limits of later calls count the new positions.
+ */
+int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *block_table, const pa_tensor *seq_lens,
+             const pa_tensor *weights, int budget, int recent, pa_tensor *kept, pa_tensor *new_seq_lens,
+             pa_tensor *new_weights, int *device_error, pa_stream_t stream);
+
+/*
  * pa_attention_varlen -- paged attention for several new query tokens per sequence
  * (speculative decoding, chunked prefill): the varlen read path of "Inside vLLM CUDA
  * Kernels", Part 3 (query_start_loc packs each request's tokens, seq_lens bounds its
@@ -515,6 +552,11 @@ int pa_bm_fork(pa_block_manager *m, int src, int dst);
 /* Drop all of a sequence's references; blocks nobody references go back to the free
  * list.  The sequence is no longer live (freeing one that is not live is a no-op). */
 int pa_bm_free(pa_block_manager *m, int seq);
+
+/* Keep the first n_tokens positions of sequence `seq` (live, n_tokens <= its length): the blocks
+ * behind them lose the sequence's reference, as in pa_bm_free.  The length becomes n_tokens.
+ * PA_ERR_INVALID_ARG (nothing changed) otherwise. */
+int pa_bm_truncate(pa_block_manager *m, int seq, int64_t n_tokens);
 
 /* Block-table rows and lengths of sequences seqs[0..n-1] into host arrays: row i of
  * block_table_out (int32, row_stride >= max_blocks_per_seq entries, unused entries -1)

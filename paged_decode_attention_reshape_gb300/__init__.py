@@ -32,6 +32,7 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", 
 
 EXPORTS = ("pa_reshape_and_cache", "pa_reshape_and_cache_opt", "pa_decode", "pa_decode_ex", "pa_decode_opt",
            "pa_gather_cache", "pa_decode_accumulate", "pa_decode_accumulate_workspace_size",
+           "pa_evict", "pa_bm_truncate",
            "pa_attention_varlen", "pa_decode_step", "pa_decode_noalloc", "pa_decode_plan", "pa_decode_workspace_size", "pa_check_device_error",
            "pa_status_string", "pa_profile_enable", "pa_profile_read", "pa_bm_create", "pa_bm_destroy",
            "pa_bm_num_free", "pa_bm_block_refs", "pa_bm_seq_len", "pa_bm_append", "pa_bm_fork", "pa_bm_free",
@@ -120,6 +121,10 @@ def lib() -> ctypes.CDLL:
             L.pa_bm_fork.argtypes = [P, i32, i32]
             L.pa_bm_free.restype = i32
             L.pa_bm_free.argtypes = [P, i32]
+            L.pa_bm_truncate.restype = i32
+            L.pa_bm_truncate.argtypes = [P, i32, ctypes.c_int64]
+            L.pa_evict.restype = i32
+            L.pa_evict.argtypes = [T, T, T, T, T, i32, i32, T, T, T, P, P]
             L.pa_bm_export.restype = i32
             L.pa_bm_export.argtypes = [P, ctypes.POINTER(i32), i32, i32, ctypes.POINTER(ctypes.c_int32),
                                        ctypes.POINTER(ctypes.c_int32)]
@@ -260,6 +265,18 @@ def pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_
     """Bytes of pa_decode_accumulate's workspace; zero-fill it once before first use (torch.zeros)."""
     return int(lib().pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size,
                                                          max_blocks_per_seq, partition_size))
+
+
+def pa_evict(k_cache, v_cache, block_table, seq_lens, weights, budget: int, recent: int, kept, new_seq_lens,
+             new_weights, device_error=None, stream=None) -> None:
+    """Shorten every sequence to `budget` tokens per KV head, in place: its last `recent` ones and those of
+    largest weights (fp32 [S, Hkv, W]).  Writes kept (int32 [S, Hkv, budget] positions, -1 padding),
+    new_seq_lens (int32 [S]) and new_weights (as weights, zeros behind the kept ones)."""
+    args = (_cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens), desc(weights))
+    outs = (desc(kept), desc(new_seq_lens), desc(new_weights))
+    rc = lib().pa_evict(*[ctypes.byref(a) for a in args], int(budget), int(recent),
+                        *[ctypes.byref(a) for a in outs], _ptr(device_error), _stream(stream))
+    _check(rc, "pa_evict")
 
 
 def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_table, seq_lens, scale: float,
@@ -419,6 +436,10 @@ class BlockManager:
 
     def free(self, seq: int) -> None:
         _check(lib().pa_bm_free(self._m, int(seq)), "pa_bm_free")
+
+    def truncate(self, seq: int, n_tokens: int) -> None:
+        """Keep the first n_tokens positions of a live sequence; the blocks behind them are given back."""
+        _check(lib().pa_bm_truncate(self._m, int(seq), int(n_tokens)), "pa_bm_truncate")
 
     def export(self, seqs, row_stride: int | None = None):
         """(block_table int32 [n, row_stride], seq_lens int32 [n]) as numpy arrays."""

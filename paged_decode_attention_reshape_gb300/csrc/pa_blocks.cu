@@ -14,7 +14,8 @@
 // token appended to a shared block that is not full would change what the other
 // sequences see, so that block is first copied to a fresh one (copy on write): the
 // append reports the (source, destination) pair and the caller runs pa_copy_blocks on
-// the device before writing the token.
+// the device before writing the token.  pa_bm_truncate gives back the blocks behind a position
+// (after pa_evict).
 //
 // The manager is host code with no device state; one instance is not thread safe.
 #include <cuda_runtime.h>
@@ -131,6 +132,19 @@ PA_API int pa_bm_free(pa_block_manager *m, int seq) {
   pa_block_manager::Seq &q = m->seqs[seq];
   for (auto it = q.blocks.rbegin(); it != q.blocks.rend(); ++it) drop_ref(m, *it);
   q = pa_block_manager::Seq{};
+  return PA_OK;
+}
+
+PA_API int pa_bm_truncate(pa_block_manager *m, int seq, int64_t n_tokens) {
+  if (!seq_ok(m, seq)) return PA_ERR_INVALID_ARG;
+  pa_block_manager::Seq &q = m->seqs[seq];
+  if (!q.live || n_tokens < 0 || n_tokens > q.len) return PA_ERR_INVALID_ARG;
+  const size_t keep = static_cast<size_t>((n_tokens + kBlock - 1) / kBlock);
+  while (q.blocks.size() > keep) {
+    drop_ref(m, q.blocks.back());
+    q.blocks.pop_back();
+  }
+  q.len = n_tokens;
   return PA_OK;
 }
 

@@ -1,0 +1,330 @@
+// pa_evict.cu -- eviction from the paged cache by accumulated attention weight.
+//
+// Of every sequence s longer than the budget B and every KV head g, the last R tokens stay
+// and, of the others, the B - R of largest weight (pa_decode_accumulate's array), equal
+// weights by lowest position.  They keep their order and move to positions 0 .. B - 1 of the
+// sequence's own blocks; the blocks behind are free afterwards.  Each KV head keeps its own
+// tokens: a head's rows of a block are its own, so only the count has to agree.
+//
+// Two kernels.
+//
+// select_kernel, one CTA per (s, g): the weight of the last token to stay is found digit by
+// digit (radix select on the floats' ordered bit patterns, 11 + 11 + 10 bits: a histogram in
+// shared memory, then the digit in which the count from the top passes what is still wanted),
+// which is exact for any distribution and needs no sort; then one ordered pass writes the
+// kept positions and their weights.  The row is re-read from L2 by each pass.  Bound: 4 bytes
+// a token from HBM once.
+//
+// move_kernel, one or more CTAs per (s, g) and cache: rows p_0 < p_1 < ... move to rows
+// 0, 1, ....  p_i >= i, so in ascending order a row is only ever overwritten after it has been
+// read, and rows of a later stretch never lie where an earlier one writes: a CTA reads a stretch
+// into registers, meets at a barrier, and writes it.  Rows at the front that stay where they
+// are (p_i = i) are not touched.  CTAs of one (s, g) take different bytes of the rows.  Bound:
+// every kept row read and written once.
+#include "pa_fp4.cuh"
+#include "pa_internal.h"
+#include "pa_merge.cuh"
+#include "pa_validate.h"
+
+#define PA_API extern "C" __attribute__((visibility("default")))
+
+namespace pa {
+namespace {
+
+struct EvictParams {
+  char *cache[2];              // K, V
+  int64_t s0[2], s1[2], s2[2]; // bytes (s2 not used by 4-bit pages)
+  const int32_t *block_table;
+  int64_t bt_ss;
+  const int32_t *seq_lens;
+  const float *weights;
+  float *new_weights;
+  int64_t w_ss, w_hs, nw_ss, nw_hs;
+  int32_t *kept;
+  int64_t k_ss, k_hs;
+  int32_t *new_lens;
+  int Hkv, D, num_blocks, max_blocks, W, budget, recent;
+  int pieces, slices;          // pieces of a row; CTAs that share a row's pieces
+  int *err;
+};
+
+constexpr int kSelectThreads = 512;
+constexpr int kBins = 2048;
+
+// Bit patterns that order as the floats do (-0 as +0, NaN below everything).
+__device__ __forceinline__ uint32_t ordered_bits(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Inclusive sum over the block of one value per thread; `scratch` holds a value per warp.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *scratch, T *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  __syncthreads();  // the scratch may still be read from the scan before
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  T before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    const T t = scratch[w];
+    before += w < warp ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return before + v;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
+  __shared__ uint32_t hist[kBins];
+  __shared__ unsigned long long scratch[kSelectThreads / 32];
+  __shared__ uint32_t s_digit, s_left;
+  const int g = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+  grid_dependency_wait();
+  const int len = __ldg(p.seq_lens + s);
+  const float *w = p.weights + s * p.w_ss + g * p.w_hs;
+  float *nw = p.new_weights + s * p.nw_ss + g * p.nw_hs;
+  int32_t *kept = p.kept + s * p.k_ss + g * p.k_hs;
+  const bool len_ok = len >= 0 && len <= p.max_blocks * kBlock;
+  bool bad = !len_ok;
+  if (len_ok) {
+    const int32_t *bt = p.block_table + s * p.bt_ss;
+    for (int b = tid; b < (len + kBlock - 1) / kBlock; b += kSelectThreads) {
+      const int id = __ldg(bt + b);
+      bad |= id < 0 || id >= p.num_blocks;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && g == 0 && tid == 0 && p.err) atomicOr(p.err, len_ok ? kErrBlock : kErrSeqLen);
+  if (bad || len <= p.budget) {  // nothing to evict, or nothing that may be touched
+    for (int i = tid; i < p.budget; i += kSelectThreads) kept[i] = !bad && i < len ? i : -1;
+    for (int i = tid; i < p.W; i += kSelectThreads) nw[i] = bad || i < len ? __ldg(w + i) : 0.f;
+    if (g == 0 && tid == 0) p.new_lens[s] = len;
+    return;
+  }
+  const int tail = min(p.recent, p.budget);
+  const int cand = len - tail;             // candidates: positions 0 .. cand - 1
+  const int want = p.budget - tail;        // of which this many stay (< cand)
+  // the threshold: `prefix` holds its leading `done` bits, `left` of the candidates that share
+  // them are still wanted
+  uint32_t prefix = 0, left = want;
+  if (want > 0) {
+    int done = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
+      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < cand; i += kSelectThreads) {
+        const uint32_t u = ordered_bits(__ldg(w + i));
+        if (done == 0 || (u >> (32 - done)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+      }
+      __syncthreads();
+      // counts from the top: thread i holds bins 2047 - 4i .. 2044 - 4i
+      uint32_t c[4], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[j] = hist[kBins - 1 - 4 * tid - j];
+        sum += c[j];
+      }
+      unsigned long long total;
+      uint32_t before = static_cast<uint32_t>(block_scan<unsigned long long>(sum, scratch, &total)) - sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (before < left && left <= before + c[j]) {
+          s_digit = kBins - 1 - 4 * tid - j;
+          s_left = left - before;
+        }
+        before += c[j];
+      }
+      __syncthreads();
+      prefix = (prefix << bits) | s_digit;
+      left = s_left;
+      done += bits;
+      __syncthreads();
+    }
+  }
+  // kept candidates in order: all above the threshold, and the first `left` equal to it
+  uint32_t above = 0, equal = 0;  // so far, over the tiles before this one
+  if (want > 0) {
+    for (int t0 = 0; t0 < cand; t0 += kSelectThreads) {
+      const int t = t0 + tid;
+      const float x = t < cand ? __ldg(w + t) : 0.f;
+      const uint32_t u = ordered_bits(x);
+      const bool gt = t < cand && u > prefix, eq = t < cand && u == prefix;
+      const unsigned long long mine = (gt ? 1ull : 0ull) | (eq ? 1ull << 32 : 0ull);
+      unsigned long long total;
+      const unsigned long long incl = block_scan(mine, scratch, &total);
+      const uint32_t a = above + static_cast<uint32_t>(incl) - (gt ? 1u : 0u);
+      const uint32_t e = equal + static_cast<uint32_t>(incl >> 32) - (eq ? 1u : 0u);
+      if (gt || (eq && e < left)) {
+        const uint32_t at = a + min(e, left);
+        kept[at] = t;
+        nw[at] = x;
+      }
+      above += static_cast<uint32_t>(total);
+      equal += static_cast<uint32_t>(total >> 32);
+    }
+  }
+  for (int i = tid; i < tail; i += kSelectThreads) {
+    kept[want + i] = cand + i;
+    nw[want + i] = __ldg(w + cand + i);
+  }
+  for (int i = p.budget + tid; i < p.W; i += kSelectThreads) nw[i] = 0.f;
+  if (g == 0 && tid == 0) p.new_lens[s] = p.budget;
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 8;
+
+// V: the piece of a row that one thread moves at a time (16 bytes, or D / 16 of a 4-bit page: 8
+// pieces of a token's codes and its scales as the ninth).
+template <typename V, bool FP4>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
+  const int which = blockIdx.x / p.slices, slice = blockIdx.x - which * p.slices;
+  const int g = blockIdx.y, s = blockIdx.z;
+  grid_dependency_wait();
+  const int32_t *kept = p.kept + s * p.k_ss + g * p.k_hs;
+  if (__ldg(p.seq_lens + s) <= p.budget || __ldcg(kept) < 0) return;  // nothing moves (kept[0] < 0: a fault)
+  const int32_t *bt = p.block_table + s * p.bt_ss;
+  char *base = p.cache[which] + g * p.s1[which];
+  const int64_t s0 = p.s0[which], s2 = p.s2[which];
+  const int q0 = slice * p.pieces / p.slices, nq = (slice + 1) * p.pieces / p.slices - q0;
+  const int rows = kMoveThreads / nq;  // rows per turn
+  const int r = threadIdx.x / nq, q = q0 + threadIdx.x - r * nq;
+  const bool on = r < rows;
+  auto place = [&](int pos) {
+    const int64_t blk = __ldg(bt + pos / kBlock);
+    const int t = pos % kBlock;
+    if constexpr (FP4) {
+      const int off = q < 8 ? fp4_code_off(p.D, t, q * static_cast<int>(sizeof(V))) : fp4_scale_off(p.D, t, 0);
+      return base + blk * s0 + off;
+    } else {
+      return base + blk * s0 + t * s2 + q * 16;
+    }
+  };
+  // the first row that moves: kept[i] - i never falls
+  int lo = 0, hi = p.budget;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldcg(kept + mid) == mid) lo = mid + 1;
+    else hi = mid;
+  }
+  for (int i0 = lo; i0 < p.budget; i0 += rows * kMoveUnroll) {
+    V v[kMoveUnroll];
+#pragma unroll
+    for (int k = 0; k < kMoveUnroll; ++k) {
+      const int i = i0 + k * rows + r;
+      if (on && i < p.budget) v[k] = __ldcg(reinterpret_cast<const V *>(place(__ldcg(kept + i))));
+    }
+    __syncthreads();  // every read of the stretch is done before its first write
+#pragma unroll
+    for (int k = 0; k < kMoveUnroll; ++k) {
+      const int i = i0 + k * rows + r;
+      if (on && i < p.budget) *reinterpret_cast<V *>(place(i)) = v[k];
+    }
+  }
+}
+
+template <typename V, bool FP4>
+cudaError_t launch_move(const EvictParams &p, int S, cudaStream_t st) {
+  return launch_pdl(move_kernel<V, FP4>, dim3(2 * p.slices, p.Hkv, S), dim3(kMoveThreads), 0, st, 1, p);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *block_table, const pa_tensor *seq_lens,
+                    const pa_tensor *weights, int budget, int recent, pa_tensor *kept, pa_tensor *new_seq_lens,
+                    pa_tensor *new_weights, int *device_error, pa_stream_t stream) {
+  int r;
+  if ((r = check_desc(block_table, 2)) || (r = check_desc(seq_lens, 1)) || (r = check_desc(weights, 3)) ||
+      (r = check_desc(kept, 3)) || (r = check_desc(new_seq_lens, 1)) || (r = check_desc(new_weights, 3)))
+    return r;
+  int NB, Hkv, D;
+  if ((r = validate_cache_pair(k_cache, v_cache, &NB, &Hkv, &D))) return r;
+  if (budget < 1 || recent < 0) return PA_ERR_INVALID_ARG;
+  if (block_table->dtype != PA_I32 || seq_lens->dtype != PA_I32 || kept->dtype != PA_I32 ||
+      new_seq_lens->dtype != PA_I32 || weights->dtype != PA_F32 || new_weights->dtype != PA_F32)
+    return PA_ERR_UNSUPPORTED_DTYPE;
+  const int cdt = k_cache->dtype;
+  const bool fp4 = cdt == PA_FP4_E2M1;
+  if (cdt != PA_F32 && cdt != PA_BF16 && cdt != PA_F16 && cdt != PA_FP8_E4M3 && !fp4) return PA_ERR_UNSUPPORTED_DTYPE;
+  const int64_t S = seq_lens->shape[0], MB = block_table->shape[1], W = weights->shape[2];
+  if (block_table->shape[0] != S || weights->shape[0] != S || kept->shape[0] != S || new_seq_lens->shape[0] != S ||
+      new_weights->shape[0] != S)
+    return PA_ERR_INVALID_ARG;
+  if (weights->shape[1] != Hkv || kept->shape[1] != Hkv || new_weights->shape[1] != Hkv) return PA_ERR_INVALID_ARG;
+  if (kept->shape[2] != budget || new_weights->shape[2] != W) return PA_ERR_INVALID_ARG;
+  if (S > 65535 || MB > INT32_MAX / kBlock || W > INT32_MAX) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (W < MB * kBlock) return PA_ERR_INVALID_ARG;
+  if (block_table->stride[1] != 1 || seq_lens->stride[0] != 1 || weights->stride[2] != 1 || kept->stride[2] != 1 ||
+      new_seq_lens->stride[0] != 1 || new_weights->stride[2] != 1)
+    return PA_ERR_INVALID_ARG;
+  const int eb = elem_bytes(cdt);
+  if (!fp4 && (D <= 0 || (static_cast<int64_t>(D) * eb) % 16 || static_cast<int64_t>(D) * eb > 16 * kMoveThreads))
+    return PA_ERR_UNSUPPORTED_SHAPE;
+  if (S == 0 || Hkv == 0 || MB == 0) return PA_OK;
+  if (!block_table->data || !seq_lens->data || !weights->data || !kept->data || !new_seq_lens->data ||
+      !new_weights->data)
+    return PA_ERR_INVALID_ARG;
+  // read by every CTA of a sequence while others write the new ones
+  if (new_weights->data == weights->data || new_seq_lens->data == seq_lens->data) return PA_ERR_INVALID_ARG;
+
+  EvictParams p{};
+  const pa_tensor *c[2] = {k_cache, v_cache};
+  for (int i = 0; i < 2; ++i) {
+    p.cache[i] = static_cast<char *>(c[i]->data);
+    p.s0[i] = c[i]->stride[0] * eb;
+    p.s1[i] = c[i]->stride[1] * eb;
+    p.s2[i] = fp4 ? 0 : c[i]->stride[2] * eb;
+  }
+  p.block_table = static_cast<const int32_t *>(block_table->data);
+  p.bt_ss = block_table->stride[0];
+  p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+  p.weights = static_cast<const float *>(weights->data);
+  p.new_weights = static_cast<float *>(new_weights->data);
+  p.w_ss = weights->stride[0];
+  p.w_hs = weights->stride[1];
+  p.nw_ss = new_weights->stride[0];
+  p.nw_hs = new_weights->stride[1];
+  p.kept = static_cast<int32_t *>(kept->data);
+  p.k_ss = kept->stride[0];
+  p.k_hs = kept->stride[1];
+  p.new_lens = static_cast<int32_t *>(new_seq_lens->data);
+  p.Hkv = Hkv;
+  p.D = D;
+  p.num_blocks = NB;
+  p.max_blocks = static_cast<int>(MB);
+  p.W = static_cast<int>(W);
+  p.budget = budget;
+  p.recent = recent;
+  p.err = device_error;
+  p.pieces = fp4 ? 9 : D * eb / 16;
+  const int sm = device_sm_count();
+  if (sm <= 0) return PA_ERR_CUDA;
+  // few (sequence, head) pairs: several CTAs share their rows, down to 64 bytes of a row each
+  const int64_t units = S * Hkv * 2;
+  const int most = fp4 ? 3 : p.pieces / 4 > 0 ? p.pieces / 4 : 1;
+  p.slices = 1;
+  while (p.slices < most && units * p.slices < 2 * sm) ++p.slices;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(select_kernel, dim3(Hkv, static_cast<unsigned>(S)), dim3(kSelectThreads), 0, st, 1, p);
+  if (e == cudaSuccess) {
+    const int n = static_cast<int>(S);
+    e = !fp4 ? launch_move<uint4, false>(p, n, st)
+        : D == 64  ? launch_move<uint32_t, true>(p, n, st)
+        : D == 128 ? launch_move<uint2, true>(p, n, st)
+                   : launch_move<uint4, true>(p, n, st);
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
