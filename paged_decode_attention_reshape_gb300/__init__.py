@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -80,30 +81,32 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libpa_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
                 raise RuntimeError("libpa_gb300.so is not built (expected at %s); run "
                                    "`python -c 'import __graft_entry__ as g; g.build()'`" % LIB_PATH)
             L = ctypes.CDLL(LIB_PATH)
-            P, T = ctypes.c_void_p, ctypes.POINTER(PaTensor)
+            P = T = ctypes.c_void_p  # (T: a pa_tensor's address; see _desc)
             i32, f32 = ctypes.c_int, ctypes.c_float
             L.pa_reshape_and_cache.restype = i32
             L.pa_reshape_and_cache.argtypes = [T, T, T, T, T, i32, P, P, P, P]
             L.pa_reshape_and_cache_opt.restype = i32
-            L.pa_reshape_and_cache_opt.argtypes = [T, T, T, T, T, i32, ctypes.POINTER(PaWriteOptions), P]
+            L.pa_reshape_and_cache_opt.argtypes = [T, T, T, T, T, i32, P, P]
             L.pa_gather_cache.restype = i32
-            L.pa_gather_cache.argtypes = [T, T, T, T, T, ctypes.POINTER(PaWriteOptions), P]
+            L.pa_gather_cache.argtypes = [T, T, T, T, T, P, P]
             L.pa_decode_opt.restype = i32
-            L.pa_decode_opt.argtypes = [T, T, T, T, T, T, f32, i32, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_decode_opt.argtypes = [T, T, T, T, T, T, f32, i32, P, P]
             L.pa_decode_accumulate.restype = i32
-            L.pa_decode_accumulate.argtypes = [T, T, T, T, T, T, f32, i32, T, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_decode_accumulate.argtypes = [T, T, T, T, T, T, f32, i32, T, P, P]
             L.pa_decode_accumulate_workspace_size.restype = ctypes.c_size_t
             L.pa_decode_accumulate_workspace_size.argtypes = [i32] * 6
             L.pa_decode_step.restype = i32
-            L.pa_decode_step.argtypes = [T, T, T, T, T, T, T, T, T, T, f32, i32, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_decode_step.argtypes = [T, T, T, T, T, T, T, T, T, T, f32, i32, P, P]
             L.pa_attention_varlen.restype = i32
-            L.pa_attention_varlen.argtypes = [T, T, T, T, T, T, T, f32, i32, i32, ctypes.POINTER(PaDecodeOptions), P]
+            L.pa_attention_varlen.argtypes = [T, T, T, T, T, T, T, f32, i32, i32, P, P]
             i64p = ctypes.POINTER(ctypes.c_int64)
             L.pa_bm_create.restype = P
             L.pa_bm_create.argtypes = [i32, i32, i32]
@@ -173,19 +176,63 @@ def desc(t: torch.Tensor, dtype_code: int | None = None) -> PaTensor:
     return d
 
 
-def _cache(t: torch.Tensor) -> PaTensor:
-    """pa_tensor of a cache: a rank-3 uint8 tensor [NB, Hkv, 9 D] is a 4-bit cache's pages."""
-    return desc(t, PA_FP4_E2M1 if t.dim() == 3 and t.dtype is torch.uint8 else None)
+# A call's descriptors and options go to the library as packed bytes of the C structs (native
+# layout), whose addresses ctypes passes on: an order of magnitude less work per call than filling
+# ctypes structures element by element, which is what a small call's time is made of.
+_TENSOR = struct.Struct("@Pii10q")
+_WRITE_OPTIONS = struct.Struct("@PPqP")
+_DECODE_OPTIONS = struct.Struct("@PPqPiPNPi0P")
+_PAD = ((0,) * 5, (0,) * 4, (0,) * 3, (0,) * 2, (0,), ())  # extents behind the rank
+
+
+def _desc(t: torch.Tensor, dtype_code: int | None = None) -> bytes:
+    """The pa_tensor of a torch tensor as the struct's bytes."""
+    shape = t.shape
+    n = len(shape)
+    if n > 5:
+        raise ValueError("rank > 5")
+    pad = _PAD[n]
+    return _TENSOR.pack(t.data_ptr() if t.numel() else 0, _DT[t.dtype] if dtype_code is None else dtype_code, n,
+                        *shape, *pad, *t.stride(), *pad)
+
+
+def _cache(t: torch.Tensor) -> bytes:
+    """_desc of a cache: a rank-3 uint8 tensor [NB, Hkv, 9 D] is a 4-bit cache's pages."""
+    return _desc(t, PA_FP4_E2M1 if t.dtype is torch.uint8 and t.dim() == 3 else None)
+
+
+def _write_options(k_scale, v_scale, scale_stride, device_error) -> bytes:
+    return _WRITE_OPTIONS.pack(_addr(k_scale), _addr(v_scale), int(scale_stride), _addr(device_error))
+
+
+def _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                    first_wait_limit) -> bytes:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _DECODE_OPTIONS.pack(_addr(k_scale), _addr(v_scale), int(scale_stride), _addr(alibi_slopes),
+                                int(partition_size), _addr(workspace), ws_bytes, _addr(device_error),
+                                int(first_wait_limit))
+
+
+# The current stream's handle without a torch.cuda.Stream object around it (a third of a small
+# call's host time), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _check(rc: int, where: str):
@@ -198,8 +245,8 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, kv_dtype: i
     """Scatter key/value [T, Hkv, D] rows into k_cache/v_cache [NB, Hkv, 16, D] at slot_mapping [T] (int64).
     kv_dtype PA_KV_FP8_E4M3 (PA_KV_FP4_E2M1: into 4-bit pages) quantises with the device fp32 scales
     k_scale/v_scale (1-element tensors)."""
-    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
-    rc = lib().pa_reshape_and_cache(*[ctypes.byref(a) for a in args], int(kv_dtype), _ptr(k_scale), _ptr(v_scale),
+    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    rc = lib().pa_reshape_and_cache(*args, int(kv_dtype), _ptr(k_scale), _ptr(v_scale),
                                     _ptr(device_error), _stream(stream))
     _check(rc, "pa_reshape_and_cache")
 
@@ -210,9 +257,9 @@ def pa_reshape_and_cache_opt(key, value, k_cache, v_cache, slot_mapping, kv_dtyp
     """pa_reshape_and_cache with per-head FP8 scales: KV head h uses k_scale[h * scale_stride]
     (scale_stride 0: one scale for every head).  The cache may be a strided view (an NHD cache
     [NB, 16, Hkv, D] passed as .permute(0, 2, 1, 3))."""
-    o = PaWriteOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(device_error))
-    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
-    rc = lib().pa_reshape_and_cache_opt(*[ctypes.byref(a) for a in args], int(kv_dtype), ctypes.byref(o),
+    o = _write_options(k_scale, v_scale, scale_stride, device_error)
+    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    rc = lib().pa_reshape_and_cache_opt(*args, int(kv_dtype), o,
                                         _stream(stream))
     _check(rc, "pa_reshape_and_cache_opt")
 
@@ -222,9 +269,9 @@ def pa_gather_cache(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_
     """Rows of the cache at slot_mapping [T] (int64) back as values into key/value [T, Hkv, D]: bit copies
     from a cache of key's type, code * scale from an E4M3 or 4-bit cache (scales as
     pa_reshape_and_cache_opt).  A negative slot leaves its row as it was."""
-    o = PaWriteOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(device_error))
-    args = (desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
-    rc = lib().pa_gather_cache(*[ctypes.byref(a) for a in args], ctypes.byref(o), _stream(stream))
+    o = _write_options(k_scale, v_scale, scale_stride, device_error)
+    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    rc = lib().pa_gather_cache(*args, o, _stream(stream))
     _check(rc, "pa_gather_cache")
 
 
@@ -235,11 +282,10 @@ def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float,
     ALiBi slopes (fp32 [Hq]: logit += slope_h * (t - (seq_len - 1))), partition size, caller
     workspace (None: the library's internal one) and device error word.  first_wait_limit: poll
     limit of the first pipeline wait (0 normal, < 0 give up at once), for testing the timeout path."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
-                        _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
-    rc = lib().pa_decode_opt(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), ctypes.byref(o),
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    rc = lib().pa_decode_opt(*args, float(scale), int(num_kv_heads), o,
                              _stream(stream))
     _check(rc, "pa_decode_opt")
 
@@ -251,12 +297,11 @@ def pa_decode_accumulate(out, q, k_cache, v_cache, block_table, seq_lens, scale:
     """pa_decode_opt that also adds every cached token's attention weight, summed over the query heads of
     its KV head, to weights (fp32 [S, Hkv, W >= max blocks * 16]).  Options as pa_decode_opt (no cluster
     or balanced split); the workspace size is pa_decode_accumulate_workspace_size."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
-                        _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
-    rc = lib().pa_decode_accumulate(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads),
-                                    ctypes.byref(desc(weights)), ctypes.byref(o), _stream(stream))
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    rc = lib().pa_decode_accumulate(*args, float(scale), int(num_kv_heads),
+                                    _desc(weights), o, _stream(stream))
     _check(rc, "pa_decode_accumulate")
 
 
@@ -272,10 +317,10 @@ def pa_evict(k_cache, v_cache, block_table, seq_lens, weights, budget: int, rece
     """Shorten every sequence to `budget` tokens per KV head, in place: its last `recent` ones and those of
     largest weights (fp32 [S, Hkv, W]).  Writes kept (int32 [S, Hkv, budget] positions, -1 padding),
     new_seq_lens (int32 [S]) and new_weights (as weights, zeros behind the kept ones)."""
-    args = (_cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens), desc(weights))
-    outs = (desc(kept), desc(new_seq_lens), desc(new_weights))
-    rc = lib().pa_evict(*[ctypes.byref(a) for a in args], int(budget), int(recent),
-                        *[ctypes.byref(a) for a in outs], _ptr(device_error), _stream(stream))
+    args = (_cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens), _desc(weights))
+    outs = (_desc(kept), _desc(new_seq_lens), _desc(new_weights))
+    rc = lib().pa_evict(*args, int(budget), int(recent),
+                        *outs, _ptr(device_error), _stream(stream))
     _check(rc, "pa_evict")
 
 
@@ -288,13 +333,12 @@ def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_tab
     positions while the write runs.  new_rows_start: None (row s = sequence s's newest token)
     or int32 [S+1] (rows of sequence s, its newest tokens in order).  Options as pa_decode_opt;
     the scales also quantise the rows written to an FP8 cache."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
-                        _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    nrs = None if new_rows_start is None else ctypes.byref(desc(new_rows_start))
-    args = (desc(out), desc(q), desc(key), desc(value), _cache(k_cache), _cache(v_cache), desc(slot_mapping))
-    rc = lib().pa_decode_step(*[ctypes.byref(a) for a in args], nrs, ctypes.byref(desc(block_table)),
-                              ctypes.byref(desc(seq_lens)), float(scale), int(num_kv_heads), ctypes.byref(o),
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    nrs = None if new_rows_start is None else _desc(new_rows_start)
+    args = (_desc(out), _desc(q), _desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    rc = lib().pa_decode_step(*args, nrs, _desc(block_table),
+                              _desc(seq_lens), float(scale), int(num_kv_heads), o,
                               _stream(stream))
     _check(rc, "pa_decode_step")
 
@@ -307,13 +351,12 @@ def pa_attention_varlen(out, q, k_cache, v_cache, query_start_loc, block_table, 
     query_start_loc[s] .. query_start_loc[s+1]-1 (int32 [S+1]); query i of s sits at position
     seq_lens[s] - n_s + i and sees the tokens up to it.  Options as pa_decode_opt; the workspace
     size is pa_decode_workspace_size with num_heads = Hq * max_query_len."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    o = PaDecodeOptions(_ptr(k_scale), _ptr(v_scale), int(scale_stride), _ptr(alibi_slopes), int(partition_size),
-                        _ptr(workspace), ws_bytes, _ptr(device_error), int(first_wait_limit))
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(query_start_loc), desc(block_table),
-            desc(seq_lens))
-    rc = lib().pa_attention_varlen(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads),
-                                   int(max_query_len), ctypes.byref(o), _stream(stream))
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(query_start_loc), _desc(block_table),
+            _desc(seq_lens))
+    rc = lib().pa_attention_varlen(*args, float(scale), int(num_kv_heads),
+                                   int(max_query_len), o, _stream(stream))
     _check(rc, "pa_attention_varlen")
 
 
@@ -321,8 +364,8 @@ def pa_decode(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num
               stream=None) -> None:
     """Paged decode attention: out/q [S, Hq, D], caches [NB, Hkv, 16, D], block_table [S, maxNB] int32,
     seq_lens [S] int32."""
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
-    rc = lib().pa_decode(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _stream(stream))
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    rc = lib().pa_decode(*args, float(scale), int(num_kv_heads), _stream(stream))
     _check(rc, "pa_decode")
 
 
@@ -331,9 +374,9 @@ def pa_decode_ex(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, 
                  stream=None) -> None:
     """pa_decode with FP8 scales, explicit partition size (0 heuristic, -1 unsplit), caller workspace
     (a zero-filled uint8 CUDA tensor, see pa_decode_workspace_size) and device error word (int32)."""
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = lib().pa_decode_ex(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _ptr(k_scale),
+    rc = lib().pa_decode_ex(*args, float(scale), int(num_kv_heads), _ptr(k_scale),
                             _ptr(v_scale), int(partition_size), _ptr(workspace), ws_bytes, _ptr(device_error),
                             _stream(stream))
     _check(rc, "pa_decode_ex")
@@ -345,8 +388,8 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_table, seq_lens, scale: fl
     where they run decode.  Split-KV scratch comes from a fixed 32 MiB buffer inside the library,
     shared by all calls on a device (calls that overlap on the GPU race on it); a problem needing
     more than that raises PAError(PA_ERR_WORKSPACE)."""
-    args = (desc(out), desc(q), _cache(k_cache), _cache(v_cache), desc(block_table), desc(seq_lens))
-    rc = lib().pa_decode_noalloc(*[ctypes.byref(a) for a in args], float(scale), int(num_kv_heads), _ptr(k_scale),
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    rc = lib().pa_decode_noalloc(*args, float(scale), int(num_kv_heads), _ptr(k_scale),
                                  _ptr(v_scale), int(partition_size), _ptr(device_error), _stream(stream))
     _check(rc, "pa_decode_noalloc")
 
@@ -458,6 +501,6 @@ class BlockManager:
 def pa_copy_blocks(k_cache, v_cache, block_pairs, device_error=None, stream=None) -> None:
     """Copy whole cache blocks: for each row (src, dst) of block_pairs (int64 [n, 2] on the
     device), block src of k_cache / v_cache is copied to block dst."""
-    args = (_cache(k_cache), _cache(v_cache), desc(block_pairs))
-    rc = lib().pa_copy_blocks(*[ctypes.byref(a) for a in args], _ptr(device_error), _stream(stream))
+    args = (_cache(k_cache), _cache(v_cache), _desc(block_pairs))
+    rc = lib().pa_copy_blocks(*args, _ptr(device_error), _stream(stream))
     _check(rc, "pa_copy_blocks")
