@@ -641,6 +641,10 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   if (kind < 0) return PA_ERR_UNSUPPORTED_DTYPE;
   if (D != 64 && D != 128 && D != 256) return PA_ERR_UNSUPPORTED_SHAPE;
   if ((kind == KIND_FP8_BF16Q || kind == KIND_FP8_F16Q) && D < 128) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (mma_fp4(kind)) {  // block 0 stands in for entries behind a sequence; 32-bit block strides
+    if (NB == 0 && S64 > 0) return PA_ERR_INVALID_ARG;
+    if (k_cache->stride[0] > UINT32_MAX || v_cache->stride[0] > UINT32_MAX) return PA_ERR_UNSUPPORTED_SHAPE;
+  }
   if (S64 > 65535 || Hq64 > 65535 || block_table->shape[1] > (INT32_MAX / kBlock)) return PA_ERR_UNSUPPORTED_SHAPE;
   if (early && new_rows_start) {
     if ((r = check_desc(new_rows_start, 1))) return r;

@@ -44,11 +44,7 @@
 // head-dimension order (each lane reads 32 contiguous bytes of a row) and the
 // query uses the same permutation, which leaves q . k unchanged.
 //
-// 4-bit (E2M1) caches: the same, with bulk copies of whole pages (pa_fp4.cuh) and every
-// widened pair multiplied by its group's E4M3 scale before the tensor-core products, which is
-// exact.  A lane's K run is whole scale groups and its V run lies inside one, so a page costs
-// a lane 4 + 4 scales; per element that is half a conversion and half a product (K), and a
-// quarter of a nibble exchange more (V).
+// 4-bit (E2M1) caches have their own page loop (pa_decode_fp4.cuh) inside the same kernel.
 //
 // After the last page, each warp writes its (m, l, acc) to its own shared-memory
 // region; the CTA merges the W warp states with max/LSE rescaling and writes
@@ -92,7 +88,11 @@ struct MmaCfg {
   static constexpr int PAGEB = FP4 ? fp4_page_bytes(D) : kBlock * ROWB;  // one (block, kv head) page
   // widened caches: lane (r, c) of a fragment covers elements 128 b + QE c + [0, QE) of a row
   static constexpr int QB = D >= 128 ? D / 128 : 1, QE = D >= 128 ? 32 : D / 4;
-  static constexpr int STAGEB = 2 * PAGEB;     // K page + V page
+  static constexpr int NP = mma_stage_pages(KIND, D);  // pages of a stage
+  static constexpr int STAGEB = 2 * PAGEB * NP;         // K pages + V pages
+  // Place, among the pages of a range, of the table entry that lane `lane` of warp `warp` holds:
+  // a warp takes every W-th stage, and a lane one page of each.
+  static __device__ __forceinline__ int entry(int warp, int lane) { return NP * (warp + (lane / NP) * W) + lane % NP; }
   static constexpr int KT = D / 16;            // k-steps of Q.K^T = d-tiles of P.V
   static constexpr int THREADS = W * 32;
   static constexpr size_t SCRATCH_OFF = static_cast<size_t>(W) * STAGES * STAGEB + W * STAGES * 8;
@@ -103,6 +103,109 @@ struct MmaCfg {
   static_assert(kMmaScratch >= kLptScratchBytes, "ranking scratch");
   static_assert(kMmaScratch >= (kFlatMaxSeqs + 1) * 4, "balanced-split page offsets");
 };
+
+// The query fragments of the CTA's columns, and the score scale (log2 units) of this lane's two
+// columns 2 (lane % 4) and + 1: the softmax scale, times (widened caches) the KV head's K scale
+// over the power of two the column's query was multiplied by.
+template <typename C, int D>
+__device__ __forceinline__ void load_query(const DecodeParams &p, const Cols &cm, int ng, uint32_t (&qf)[C::KT][2],
+                                           float &sc0, float &sc1) {
+  const int lane = threadIdx.x & 31, g = cm.g;
+  const int qh = lane >> 2, qc = lane & 3;  // fragment row (head / token) and column group
+  const bool qvalid = qh < ng;
+  const char *qrow = static_cast<const char *>(p.q) + cm.q_off(p, qvalid ? qh : 0) * 2;
+  if constexpr (!C::WIDEN) {
+#pragma unroll
+    for (int j = 0; j < C::KT; ++j) {
+      const uint32_t lo = __ldg(reinterpret_cast<const uint32_t *>(qrow + (16 * j + 2 * qc) * 2));
+      const uint32_t hi = __ldg(reinterpret_cast<const uint32_t *>(qrow + (16 * j + 8 + 2 * qc) * 2));
+      qf[j][0] = qvalid ? lo : 0u;
+      qf[j][1] = qvalid ? hi : 0u;
+    }
+    sc0 = sc1 = p.scale_log2;
+  } else {
+    // lane covers d = 128 b + QE qc + [0, QE) of head qh
+    uint4 raw[C::QB][C::QE / 8];
+    float mx = 0.f;
+#pragma unroll
+    for (int b = 0; b < C::QB; ++b) {
+#pragma unroll
+      for (int i = 0; i < C::QE / 8; ++i) {
+        raw[b][i] = __ldg(reinterpret_cast<const uint4 *>(qrow + (128 * b + C::QE * qc + 8 * i) * 2));
+        const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = C::QBF16 ? unpack_bf16(w4[e]) : unpack_f16(w4[e]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int ex = 0;
+    if (mx > 0.f && mx <= 3.0e38f) {
+      frexpf(mx, &ex);  // mx = f * 2^ex, f in [0.5, 1)
+      ex -= 1;          // floor(log2 mx)
+    }
+    const int sh = max(-120, min(120, 14 - ex));
+    const float ks = p.k_scale ? __ldg(p.k_scale + g * p.scale_stride) : 1.f;  // this KV head's
+    // max |q| * sfac in [2^14, 2^15); the 4-bit loop wants sc0, sc1 >= 0 and takes a sign here
+    const float sfac = ldexpf(C::FP4 && p.scale_log2 * ks < 0.f ? -1.f : 1.f, sh);
+#pragma unroll
+    for (int b = 0; b < C::QB; ++b) {
+#pragma unroll
+      for (int i = 0; i < C::QE / 8; ++i) {
+        const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
+        // elements 8i .. 8i+7 of the lane's QE = k-steps j = 2i, 2i+1 (4 elements each)
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const float2 f0 = C::QBF16 ? unpack_bf16(w4[2 * jj]) : unpack_f16(w4[2 * jj]);
+          const float2 f1 = C::QBF16 ? unpack_bf16(w4[2 * jj + 1]) : unpack_f16(w4[2 * jj + 1]);
+          const int j = b * 8 + 2 * i + jj;
+          qf[j][0] = qvalid ? pack_f16(f0.x * sfac, f0.y * sfac) : 0u;
+          qf[j][1] = qvalid ? pack_f16(f1.x * sfac, f1.y * sfac) : 0u;
+        }
+      }
+    }
+    const float sf0 = __shfl_sync(0xffffffffu, sfac, (2 * qc) * 4);
+    const float sf1 = __shfl_sync(0xffffffffu, sfac, (2 * qc + 1) * 4);
+    sc0 = p.scale_log2 * ks / sf0;
+    sc1 = p.scale_log2 * ks / sf1;
+  }
+}
+
+// A warp's state (running max, sum, accumulator) into its own region: its stage buffers, with no
+// copies in flight.  ml[8][2], then acc[8][D].
+template <typename C, int D, int STAGES>
+__device__ __forceinline__ void store_warp_state(uint8_t *sgen, float m0, float m1, float l0, float l1,
+                                                 const float (&acc)[C::KT][4]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ra = lane >> 2, qc = lane & 3;
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+  }
+  float *wml = reinterpret_cast<float *>(sgen + warp * STAGES * C::STAGEB);
+  float *wacc = wml + 16;
+  if (ra == 0) {
+    wml[2 * (2 * qc)] = m0;
+    wml[2 * (2 * qc) + 1] = l0;
+    wml[2 * (2 * qc + 1)] = m1;
+    wml[2 * (2 * qc + 1) + 1] = l1;
+  }
+#pragma unroll
+  for (int t = 0; t < C::KT; ++t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int head = 2 * qc + (i & 1);
+      int d;
+      if constexpr (!C::WIDEN) d = 16 * t + ra + 8 * (i >> 1);
+      else if constexpr (D == 64) d = 8 * ra + 2 * t + (i >> 1);
+      else d = 128 * (t >> 3) + 16 * ra + 2 * (t & 7) + (i >> 1);
+      wacc[head * D + d] = acc[t][i];
+    }
+  }
+}
 
 // Runs pages [pb, pe) of sequence s (length len) for KV head g and the CTA's query
 // columns 0 .. ng-1 (cm; column j sees the tokens up to position pos0 + (v0 + j) / G)
@@ -115,7 +218,7 @@ struct MmaCfg {
 // on a timeout, after which the CTA must not issue into its stages again.
 // ACC: every score goes to p.scores too (log2 units; -inf where a column does not see the token).
 template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
-__device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
+__device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
                                           const uint32_t sbase, uint8_t *const sgen, int &used, bool &stalled,
                                           const int s, const int len, const Cols &cm, const int pos0,
                                           const int ng, const int pb, const int pe, int pid_reg,
@@ -153,11 +256,6 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
       const uint32_t bar = bar0 + 8 * st;
       const uint32_t kdst = stage0 + st * C::STAGEB;
       mbar_arrive_expect_tx(bar, C::STAGEB);
-      if constexpr (C::FP4) {  // a page is one contiguous run: one bulk copy each
-        bulk_load(kdst, p.k4 + pid * p.kc_s0 + g * p.kc_s1, C::PAGEB, bar, pol);
-        bulk_load(kdst + C::PAGEB, p.v4 + pid * p.vc_s0 + g * p.vc_s1, C::PAGEB, bar, pol);
-        return;
-      }
       const int c1 = p.nhd ? g : 0, c2 = p.nhd ? 0 : g;  // (token, head) or (head, token) order
 #pragma unroll
       for (int b = 0; b < C::NBOX; ++b) tma_load_4d(kdst + b * 2048, tmK, bar, b * C::BOXE, c1, c2, pid, pol);
@@ -170,70 +268,10 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
   const int npre = min(STAGES, nmine);
   for (int kk = 0; kk < npre; ++kk) issue(kk);
 
-  // ------------------------------------------------------- query fragments
-  const int qh = lane >> 2, qc = lane & 3;  // fragment row (head / token) and column group
-  const bool qvalid = qh < ng;
-  const char *qrow = static_cast<const char *>(p.q) + cm.q_off(p, qvalid ? qh : 0) * 2;
+  const int qc = lane & 3;  // fragment column group
   uint32_t qf[C::KT][2];
   float sc0, sc1;  // score scale (log2 units) of this lane's two head columns 2qc, 2qc+1
-  if constexpr (!C::WIDEN) {
-#pragma unroll
-    for (int j = 0; j < C::KT; ++j) {
-      const uint32_t lo = __ldg(reinterpret_cast<const uint32_t *>(qrow + (16 * j + 2 * qc) * 2));
-      const uint32_t hi = __ldg(reinterpret_cast<const uint32_t *>(qrow + (16 * j + 8 + 2 * qc) * 2));
-      qf[j][0] = qvalid ? lo : 0u;
-      qf[j][1] = qvalid ? hi : 0u;
-    }
-    sc0 = sc1 = p.scale_log2;
-  } else {
-    // lane covers d = 128 b + QE qc + [0, QE) of head qh
-    uint4 raw[C::QB][C::QE / 8];
-    float mx = 0.f;
-#pragma unroll
-    for (int b = 0; b < C::QB; ++b) {
-#pragma unroll
-      for (int i = 0; i < C::QE / 8; ++i) {
-        raw[b][i] = __ldg(reinterpret_cast<const uint4 *>(qrow + (128 * b + C::QE * qc + 8 * i) * 2));
-        const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = C::QBF16 ? unpack_bf16(w4[e]) : unpack_f16(w4[e]);
-          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int ex = 0;
-    if (mx > 0.f && mx <= 3.0e38f) {
-      frexpf(mx, &ex);  // mx = f * 2^ex, f in [0.5, 1)
-      ex -= 1;          // floor(log2 mx)
-    }
-    const int sh = max(-120, min(120, 14 - ex));
-    const float sfac = ldexpf(1.f, sh);  // max |q| * sfac in [2^14, 2^15)
-#pragma unroll
-    for (int b = 0; b < C::QB; ++b) {
-#pragma unroll
-      for (int i = 0; i < C::QE / 8; ++i) {
-        const uint32_t w4[4] = {raw[b][i].x, raw[b][i].y, raw[b][i].z, raw[b][i].w};
-        // elements 8i .. 8i+7 of the lane's QE = k-steps j = 2i, 2i+1 (4 elements each)
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const float2 f0 = C::QBF16 ? unpack_bf16(w4[2 * jj]) : unpack_f16(w4[2 * jj]);
-          const float2 f1 = C::QBF16 ? unpack_bf16(w4[2 * jj + 1]) : unpack_f16(w4[2 * jj + 1]);
-          const int j = b * 8 + 2 * i + jj;
-          qf[j][0] = qvalid ? pack_f16(f0.x * sfac, f0.y * sfac) : 0u;
-          qf[j][1] = qvalid ? pack_f16(f1.x * sfac, f1.y * sfac) : 0u;
-        }
-      }
-    }
-    const float ks = p.k_scale ? __ldg(p.k_scale + g * p.scale_stride) : 1.f;  // this KV head's
-    const float sf0 = __shfl_sync(0xffffffffu, sfac, (2 * qc) * 4);
-    const float sf1 = __shfl_sync(0xffffffffu, sfac, (2 * qc + 1) * 4);
-    sc0 = p.scale_log2 * ks / sf0;
-    sc1 = p.scale_log2 * ks / sf1;
-  }
-
+  load_query<C, D>(p, cm, ng, qf, sc0, sc1);
 
   // --------------------------------------------------------------- main loop
   float acc[C::KT][4];
@@ -285,33 +323,7 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
 
     // ---- scores: two accumulation chains over the k-steps
     float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (C::FP4) {
-      // lane (ra, qc) holds elements QE qc .. of tokens ra and ra + 8: whole scale groups, so
-      // each f16x2 of codes takes one product with its own token's and group's scale (exact:
-      // at most 6 significant bits, magnitudes 2^-10 .. 2688)
-#pragma unroll
-      for (int b = 0; b < C::QB; ++b) {
-        uint32_t wa[C::QE / 8], wb[C::QE / 8], sa[C::QE / 16], sb[C::QE / 16];
-        fp4_lane_codes<D>(kb, ra, b, qc, wa);
-        fp4_lane_codes<D>(kb, ra + 8, b, qc, wb);
-        fp4_lane_scales<D>(kb, ra, b, qc, sa);
-        fp4_lane_scales<D>(kb, ra + 8, b, qc, sb);
-#pragma unroll
-        for (int i = 0; i < C::QE / 8; ++i) {
-          uint32_t a0[4], a1[4];  // k-steps 2i and 2i + 1
-          e2m1x8_to_f16x2x4(wa[i], a0[0], a0[2], a1[0], a1[2]);
-          e2m1x8_to_f16x2x4(wb[i], a0[1], a0[3], a1[1], a1[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a0[e] = mul_f16x2(a0[e], (e & 1) ? sb[i >> 1] : sa[i >> 1]);
-            a1[e] = mul_f16x2(a1[e], (e & 1) ? sb[i >> 1] : sa[i >> 1]);
-          }
-          const int j = b * (C::QE / 4) + 2 * i;
-          mma_f16(c0, a0, qf[j][0], qf[j][1]);
-          mma_f16(c1, a1, qf[j + 1][0], qf[j + 1][1]);
-        }
-      }
-    } else if constexpr (!C::FP8) {
+    if constexpr (!C::FP8) {
       const int lrow = (lane & 7) | (lane & 8);
       const int lhi = lane >> 4;
 #pragma unroll
@@ -422,48 +434,7 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
     }
 
     // ---- O^T += V^T . P^T (tail rows of the last page zeroed first)
-    if constexpr (C::FP4) {
-      // lane (ra, qc) holds codes of one run of D / 8 (at most 16) elements, inside one scale
-      // group, of tokens 2qc, 2qc+1 | 2qc+8, 2qc+9.  Nibbles of two tokens are brought
-      // together so that one conversion gives the pair the product contracts over: bytes
-      // (token t0 | token t1 << 4) of the even elements, then of the odd ones.  A hidden
-      // token's scale becomes 0 (its codes are finite), so nothing stale reaches the sum.
-      constexpr int VW = D >= 128 ? 2 : 1;  // words of eight codes per token and section
-      const int t0 = 2 * qc, t1 = t0 + 1, t2 = t0 + 8, t3 = t0 + 9;
-#pragma unroll
-      for (int b = 0; b < C::QB; ++b) {
-        uint32_t w[4][VW];
-        fp4_run_codes<D>(vb, t0, b, ra, w[0]);
-        fp4_run_codes<D>(vb, t1, b, ra, w[1]);
-        fp4_run_codes<D>(vb, t2, b, ra, w[2]);
-        fp4_run_codes<D>(vb, t3, b, ra, w[3]);
-        const int sj = D == 64 ? ra >> 1 : 8 * b + ra;  // the run's scale group
-        const uint32_t z0 = t0 < nv ? lds_u8(vb + fp4_scale_off(D, t0, sj)) : 0u;
-        const uint32_t z1 = t1 < nv ? lds_u8(vb + fp4_scale_off(D, t1, sj)) : 0u;
-        const uint32_t z2 = t2 < nv ? lds_u8(vb + fp4_scale_off(D, t2, sj)) : 0u;
-        const uint32_t z3 = t3 < nv ? lds_u8(vb + fp4_scale_off(D, t3, sj)) : 0u;
-        const uint32_t s01 = e4m3x2_to_f16x2(z0 | (z1 << 8)), s23 = e4m3x2_to_f16x2(z2 | (z3 << 8));
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-          constexpr uint32_t kLow = 0x0f0f0f0fu;
-          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd elements of the word
-          const uint32_t xe = (w[0][i] & kLow) | ((w[1][i] << 4) & ~kLow), xo = ((w[0][i] >> 4) & kLow) | (w[1][i] & ~kLow);
-          const uint32_t ye = (w[2][i] & kLow) | ((w[3][i] << 4) & ~kLow), yo = ((w[2][i] >> 4) & kLow) | (w[3][i] & ~kLow);
-          e2m1x8_to_f16x2x4(xe, e01[0], e01[1], e01[2], e01[3]);
-          e2m1x8_to_f16x2x4(xo, o01[0], o01[1], o01[2], o01[3]);
-          e2m1x8_to_f16x2x4(ye, e23[0], e23[1], e23[2], e23[3]);
-          e2m1x8_to_f16x2x4(yo, o23[0], o23[1], o23[2], o23[3]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {  // fragment rows ra: element 2m of the word, ra + 8: 2m + 1
-            const uint32_t a[4] = {mul_f16x2(e01[m], s01), mul_f16x2(o01[m], s01), mul_f16x2(e23[m], s23),
-                                   mul_f16x2(o23[m], s23)};
-            const int t = b * 8 + 4 * i + m;
-            mma_f16(acc[t], a, bh0, bh1);
-            mma_f16(acc[t], a, bl0, bl1);
-          }
-        }
-      }
-    } else if constexpr (!C::FP8) {
+    if constexpr (!C::FP8) {
       const uint32_t mA = (2 * qc < nv ? 0x0000FFFFu : 0u) | (2 * qc + 1 < nv ? 0xFFFF0000u : 0u);
       const uint32_t mB = (2 * qc + 8 < nv ? 0x0000FFFFu : 0u) | (2 * qc + 9 < nv ? 0xFFFF0000u : 0u);
       const int vtok = (lane & 7) | ((lane >> 4) << 3);
@@ -528,34 +499,28 @@ __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorM
   }
   used = u0 + nmine;
 
-  // ------------------------------------------------------ merge warp states
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-  }
-  // warp region (its own stage buffers, no copies in flight): ml[8][2], then acc[8][D]
-  float *wml = reinterpret_cast<float *>(sgen + warp * STAGES * C::STAGEB);
-  float *wacc = wml + 16;
-  if (ra == 0) {
-    wml[2 * (2 * qc)] = m0;
-    wml[2 * (2 * qc) + 1] = l0;
-    wml[2 * (2 * qc + 1)] = m1;
-    wml[2 * (2 * qc + 1) + 1] = l1;
-  }
-#pragma unroll
-  for (int t = 0; t < C::KT; ++t) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int head = 2 * qc + (i & 1);
-      int d;
-      if constexpr (!C::WIDEN) d = 16 * t + ra + 8 * (i >> 1);
-      else if constexpr (D == 64) d = 8 * ra + 2 * t + (i >> 1);
-      else d = 128 * (t >> 3) + 16 * ra + 2 * (t & 7) + (i >> 1);
-      wacc[head * D + d] = acc[t][i];
-    }
-  }
+  store_warp_state<C, D, STAGES>(sgen, m0, m1, l0, l1, acc);
   return bad;
+}
+
+}  // namespace pa
+
+#include "pa_decode_fp4.cuh"  // run_pages_fp4: the same over 4-bit pages
+
+namespace pa {
+
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+__device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
+                                          const uint32_t sbase, uint8_t *const sgen, int &used, bool &stalled,
+                                          const int s, const int len, const Cols &cm, const int pos0, const int ng,
+                                          const int pb, const int pe, const int pid_reg, const bool pid_ready,
+                                          const uint64_t pol, const int wait_page) {
+  if constexpr (MmaCfg<KIND, D, W, STAGES>::FP4)
+    return run_pages_fp4<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, sbase, sgen, used, s, len, cm, pos0, ng, pb,
+                                                               pe, pid_reg, pid_ready, pol, wait_page);
+  else
+    return run_pages_tma<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, tmK, tmV, sbase, sgen, used, stalled, s, len, cm,
+                                                               pos0, ng, pb, pe, pid_reg, pid_ready, pol, wait_page);
 }
 
 // Merges the W warp states of the CTA (max / log-sum-exp rescaling) and, for every
@@ -628,14 +593,12 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   const bool flat = p.flat > 0;
   using OutT = typename std::conditional<C::QBF16, __nv_bfloat16, __half>::type;
 
-  if (lane == 0) {  // this warp's stage barriers, before any memory operation (the init fence is a release)
+  if (!C::FP4 && lane == 0) {  // this warp's stage barriers, before any memory operation (the init fence is a release)
     const uint32_t bar0 = sbase + static_cast<uint32_t>(W * STAGES * C::STAGEB + warp * STAGES * 8);
     for (int st = 0; st < STAGES; ++st) mbar_init(bar0 + 8 * st, 1);
     fence_barrier_init();
-    if constexpr (!C::FP4) {
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
-    }
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
   }
   __syncwarp();
   // Warm L2 with the metadata this launch reads on its critical path.  A prefetch
@@ -797,7 +760,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   int pid_reg = 0;  // lane i: physical block of my page i; with fixed-size partitions it is
                     // read speculatively (bounded by the table width) alongside seq_len
   if (!clustered) {
-    const int pg = part * p.pages_per_part + warp + lane * W;
+    const int pg = part * p.pages_per_part + C::entry(warp, lane);
     if (pg < p.max_blocks) pid_reg = __ldg(bt + pg);
   }
   if (len < 0 || len > p.max_blocks * kBlock) {  // (all ranks of a cluster see the same length)
@@ -827,7 +790,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   if (clustered) {
     pb = static_cast<int>(static_cast<int64_t>(part) * npages / p.cluster);
     pe = static_cast<int>(static_cast<int64_t>(part + 1) * npages / p.cluster);
-    const int pg = pb + warp + lane * W;
+    const int pg = pb + C::entry(warp, lane);
     if (pg < pe) pid_reg = __ldg(bt + pg);
   } else {
     pb = part * p.pages_per_part;

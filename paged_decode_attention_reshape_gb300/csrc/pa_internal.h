@@ -184,7 +184,7 @@ constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND
 constexpr int mma_warps(int kind, int D) { return (void)kind, D == 64 ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
-constexpr int mma_stages(int kind, int D) { return (void)D, mma_fp4(kind) ? 4 : 2; }
+constexpr int mma_stages(int kind, int D) { return (void)kind, (void)D, 2; }
 // Resident CTAs per SM the register allocation must allow (ptxas launch bound): as
 // many as the shared memory admits, so registers never cut the occupancy, except
 // for the E4M3 head-size-128 kernel (6 by shared memory; held at 4 to avoid spills).
@@ -196,9 +196,12 @@ constexpr int mma_min_ctas(int kind, int D) {
 constexpr int mma_page_bytes(int kind, int D) {
   return mma_fp4(kind) ? 9 * D : kBlock * D * (mma_fp8(kind) ? 1 : 2);
 }
+// Pages of one stage.  4-bit pages are small (1152 bytes at head size 128) and cheap to multiply,
+// so several share a stage, and with it a barrier wait, the running maximum's vote and the loop.
+constexpr int mma_stage_pages(int kind, int D) { return !mma_fp4(kind) ? 1 : D == 64 ? 4 : 2; }
 constexpr size_t kMmaScratch = 2048;  // sequence-order ranking scratch (after the barriers)
 constexpr size_t mma_smem(int kind, int D) {
-  return 1024 + static_cast<size_t>(mma_warps(kind, D)) * mma_stages(kind, D) * (2 * mma_page_bytes(kind, D) + 8) +
+  return 1024 + static_cast<size_t>(mma_warps(kind, D)) * mma_stages(kind, D) * (2 * mma_page_bytes(kind, D) * mma_stage_pages(kind, D) + 8) +
          kMmaScratch;
 }
 

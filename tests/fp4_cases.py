@@ -3,8 +3,10 @@ reference with the error bound the tests hold outputs to.
 
 Bound of one output element, with p and A = sum_t p_t |v_t| in fp64:
   half a step of the output type, relative to the value (bf16 2^-8, f16 2^-11, f16 below its
-  normal range 2^-25 absolute), plus A (2 e + 2^-17), where e bounds the error of a logit and
-  2^-17 covers the two 11-bit halves of p, the fp32 sums over tokens and the 2^x function.
+  normal range 2^-25 absolute), plus A (2 e + 2^-17 + r), where e bounds the error of a logit,
+  2^-17 covers the fp32 sums over tokens, the 2^x function and the two halves (22 bits) that p
+  is held in for an f16 query, and r = 2^-11 with a bf16 query, for which p is held in one f16:
+  half a step of f16, relative.
 The codes, their scales and the query (scaled by a power of two, f16) enter the products
 exactly; a logit is D / 16 fp32 tensor-core sums, each off by at most 2^-22 of the sum of
 magnitudes B = scale sum_d |q_d k_d|, and four fp32 roundings: e = (D / 16 + 4) 2^-22 max B
@@ -109,7 +111,7 @@ def reference(c):
                 pr[i, h, :see] = p
                 out[row + i, h] = p @ V
                 e = (c.D / 16 + 4) * 2.0 ** -22 * B.max()
-                tol[row + i, h] = p @ np.abs(V) * (2 * e + 2.0 ** -17) + 2.0 ** -25 * np.abs(V).sum(0)
+                tol[row + i, h] = p @ np.abs(V) * (2 * e + 2.0 ** -17 + (2.0 ** -11 if c.dtype == torch.bfloat16 else 0)) + 2.0 ** -25 * np.abs(V).sum(0)
         probs.append(pr)
         row += n
     tol += HALF[c.dtype] * np.abs(out) + (2.0 ** -25 if c.dtype == torch.float16 else 0)

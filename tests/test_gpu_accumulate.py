@@ -140,7 +140,7 @@ def test_faults_add_nothing(kind):
 
 
 def test_timed_out_wait_adds_nothing():
-    c, g, _ = _case("fp4", 8, 2, 64)
+    c, g, _ = _case("bf16", 8, 2, 64)
     weights = torch.zeros(c.S, 2, g.block_table.shape[1] * 16, device="cuda")
     for P in (-1, 64):
         pa.pa_decode_accumulate(*_args(c, g), weights, partition_size=P, device_error=g.err, first_wait_limit=-1)

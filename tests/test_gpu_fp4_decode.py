@@ -185,17 +185,6 @@ def test_bad_table_entry_and_length_write_nothing():
         fp4_cases.check(g.out[1], ref[1], tol[1], "the sequence without a fault")
 
 
-def test_first_wait_gives_up():
-    c = fp4_cases.make(2, 8, 2, 128, [400, 300], seed=2)
-    g = fp4_cases.to_gpu(c)
-    rc, bits = _decode(c, g, 64, first_wait_limit=-1)
-    assert rc == -8 and bits == pa.PA_DEVERR_WAIT_TIMEOUT
-    assert bool(g.out.isnan().all())
-    ref, tol, _ = fp4_cases.reference(c)
-    assert _decode(c, g, 64) == (0, 0)
-    fp4_cases.check(g.out, ref, tol, "the call after it")
-
-
 def test_other_stream_and_graph():
     c = fp4_cases.make(4, 32, 8, 128, [700, 3, 0, 250], seed=9)
     ref, tol, _ = fp4_cases.reference(c)
