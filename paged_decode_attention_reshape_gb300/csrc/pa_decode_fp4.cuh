@@ -139,11 +139,18 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
   if constexpr (ACC)
     score_lane = p.scores + ((static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * p.max_blocks * kBlock + ra) * p.score_cols +
                  2 * qc;
+  using Rows = Fp4Rows<D>;
+  using Runs = Fp4Runs<D>;
+  const int kon8 = Rows::on8(Rows::code_lane(ra, qc)), von8 = Rows::on8(Runs::code_lane(ra, qc));
+  const int vodd = Runs::odd(Runs::code_lane(ra, qc));
+  const uint32_t kcode0 = stage0 + Rows::code_lane(ra, qc), kscale0 = stage0 + Rows::scale_lane(ra, qc);
+  const uint32_t vcode0 = stage0 + NP * C::PAGEB + Runs::code_lane(ra, qc);
+  const uint32_t vscale0 = stage0 + NP * C::PAGEB + Runs::scale_lane(ra, qc);
+
   for (int k = 0; k < nmine; ++k) {
-    const int st = (u0 + k) % STAGES;
+    const uint32_t sto = (u0 + k) % STAGES * C::STAGEB;  // the stage's offset
     copy_wait<STAGES - 1>();  // this lane's copies of the stage, then the whole warp's
     __syncwarp();
-    const uint32_t kst = stage0 + st * C::STAGEB, vst = kst + NP * C::PAGEB;
     const int tok0 = (pb + NP * (warp + k * W)) * kBlock;  // the stage's first token
     const int left = end - tok0;                           // the range's tokens from there
     const bool tail = left < NP * kBlock;
@@ -152,15 +159,15 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
     float x[NP][4];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const uint32_t kb = kst + j * C::PAGEB;
+      const uint32_t ka = kcode0 + sto + j * C::PAGEB, kq = kscale0 + sto + j * C::PAGEB;
       x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
 #pragma unroll
       for (int b = 0; b < C::QB; ++b) {
         uint32_t wa[C::QE / 8], wb[C::QE / 8], sa[C::QE / 16], sb[C::QE / 16];
-        fp4_lane_codes<D>(kb, ra, b, qc, wa);
-        fp4_lane_codes<D>(kb, ra + 8, b, qc, wb);
-        fp4_lane_scales<D>(kb, ra, b, qc, sa);
-        fp4_lane_scales<D>(kb, ra + 8, b, qc, sb);
+        Rows::codes(ka, b, wa);
+        Rows::codes(ka + kon8, b, wb);
+        Rows::scales(kq, false, b, sa);
+        Rows::scales(kq, true, b, sb);
 #pragma unroll
         for (int i = 0; i < C::QE / 8; ++i) {
           uint32_t a0[4], a1[4];  // k-steps 2i and 2i + 1
@@ -277,18 +284,16 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
         bl0 = movmatrix_trans(pack_f16(x[j][0] - fa.x, x[j][1] - fa.y));
         bl1 = movmatrix_trans(pack_f16(x[j][2] - fb.x, x[j][3] - fb.y));
       }
-      const uint32_t vb = vst + j * C::PAGEB;
-      constexpr int VW = D >= 128 ? 2 : 1;  // words of eight codes per token and section
+      const uint32_t va = vcode0 + sto + j * C::PAGEB, vq = vscale0 + sto + j * C::PAGEB;
+      constexpr int VW = Runs::NW;
 #pragma unroll
       for (int b = 0; b < C::QB; ++b) {
         uint32_t w[4][VW];
-        fp4_run_codes<D>(vb, t0, b, ra, w[0]);
-        fp4_run_codes<D>(vb, t1, b, ra, w[1]);
-        fp4_run_codes<D>(vb, t2, b, ra, w[2]);
-        fp4_run_codes<D>(vb, t3, b, ra, w[3]);
-        const int sj = D == 64 ? ra >> 1 : 8 * b + ra;  // the run's scale group
-        uint32_t z01 = lds_u8(vb + fp4_scale_off(D, t0, sj)) | (lds_u8(vb + fp4_scale_off(D, t1, sj)) << 8);
-        uint32_t z23 = lds_u8(vb + fp4_scale_off(D, t2, sj)) | (lds_u8(vb + fp4_scale_off(D, t3, sj)) << 8);
+        Runs::codes(va, b, w[0]);
+        Runs::codes(va + vodd, b, w[1]);
+        Runs::codes(va + von8, b, w[2]);
+        Runs::codes(va + von8 + vodd, b, w[3]);
+        uint32_t z01 = Runs::scale_pair(vq, 0, b), z23 = Runs::scale_pair(vq, 1, b);
         if (tail) {  // zero scales for the tokens behind the end
           const int lv = left - j * kBlock;
           z01 &= (t0 < lv ? 0x00ffu : 0u) | (t1 < lv ? 0xff00u : 0u);

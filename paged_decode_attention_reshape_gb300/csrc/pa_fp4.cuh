@@ -57,45 +57,82 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Lane (r, c)'s codes of token t in section b of the page at shared address `page`: elements
-// 128 b + 32 c .. + 31 in four words (head size 64: 16 c .. + 15 in two).
+// What one lane reads of a page, from shared address `at` = the page's address plus the lane's own
+// offset.  The XOR takes its bits from lin / 128, which is t / 2 at head sizes 128 and 256 (rows of
+// 64 bytes) and t / 4 at 64 (rows of 32).  8 tokens on is 8 rows on at 128 and 256, for every
+// lane; at 64 it is 256 bytes on with bit 6 flipped.  The token after an even one, a row on, has
+// the row's bit (6 or 5) flipped.  A lane keeps those steps (`on8`, `odd`) as numbers.
+//
+// Lane (r, c) of a score fragment: elements 128 b + 32 c .. + 31 (head size 64: 16 c .. + 15)
+// of tokens r and r + 8.
 template <int D>
-__device__ __forceinline__ void fp4_lane_codes(uint32_t page, int t, int b, int c, uint32_t (&w)[D >= 128 ? 4 : 2]) {
-  if constexpr (D >= 128) {
-    const uint4 v = lds128(page + fp4_code_off(D, t, 64 * b + 16 * c));
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  } else {
-    const uint2 v = lds64(page + fp4_code_off(D, t, 8 * c));
-    w[0] = v.x;
-    w[1] = v.y;
+struct Fp4Rows {
+  static constexpr int ROWB = D >= 128 ? 64 : 32;   // code bytes of a token in a section
+  static constexpr int NW = D >= 128 ? 4 : 2;       // words of eight codes
+  static constexpr int NS = NW / 2;                 // scales
+  static __device__ __forceinline__ int code_lane(int r, int c) { return fp4_code_off(D, r, 4 * NW * c); }
+  static __device__ __forceinline__ int scale_lane(int r, int c) { return fp4_scale_off(D, r, NS * c); }
+  static __device__ __forceinline__ int on8(int code_lane) {
+    return D >= 128 ? 8 * ROWB : 256 + ((code_lane & 64) ? -64 : 64);
   }
-}
-// The scales of those elements, each in both halves of an f16x2.
+  // at: token r's, or on8 behind it token r + 8's
+  static __device__ __forceinline__ void codes(uint32_t at, int b, uint32_t (&w)[NW]) {
+    const uint32_t a = at + b * 1024;
+    if constexpr (D >= 128) {
+      const uint4 v = lds128(a);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else {
+      const uint2 v = lds64(a);
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+  }
+  // the scales of those elements, each in both halves of an f16x2
+  static __device__ __forceinline__ void scales(uint32_t at, bool second, int b, uint32_t (&s)[NS]) {
+    const uint32_t a = at + (second ? 8 * (D / 16) : 0) + b * 8;
+    if constexpr (D >= 128) {
+      const uint32_t two = e4m3x2_to_f16x2(lds_u16(a));
+      s[0] = __byte_perm(two, two, 0x1010);
+      s[1] = __byte_perm(two, two, 0x3232);
+    } else {
+      const uint32_t one = lds_u8(a);
+      s[0] = e4m3x2_to_f16x2(one | (one << 8));
+    }
+  }
+};
+
+// Lane (r, c) of a P.V fragment: run r, elements 128 b + 16 r .. + 15 (head size 64: 8 r .. + 7), of
+// tokens 2c + {0, 1, 8, 9}.
 template <int D>
-__device__ __forceinline__ void fp4_lane_scales(uint32_t page, int t, int b, int c, uint32_t (&s)[D >= 128 ? 2 : 1]) {
-  if constexpr (D >= 128) {
-    const uint32_t two = e4m3x2_to_f16x2(lds_u16(page + fp4_scale_off(D, t, 8 * b + 2 * c)));
-    s[0] = __byte_perm(two, two, 0x1010);
-    s[1] = __byte_perm(two, two, 0x3232);
-  } else {
-    const uint32_t one = lds_u8(page + fp4_scale_off(D, t, c));
-    s[0] = e4m3x2_to_f16x2(one | (one << 8));
+struct Fp4Runs {
+  static constexpr int NW = D >= 128 ? 2 : 1;       // words of eight codes
+  static __device__ __forceinline__ int code_lane(int r, int c) { return fp4_code_off(D, 2 * c, 4 * NW * r); }
+  static __device__ __forceinline__ int scale_lane(int r, int c) {
+    return fp4_scale_off(D, 2 * c, D == 64 ? r >> 1 : r);
   }
-}
-// Run r of token t in section b: elements 128 b + 16 r .. + 15 in two words (head size 64:
-// 8 r .. + 7 in one).
-template <int D>
-__device__ __forceinline__ void fp4_run_codes(uint32_t page, int t, int b, int r, uint32_t (&w)[D >= 128 ? 2 : 1]) {
-  if constexpr (D >= 128) {
-    const uint2 v = lds64(page + fp4_code_off(D, t, 64 * b + 8 * r));
-    w[0] = v.x;
-    w[1] = v.y;
-  } else {
-    w[0] = lds32(page + fp4_code_off(D, t, 4 * r));
+  static __device__ __forceinline__ int odd(int code_lane) {
+    constexpr int R = Fp4Rows<D>::ROWB;
+    return (code_lane & R) ? -R : R;
   }
-}
+  // at: token 2c's; on8 and odd behind it the others'
+  static __device__ __forceinline__ void codes(uint32_t at, int b, uint32_t (&w)[NW]) {
+    const uint32_t a = at + b * 1024;
+    if constexpr (D >= 128) {
+      const uint2 v = lds64(a);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      w[0] = lds32(a);
+    }
+  }
+  // E4M3 codes of tokens 2c + 8 i and 2c + 1 + 8 i
+  static __device__ __forceinline__ uint32_t scale_pair(uint32_t at, int i, int b) {
+    const uint32_t a = at + i * 8 * (D / 16) + b * 8;
+    return lds_u8(a) | (lds_u8(a + D / 16) << 8);
+  }
+};
 
 }  // namespace pa
