@@ -147,20 +147,19 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
   const uint32_t vcode0 = stage0 + NP * C::PAGEB + Runs::code_lane(ra, qc);
   const uint32_t vscale0 = stage0 + NP * C::PAGEB + Runs::scale_lane(ra, qc);
 
-  for (int k = 0; k < nmine; ++k) {
-    const uint32_t sto = (u0 + k) % STAGES * C::STAGEB;  // the stage's offset
-    copy_wait<STAGES - 1>();  // this lane's copies of the stage, then the whole warp's
-    __syncwarp();
+  // One stage; TAIL when the range ends inside it (a range's last stage at most): the two are
+  // compiled apart, so that the others carry no trace of the end.
+  auto step = [&](auto tail_constant, const int k) {
+    constexpr bool TAIL = decltype(tail_constant)::value;
+    const uint32_t sto = (u0 + k) % STAGES * C::STAGEB;    // the stage's offset
     const int tok0 = (pb + NP * (warp + k * W)) * kBlock;  // the stage's first token
     const int left = end - tok0;                           // the range's tokens from there
-    const bool tail = left < NP * kBlock;
 
     // ---- scores: fragment rows ra, ra + 8 = tokens, columns 2qc, 2qc + 1
     float x[NP][4];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const uint32_t ka = kcode0 + sto + j * C::PAGEB, kq = kscale0 + sto + j * C::PAGEB;
-      x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
 #pragma unroll
       for (int b = 0; b < C::QB; ++b) {
         uint32_t wa[C::QE / 8], wb[C::QE / 8], sa[C::QE / 16], sb[C::QE / 16];
@@ -179,7 +178,8 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
             a1[e] = mul_f16x2(a1[e], (e & 1) ? sb[i >> 1] : sa[i >> 1]);
           }
           const int jq = b * (C::QE / 4) + 2 * i;
-          mma_f16(x[j], a0, qf[jq][0], qf[jq][1]);
+          if (jq == 0) mma_f16_zero(x[j], a0, qf[0][0], qf[0][1]);
+          else mma_f16(x[j], a0, qf[jq][0], qf[jq][1]);
           mma_f16(x[j], a1, qf[jq + 1][0], qf[jq + 1][1]);
         }
       }
@@ -187,7 +187,7 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
     // PLAIN keeps the raw sums (sc0, sc1 are never negative, so the largest stays the largest)
     // and scales them inside the exponent's FMA; else scores become log2 units here.
     if constexpr (PLAIN) {
-      if (tail) {
+      if constexpr (TAIL) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           if (j * kBlock + ra >= left) x[j][0] = x[j][1] = -INFINITY;
@@ -208,14 +208,15 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
       if (2 * qc < p.score_cols) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          if (j * kBlock >= left) break;
+          if (TAIL && j * kBlock >= left) break;
+          const float f0 = PLAIN ? sc0 : 1.f, f1 = PLAIN ? sc1 : 1.f;
           float *d = score_lane + static_cast<int64_t>(tok0 + j * kBlock) * p.score_cols;
           if (p.score_cols > 1) {
-            *reinterpret_cast<float2 *>(d) = make_float2(x[j][0], x[j][1]);
-            *reinterpret_cast<float2 *>(d + 8 * p.score_cols) = make_float2(x[j][2], x[j][3]);
+            *reinterpret_cast<float2 *>(d) = make_float2(x[j][0] * f0, x[j][1] * f1);
+            *reinterpret_cast<float2 *>(d + 8 * p.score_cols) = make_float2(x[j][2] * f0, x[j][3] * f1);
           } else {
-            d[0] = x[j][0];
-            d[8] = x[j][2];
+            d[0] = x[j][0] * f0;
+            d[8] = x[j][2] * f0;
           }
         }
       }
@@ -260,18 +261,15 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
         else x[j][i] = ex2(x[j][i] - m);
       }
     }
-    if constexpr (PLAIN) {
-      if (tail) {  // (a zero scale times the -inf above is no number)
+    if constexpr (PLAIN && TAIL) {  // (a zero scale times the -inf above is no number)
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          if (j * kBlock + ra >= left) x[j][0] = x[j][1] = 0.f;
-          if (j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = 0.f;
-        }
+      for (int j = 0; j < NP; ++j) {
+        if (j * kBlock + ra >= left) x[j][0] = x[j][1] = 0.f;
+        if (j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = 0.f;
       }
     }
 
     // ---- O^T += V^T . P^T
-    const int t0 = 2 * qc, t1 = t0 + 1, t2 = t0 + 8, t3 = t0 + 9;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       l0 += x[j][0] + x[j][2];
@@ -294,10 +292,10 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
         Runs::codes(va + von8, b, w[2]);
         Runs::codes(va + von8 + vodd, b, w[3]);
         uint32_t z01 = Runs::scale_pair(vq, 0, b), z23 = Runs::scale_pair(vq, 1, b);
-        if (tail) {  // zero scales for the tokens behind the end
-          const int lv = left - j * kBlock;
-          z01 &= (t0 < lv ? 0x00ffu : 0u) | (t1 < lv ? 0xff00u : 0u);
-          z23 &= (t2 < lv ? 0x00ffu : 0u) | (t3 < lv ? 0xff00u : 0u);
+        if constexpr (TAIL) {  // zero scales for the tokens behind the end
+          const int lv = left - j * kBlock - 2 * qc;  // of tokens 2qc, + 1, + 8, + 9
+          z01 &= (lv > 0 ? 0x00ffu : 0u) | (lv > 1 ? 0xff00u : 0u);
+          z23 &= (lv > 8 ? 0x00ffu : 0u) | (lv > 9 ? 0xff00u : 0u);
         }
         const uint32_t s01 = e4m3x2_to_f16x2(z01), s23 = e4m3x2_to_f16x2(z23);
 #pragma unroll
@@ -320,6 +318,13 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
       }
     }
 
+  };
+
+  for (int k = 0; k < nmine; ++k) {
+    copy_wait<STAGES - 1>();  // this lane's copies of the stage, then the whole warp's
+    __syncwarp();
+    if (end - (pb + NP * (warp + k * W)) * kBlock >= NP * kBlock) step(std::false_type{}, k);
+    else step(std::true_type{}, k);
     __syncwarp();  // every lane has read the stage
     if (k + STAGES < nmine) issue(k + STAGES);
     else copy_commit();

@@ -55,10 +55,11 @@
 //
 // The kernel is launched as a programmatic dependent of the previous grid on the
 // stream: it waits for that grid before its first global read, so its launch
-// overlaps the previous kernel's tail.  Four variants per shape: the general one
-// (several query tokens, ALiBi), the same storing its scores (pa_decode_accumulate), PLAIN (one query token, no ALiBi: one compare per score
+// overlaps the previous kernel's tail.  Five variants per shape: the general one
+// (several query tokens, ALiBi), PLAIN (one query token, no ALiBi: one compare per score
 // for the page tail), and PLAIN + EARLY for pa_decode_step's multi-row steps, which reads
-// everything but the pages with new positions before that wait.
+// everything but the pages with new positions before that wait; and the first two storing
+// their scores (pa_decode_accumulate).
 #pragma once
 
 #include "pa_device.cuh"
@@ -573,7 +574,7 @@ __device__ __forceinline__ void zero_rows(const DecodeParams &p, const Cols &cm,
 // per-column causal limits and the bias.  EARLY (with PLAIN only): the early reads of
 // pa_decode_step (DecodeParams::early); a wait inside the page loop costs the other
 // variants about 1.4 us on a 30 us decode, so only this one carries it.
-// ACC (general variant only): scores stored for pa_decode_accumulate.
+// ACC: scores stored for pa_decode_accumulate.
 template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
 __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
@@ -884,8 +885,9 @@ struct MmaLaunch {
     return e != cudaSuccess ? e : cudaGetLastError();
   }
   static cudaError_t launch(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
-    if (p.scores) return launch_variant<false, false, true>(p, tmK, tmV, st);
     const bool plain = !p.qsl && !p.alibi;
+    if (p.scores) return plain ? launch_variant<true, false, true>(p, tmK, tmV, st)
+                               : launch_variant<false, false, true>(p, tmK, tmV, st);
     if (!plain) return launch_variant<false, false, false>(p, tmK, tmV, st);  // (ignores p.early: it waits first)
     return p.early ? launch_variant<true, true, false>(p, tmK, tmV, st) : launch_variant<true, false, false>(p, tmK, tmV, st);
   }
