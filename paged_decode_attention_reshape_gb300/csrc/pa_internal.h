@@ -181,7 +181,7 @@ constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND
 // page math, 2 to 4 stages alike), so the warps per CTA set how fast one long
 // sequence streams.  Head size 64: 8 warps (3 CTAs per SM); 128 and 256: 4 warps,
 // whose larger pages already fill HBM with 3 CTAs per SM.
-constexpr int mma_warps(int kind, int D) { return (void)kind, D == 64 ? 8 : 4; }
+constexpr int mma_warps(int kind, int D) { return D == 64 || (mma_fp4(kind) && D == 128) ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
 constexpr int mma_stages(int kind, int D) { return (void)kind, (void)D, 2; }
@@ -190,7 +190,7 @@ constexpr int mma_stages(int kind, int D) { return (void)kind, (void)D, 2; }
 // for the E4M3 head-size-128 kernel (6 by shared memory; held at 4 to avoid spills).
 constexpr bool mma_fp8(int kind) { return kind == KIND_FP8_BF16Q || kind == KIND_FP8_F16Q; }
 constexpr int mma_min_ctas(int kind, int D) {
-  if (mma_fp4(kind)) return D == 64 ? 2 : D == 128 ? 4 : 3;
+  if (mma_fp4(kind)) return D == 256 ? 3 : 2;
   return D == 64 ? 3 : D == 128 ? (mma_fp8(kind) ? 4 : 3) : (mma_fp8(kind) ? 3 : 1);
 }
 constexpr int mma_page_bytes(int kind, int D) {

@@ -185,11 +185,13 @@ __device__ __forceinline__ int lpt_sequence(const int32_t *seq_lens, int S, int 
   int(*s_rank)[kLptMax] = reinterpret_cast<int(*)[kLptMax]>(smem_rank);
   __shared__ int s_pick;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = threads >> 5;
+  // one key per sequence that orders as (longest first, then by index): unique, so the ranks are a
+  // permutation (lengths past 2^24 - 1 tie, and an invalid one counts as empty)
   int L[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int i = lane + 32 * k;
-    L[k] = i < S ? __ldg(seq_lens + i) : INT_MIN;
+    L[k] = i < S ? (min(max(__ldg(seq_lens + i), 0), 0xffffff) << 7) | (127 - i) : -1;
   }
   // warp w counts, for every i, the j in its 32-block(s) that come before i in the order
   for (int jb = warp; jb < 4; jb += nw) {
@@ -199,9 +201,8 @@ __device__ __forceinline__ int lpt_sequence(const int32_t *seq_lens, int S, int 
 #pragma unroll 8
       for (int jj = 0; jj < 32; ++jj) {
         const int Lj = __shfl_sync(0xffffffffu, Lb, jj);
-        const int j = jb * 32 + jj;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) rk[k] += (Lj > L[k]) | ((Lj == L[k]) & (j < lane + 32 * k));
+        for (int k = 0; k < 4; ++k) rk[k] += Lj > L[k];
       }
     }
 #pragma unroll
