@@ -258,7 +258,9 @@ int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, cons
  *                     ranges over one resident wave of CTAs per (kv head, head group),
  *                     the parts of a cut sequence merged through the workspace
  *                     (batches of at most 511 sequences, else
- *                     PA_ERR_UNSUPPORTED_SHAPE; the fp32 cache runs it unsplit).
+ *                     PA_ERR_UNSUPPORTED_SHAPE; the fp32 cache runs it unsplit; over a
+ *                     4-bit cache the ranges belong to single warps where the batch has
+ *                     many (sequence, KV head) pairs, and 0 chooses this split too).
  *   workspace,        device memory for split-KV partition states; at least
  *   workspace_bytes   pa_decode_workspace_size(...) bytes for the partition size
  *                     the call ends up using (0 bytes when it does not split or
@@ -326,9 +328,10 @@ int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, 
  *                    every sequence s, KV head g and token t < seq_lens[s], weights[s, g, t]
  *                    grows by the sum over the Hq / Hkv query heads of g of their softmax
  *                    weight of t (so by Hq / Hkv over the whole row).  Other entries are not
- *                    touched.  A sequence that sets an error bit adds nothing.
- *   other arguments  as pa_decode_opt, and the same outputs.  partition_size: 0, -1 or > 0
- *                    (the cluster and balanced splits give PA_ERR_UNSUPPORTED_SHAPE).  The
+ *                    touched.  A sequence that sets an error bit adds nothing, nor does a head
+ *                    whose softmax sum is not a positive number.
+ *   other arguments  as pa_decode_opt, and the same outputs.  partition_size: 0, -1, > 0 or
+ *                    PA_PARTITION_BALANCED (the cluster splits give PA_ERR_UNSUPPORTED_SHAPE).  The
  *                    workspace (pa_decode_accumulate_workspace_size bytes, used by every
  *                    call, split or not) holds one fp32 score per (query head, token):
  *                    4 bytes against the 2 head_size * (element bytes) of a token's K and V.

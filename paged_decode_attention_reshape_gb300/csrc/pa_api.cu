@@ -201,7 +201,10 @@ int plan_partition(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, b
     const int64_t slots = static_cast<int64_t>(std::max(sm, 1)) * ctas_per_sm(kind, D, device);
     if ((longest_first(kind, S) && units >= slots) || units >= 2 * slots) return 0;
     const int64_t work = units * std::max(1, maxNB / 2);  // pages, assuming half-full tables
-    const int64_t pages = std::max<int64_t>(work / (2 * slots), 64);
+    // 4-bit pages take less time each, so a CTA's fixed time weighs more against them: one wave of
+    // partitions over full tables, and half the smallest size (1 x 8k tokens: 10.4 us against 11.6)
+    const int64_t pages = mma_fp4(kind) ? std::max<int64_t>(units * maxNB / slots, 32)
+                                        : std::max<int64_t>(work / (2 * slots), 64);
     if (pages >= maxNB) return 0;
     P = static_cast<int>(pages * kBlock);
   }
@@ -221,19 +224,52 @@ int plan_partition(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, b
 struct Plan {
   int P;        // tokens per fixed partition (0 = none)
   int cluster;  // parts per unit of the cluster split (0 = none)
-  int flat;     // CTAs per head row of the balanced split (0 = none)
+  int flat;     // CTAs (with `warps`: warps) per head row of the balanced split (0 = none)
   int status;
+  int warps;    // 1: the balanced split over warps (4-bit caches)
 };
 int balanced_ctas(int Hq, int Hkv, int D, int kind, int sm, bool device) {
   const int64_t rows = static_cast<int64_t>(Hkv) * ((Hq / Hkv + 7) / 8);
   const int64_t slots = static_cast<int64_t>(std::max(sm, 1)) * ctas_per_sm(kind, D, device);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(slots / rows, 65535)));
 }
-Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, int request) {
-  Plan pl{0, 0, 0, PA_OK};
+// 4-bit caches, one query token and no ALiBi (`plain`): the balanced split over warps
+// (pa_decode_fp4_warps.cuh) where the batch has at least two (sequence, kv head, head group) units
+// for every three warps of a resident wave (on request: one for eight), and the balanced split over
+// CTAs where there are too few units for the CTAs and a CTA still gets 128 pages or more; else whole
+// units or fixed partitions.  Measured on GB300 (2432 warps, 304 CTAs; us over warps / unsplit or
+// over CTAs / fixed partitions): 304 x 256 tokens, 2432 units, 21.6 / 41.5 / -; 256 x 512..4096,
+// 2048 units, 124.0 / 139.3 / -; 128 x 1k..8k, 1024 units, 124.3 / 121.6 / -; 64 x 0..2048, 512
+// units, 26.4 / 18.5 / - (the parts of cut units cost more than the waves); 16 x 4k..32k, 128
+// units, - / 66.8 / 87.3; 4 x 32k..128k, 32 units, - / 73.1 / 92.7; 1 x 8k, 8 units, - / 17.2 / 10.4.
+bool plan_fp4(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, bool varlen, bool plain,
+              bool balanced, Plan *pl) {
+  const int64_t rows = static_cast<int64_t>(Hkv) * ((Hq / Hkv + 7) / 8), units = S * rows;
+  const int64_t ctas = static_cast<int64_t>(std::max(sm, 1)) * mma_min_ctas(kind, D);
+  const int64_t workers = ctas * mma_warps(kind, D);
+  if (S > kFlatMaxSeqs || varlen) return false;
+  if (plain && (balanced ? units * 8 >= workers : units * 3 >= workers * 2) && rows <= ctas) {
+    pl->warps = 1;
+    pl->flat = static_cast<int>(ctas / rows) * mma_warps(kind, D);
+    return true;
+  }
+  const int64_t slots = static_cast<int64_t>(std::max(sm, 1)) * ctas_per_sm(kind, D, device);
+  if (!balanced && units * (maxNB / 2) < 128 * slots) return false;
+  if (units >= slots) return false;  // (not `plain`: whole units fill the slots)
+  pl->flat = balanced_ctas(Hq, Hkv, D, kind, sm, device);
+  return true;
+}
+// varlen: several query tokens; plain: one, and no ALiBi
+Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, int request,
+               bool varlen = false, bool plain = true) {
+  Plan pl{0, 0, 0, PA_OK, 0};
+  if (mma_fp4(kind) && request == 0 &&
+      plan_fp4(S, Hq, Hkv, D, maxNB, kind, sm, device, varlen, plain, false, &pl))
+    return pl;
   if (request == PA_PARTITION_BALANCED) {
     if (kind == KIND_F32) return pl;  // the CUDA-core kernel runs it unsplit
     if (S > kFlatMaxSeqs) pl.status = PA_ERR_UNSUPPORTED_SHAPE;
+    else if (mma_fp4(kind) && plan_fp4(S, Hq, Hkv, D, maxNB, kind, sm, device, varlen, plain, true, &pl)) return pl;
     else pl.flat = balanced_ctas(Hq, Hkv, D, kind, sm, device);
     return pl;
   }
@@ -574,10 +610,17 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
     // quantised kernels admit the most CTAs per SM
     const int sm = device_sm_count();
     if (sm <= 0 || num_seqs > kFlatMaxSeqs) return 0;
-    const int kind = head_size >= 128 ? KIND_FP8_BF16Q : KIND_BF16;
-    const int flat = std::max(balanced_ctas(num_heads, num_kv_heads, head_size, kind, sm, false),
-                              balanced_ctas(num_heads, num_kv_heads, head_size, KIND_FP4_BF16Q, sm, false));
-    return workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, 0, flat).total;
+    const int kind = head_size >= 128 ? KIND_FP8_BF16Q : KIND_BF16, kind4 = KIND_FP4_BF16Q;
+    int flat = std::max(balanced_ctas(num_heads, num_kv_heads, head_size, kind, sm, false),
+                        balanced_ctas(num_heads, num_kv_heads, head_size, kind4, sm, false));
+    // 4-bit caches: split over warps, or (ALiBi, several query tokens) into fixed partitions
+    Plan pl{0, 0, 0, PA_OK, 0};
+    if (plan_fp4(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, kind4, sm, false, false, true, true,
+                 &pl))
+      flat = std::max(flat, pl.flat);
+    const int P = plan_partition(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, kind4, sm, true, 0);
+    return std::max(workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, 0, flat).total,
+                    workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, P, 0).total);
   }
   const int P = partition_size > 0 ? (partition_size + kBlock - 1) / kBlock * kBlock : 0;
   if (P >= max_blocks_per_seq * kBlock) return 0;
@@ -587,7 +630,7 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
 PA_API size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                                   int max_blocks_per_seq, int partition_size) {
   if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_size < 0 ||
-      max_blocks_per_seq < 0 || partition_size < -1)
+      max_blocks_per_seq < 0 || (partition_size < -1 && partition_size != PA_PARTITION_BALANCED))
     return 0;
   return round256(pa_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,
                                            partition_size)) +
@@ -658,7 +701,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     if (weights->shape[0] != S64 || weights->shape[1] != Hkv || weights->shape[2] < block_table->shape[1] * kBlock ||
         weights->stride[2] != 1)
       return PA_ERR_INVALID_ARG;
-    if (o.partition_size < -1) return PA_ERR_UNSUPPORTED_SHAPE;  // cluster and balanced splits
+    if (o.partition_size < -1 && o.partition_size != PA_PARTITION_BALANCED)
+      return PA_ERR_UNSUPPORTED_SHAPE;  // cluster splits
   }
   if (S64 == 0 || q->shape[0] == 0) return PA_OK;
   if (weights && block_table->shape[1] > 0 && !weights->data) return PA_ERR_INVALID_ARG;
@@ -681,7 +725,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   // shared by 64 rows, no split) unless a split was asked for.
   const bool chunk = varlen && (kind == KIND_BF16 || kind == KIND_F16) && (D == 64 || D == 128) &&
                      (partition_size == 0 || partition_size == -1) && VH >= chunk_min_columns(D);
-  const Plan pl = make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size);
+  const Plan pl = make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,
+                            !varlen && !o.alibi_slopes);
   if (pl.status != PA_OK) return pl.status;
   const int P = pl.P;
   const int max_parts = pl.cluster > 1 ? pl.cluster : P > 0 ? (maxNB * kBlock + P - 1) / P : 1;
@@ -791,7 +836,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     p.vc_s0 = v_cache->stride[0];
     p.vc_s1 = v_cache->stride[1];
     ProfScope ps(PA_KERNEL_DECODE, st);
-    e = launch_decode_mma_fp4(p, kind, st);
+    e = pl.warps ? launch_decode_fp4_warps(p, kind, sm * mma_min_ctas(kind, D), st) : launch_decode_mma_fp4(p, kind, st);
   } else {
     CUtensorMap tmK, tmV;
     int nhd_k = 0, nhd_v = 0;

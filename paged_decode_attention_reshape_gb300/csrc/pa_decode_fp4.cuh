@@ -22,8 +22,8 @@
 //      2^kLift below the largest score, so p reaches 2^15 (f16 holds 65504) and the smallest p
 //      an f16 tells from zero is 2^-24 of 2^7, not of 1.
 //   P: f16.  With an f16 query in two halves (22 bits; the second product adds the rest).  With a
-//      bf16 query in one, 11 bits: each p is off by at most 2^-12 of itself, with random sign
-//      over the tokens, an eighth of the 2^-9 of rounding the output to bf16.
+//      bf16 query in one, 11 bits: each p is off by at most 2^-11 of itself, with a sign that
+//      varies over the tokens, against the 2^-8 of rounding the output to bf16.
 //
 // Tokens behind the end exist only in a range's last stage, which takes a branch of its own:
 // scores -inf, p = 0 and V scales 0 (codes are always finite), so nothing stale is summed.
@@ -34,65 +34,29 @@ namespace pa {
 constexpr float kLift = 7.f;       // log2 units the running maximum is kept below the scores'
 constexpr float kFp4Slack = 15.f;  // p <= 2^15
 
-// Runs pages [pb, pe) of sequence s; arguments and result as run_pages_tma (there is no wait here
-// that could give up).
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
-__device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint32_t sbase, uint8_t *const sgen,
-                                              int &used, const int s, const int len, const Cols &cm,
-                                              const int pos0, const int ng, const int pb, const int pe, int entry,
-                                              const bool entry_ready, const uint64_t pol, const int wait_page) {
-  using C = MmaCfg<KIND, D, W, STAGES>;
-  constexpr int NP = C::NP;
-  constexpr int PER = 32 / NP;  // stages whose table entries the warp's lanes hold at a time
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ra = lane >> 2, qc = lane & 3;
-  const int32_t *bt = p.block_table + static_cast<int64_t>(s) * p.bt_ss + pb;
-  const int n = pe - pb;                                      // pages of the range
-  const int nst = (n + NP - 1) / NP;                          // its stages, every W-th one this warp's
-  const int nmine = nst > warp ? (nst - warp + W - 1) / W : 0;
-  const uint32_t stage0 = sbase + static_cast<uint32_t>(warp * STAGES * C::STAGEB);
-  const int u0 = used;
-  bool bad = false, waited = false;
-
-  // Table entries, one page of the warp's next PER stages per lane.  An entry behind the range reads
-  // as block 0, and so does a bad one (the CTA then writes nothing), so every copy has a source.
-  auto check_entries = [&](int k) {
-    const bool in = C::entry(warp, lane) + k * NP * W < n;
-    const bool out = in && (entry < 0 || entry >= p.num_blocks);
-    if (out && p.err) atomicOr(p.err, kErrBlock);
-    if (out || !in) entry = 0;
-    bad |= __any_sync(0xffffffffu, out);
-  };
-  // This lane's share of the copies: 16 bytes of every 512 of a page's codes, and 16 bytes of the
-  // scales of one of the stage's pages (K pages first, as they lie in the stage).
-  constexpr int CODEB = 8 * D;                      // code bytes of a page: whole runs of 512
-  constexpr int SL = D / 16;                        // lanes for a page's scales
-  constexpr int SPAGES = 32 / SL;                   // pages whose scales one copy takes
-  constexpr int SRUNS = 2 * NP / SPAGES;            // copies for a stage's scales
-  static_assert(CODEB % 512 == 0 && SRUNS * SPAGES == 2 * NP && (NP % SPAGES == 0 || SRUNS == 1), "copy shares");
-  const char *const kbase = p.k4 + cm.g * p.kc_s1, *const vbase = p.v4 + cm.g * p.vc_s1;
-  const char *const kcode = kbase + lane * 16, *const vcode = vbase + lane * 16;
-  const uint32_t ks0 = static_cast<uint32_t>(p.kc_s0), vs0 = static_cast<uint32_t>(p.vc_s0);  // (below 2^32)
-  auto issue = [&](int k) {  // whole warp; k increases by one per call
-    if constexpr (EARLY) {
-      if (!waited && pb + NP * (warp + k * W) + NP > wait_page) {  // a page that may hold new positions
-        grid_dependency_wait();
-        waited = true;
-      }
-    }
-    const int at = k % PER;
-    if (at == 0) {
-      if (k > 0 || !entry_ready) {
-        const int i = C::entry(warp, lane) + k * NP * W;
-        entry = i < n ? __ldg(bt + i) : 0;
-      }
-      check_entries(k);
-    }
-    const uint32_t dst = stage0 + (u0 + k) % STAGES * C::STAGEB;
+// A lane's share of a stage's copies: 16 bytes of every 512 of a page's codes, and 16 bytes of the
+// scales of one of the stage's pages (K pages first, as they lie in the stage).
+template <typename C, int D>
+struct Fp4Copies {
+  static constexpr int NP = C::NP;
+  static constexpr int CODEB = 8 * D;                // code bytes of a page: whole runs of 512
+  static constexpr int SL = D / 16;                  // lanes for a page's scales
+  static constexpr int SPAGES = 32 / SL;             // pages whose scales one copy takes
+  static constexpr int SRUNS = 2 * NP / SPAGES;      // copies for a stage's scales
+  static_assert(CODEB % 512 == 0 && SRUNS * SPAGES == 2 * NP, "copy shares");
+  const char *kbase, *vbase;
+  uint32_t ks0, vs0;  // block strides (below 2^32)
+  int lane;
+  __device__ __forceinline__ Fp4Copies(const DecodeParams &p, int g, int lane_)
+      : kbase(p.k4 + g * p.kc_s1), vbase(p.v4 + g * p.vc_s1), ks0(static_cast<uint32_t>(p.kc_s0)),
+        vs0(static_cast<uint32_t>(p.vc_s0)), lane(lane_) {}
+  // Whole warp: the stage at shared address dst, its pages' blocks in lanes at .. at + NP - 1 of entry.
+  __device__ __forceinline__ void stage(uint32_t dst, int entry, int at, uint64_t pol) const {
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const uint32_t blk = static_cast<uint32_t>(__shfl_sync(0xffffffffu, entry, at * NP + j));
-      const char *ks = kcode + static_cast<uint64_t>(blk) * ks0, *vs = vcode + static_cast<uint64_t>(blk) * vs0;
+      const uint32_t blk = static_cast<uint32_t>(__shfl_sync(0xffffffffu, entry, at + j));
+      const char *ks = kbase + lane * 16 + static_cast<uint64_t>(blk) * ks0;
+      const char *vs = vbase + lane * 16 + static_cast<uint64_t>(blk) * vs0;
 #pragma unroll
       for (int i = 0; i < CODEB / 512; ++i) {
         copy16_async(dst + j * C::PAGEB + i * 512 + lane * 16, ks + i * 512, pol);
@@ -102,59 +66,74 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
 #pragma unroll
     for (int i = 0; i < SRUNS; ++i) {
       const int pg = i * SPAGES + lane / SL;  // page of the stage: K 0 .. NP - 1, V 0 .. NP - 1
-      const uint32_t blk = static_cast<uint32_t>(__shfl_sync(0xffffffffu, entry, at * NP + pg % NP));
+      const uint32_t blk = static_cast<uint32_t>(__shfl_sync(0xffffffffu, entry, at + pg % NP));
       const char *src = (pg < NP ? kbase : vbase) + static_cast<uint64_t>(blk) * (pg < NP ? ks0 : vs0);
       copy16_async(dst + pg * C::PAGEB + CODEB + (lane % SL) * 16, src + CODEB + (lane % SL) * 16, pol);
     }
-    copy_commit();
-  };
-
-  // (a group is committed for every stage, filled or not: the waits count groups)
-#pragma unroll
-  for (int k = 0; k < STAGES; ++k) {
-    if (k < nmine) issue(k);
-    else copy_commit();
   }
+};
 
-  uint32_t qf[C::KT][2];
-  float sc0, sc1;
-  load_query<C, D>(p, cm, ng, qf, sc0, sc1);
+// ACC: this lane's place in the first page of scores of head row `row` of sequence s.
+__device__ __forceinline__ float *fp4_score_lane(const DecodeParams &p, int s, int row) {
+  const int lane = threadIdx.x & 31;
+  return p.scores +
+         ((static_cast<int64_t>(s) * (p.Hkv * p.HG) + row) * p.max_blocks * kBlock + (lane >> 2)) * p.score_cols +
+         2 * (lane & 3);
+}
 
-  float acc[C::KT][4];
-#pragma unroll
-  for (int t = 0; t < C::KT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-  float m0 = kEmptyMax, m1 = kEmptyMax, l0 = 0.f, l1 = 0.f;
-  const int posA = 2 * qc < ng ? pos0 + (cm.v0 + 2 * qc) / cm.G : -1;
-  const int posB = 2 * qc + 1 < ng ? pos0 + (cm.v0 + 2 * qc + 1) / cm.G : -1;
-  const int end = min(len, pe * kBlock);  // tokens behind it are another range's, or nobody's
-  const int seeA = min(posA, end - 1), seeB = min(posB, end - 1);
-  float ab0 = 0.f, ab1 = 0.f;
-  if constexpr (!PLAIN) {
-    if (p.alibi) {
-      if (2 * qc < ng) ab0 = __ldg(p.alibi + cm.head(2 * qc)) * kLog2e;
-      if (2 * qc + 1 < ng) ab1 = __ldg(p.alibi + cm.head(2 * qc + 1)) * kLog2e;
-    }
-  }
-  float *score_lane = nullptr;  // ACC: this lane's place in the unit's first page of scores
-  if constexpr (ACC)
-    score_lane = p.scores + ((static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * p.max_blocks * kBlock + ra) * p.score_cols +
-                 2 * qc;
+// One warp's attention over the stages of a range: query fragments, softmax state, accumulator, and
+// the places its lane reads in a stage.
+template <typename C, int D, bool PLAIN>
+struct Fp4State {
+  static constexpr int NP = C::NP;
   using Rows = Fp4Rows<D>;
   using Runs = Fp4Runs<D>;
-  const int kon8 = Rows::on8(Rows::code_lane(ra, qc)), von8 = Rows::on8(Runs::code_lane(ra, qc));
-  const int vodd = Runs::odd(Runs::code_lane(ra, qc));
-  const uint32_t kcode0 = stage0 + Rows::code_lane(ra, qc), kscale0 = stage0 + Rows::scale_lane(ra, qc);
-  const uint32_t vcode0 = stage0 + NP * C::PAGEB + Runs::code_lane(ra, qc);
-  const uint32_t vscale0 = stage0 + NP * C::PAGEB + Runs::scale_lane(ra, qc);
+  uint32_t qf[C::KT][2];
+  float sc0, sc1;  // score scale (log2 units) of the lane's columns 2qc, 2qc + 1; never negative
+  float acc[C::KT][4];
+  float m0, m1, l0, l1;
+  int posA, posB, seeA, seeB;  // not PLAIN: the columns' positions, and the last tokens they see here
+  float ab0, ab1;              // not PLAIN: ALiBi slopes (log2 units)
+  int ra, qc, kon8, von8, vodd;
+  uint32_t kcode0, kscale0, vcode0, vscale0;
 
-  // One stage; TAIL when the range ends inside it (a range's last stage at most): the two are
-  // compiled apart, so that the others carry no trace of the end.
-  auto step = [&](auto tail_constant, const int k) {
-    constexpr bool TAIL = decltype(tail_constant)::value;
-    const uint32_t sto = (u0 + k) % STAGES * C::STAGEB;    // the stage's offset
-    const int tok0 = (pb + NP * (warp + k * W)) * kBlock;  // the stage's first token
-    const int left = end - tok0;                           // the range's tokens from there
+  // stage0: shared address of the warp's first stage
+  __device__ __forceinline__ void place(uint32_t stage0) {
+    ra = (threadIdx.x & 31) >> 2;
+    qc = threadIdx.x & 3;
+    kon8 = Rows::on8(Rows::code_lane(ra, qc));
+    von8 = Rows::on8(Runs::code_lane(ra, qc));
+    vodd = Runs::odd(Runs::code_lane(ra, qc));
+    kcode0 = stage0 + Rows::code_lane(ra, qc);
+    kscale0 = stage0 + Rows::scale_lane(ra, qc);
+    vcode0 = stage0 + NP * C::PAGEB + Runs::code_lane(ra, qc);
+    vscale0 = stage0 + NP * C::PAGEB + Runs::scale_lane(ra, qc);
+  }
+  // A range that ends before token `end`, for columns 0 .. ng - 1 of cm, the first query at pos0.
+  __device__ __forceinline__ void begin(const DecodeParams &p, const Cols &cm, int ng, int pos0, int end) {
+    load_query<C, D>(p, cm, ng, qf, sc0, sc1);
+#pragma unroll
+    for (int t = 0; t < C::KT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    m0 = m1 = kEmptyMax;
+    l0 = l1 = 0.f;
+    ab0 = ab1 = 0.f;
+    if constexpr (!PLAIN) {
+      posA = 2 * qc < ng ? pos0 + (cm.v0 + 2 * qc) / cm.G : -1;
+      posB = 2 * qc + 1 < ng ? pos0 + (cm.v0 + 2 * qc + 1) / cm.G : -1;
+      seeA = min(posA, end - 1);  // (tokens from `end` on are another range's, or nobody's)
+      seeB = min(posB, end - 1);
+      if (p.alibi) {
+        if (2 * qc < ng) ab0 = __ldg(p.alibi + cm.head(2 * qc)) * kLog2e;
+        if (2 * qc + 1 < ng) ab1 = __ldg(p.alibi + cm.head(2 * qc + 1)) * kLog2e;
+      }
+    }
+  }
 
+  // One stage at offset sto: tokens from tok0 on, `left` of them the range's.  TAIL when the range
+  // ends inside it (its last stage at most): compiled apart, so that the others carry no trace of
+  // the end.  ACC: scores to score_lane, this lane's place in the unit's first page of scores.
+  template <bool TAIL, bool ACC>
+  __device__ __forceinline__ void stage(const DecodeParams &p, uint32_t sto, int tok0, int left, float *score_lane) {
     // ---- scores: fragment rows ra, ra + 8 = tokens, columns 2qc, 2qc + 1
     float x[NP][4];
 #pragma unroll
@@ -317,21 +296,90 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
         }
       }
     }
+  }
 
+  // A whole stage or a range's end.
+  template <bool ACC>
+  __device__ __forceinline__ void any_stage(const DecodeParams &p, uint32_t sto, int tok0, int left, float *score_lane) {
+    if (left >= NP * kBlock) stage<false, ACC>(p, sto, tok0, left, score_lane);
+    else stage<true, ACC>(p, sto, tok0, left, score_lane);
+  }
+};
+
+// Runs pages [pb, pe) of sequence s; arguments and result as run_pages_tma (there is no wait here
+// that could give up).
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+__device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint32_t sbase, uint8_t *const sgen,
+                                              int &used, const int s, const int len, const Cols &cm,
+                                              const int pos0, const int ng, const int pb, const int pe, int entry,
+                                              const bool entry_ready, const uint64_t pol, const int wait_page) {
+  using C = MmaCfg<KIND, D, W, STAGES>;
+  constexpr int NP = C::NP;
+  constexpr int PER = 32 / NP;  // stages whose table entries the warp's lanes hold at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t *bt = p.block_table + static_cast<int64_t>(s) * p.bt_ss + pb;
+  const int n = pe - pb;                                      // pages of the range
+  const int nst = (n + NP - 1) / NP;                          // its stages, every W-th one this warp's
+  const int nmine = nst > warp ? (nst - warp + W - 1) / W : 0;
+  const uint32_t stage0 = sbase + static_cast<uint32_t>(warp * STAGES * C::STAGEB);
+  const int u0 = used;
+  bool bad = false, waited = false;
+
+  // Table entries, one page of the warp's next PER stages per lane.  An entry behind the range reads
+  // as block 0, and so does a bad one (the CTA then writes nothing), so every copy has a source.
+  auto check_entries = [&](int k) {
+    const bool in = C::entry(warp, lane) + k * NP * W < n;
+    const bool out = in && (entry < 0 || entry >= p.num_blocks);
+    if (out && p.err) atomicOr(p.err, kErrBlock);
+    if (out || !in) entry = 0;
+    bad |= __any_sync(0xffffffffu, out);
   };
+  const Fp4Copies<C, D> copies(p, cm.g, lane);
+  auto issue = [&](int k) {  // whole warp; k increases by one per call
+    if constexpr (EARLY) {
+      if (!waited && pb + NP * (warp + k * W) + NP > wait_page) {  // a page that may hold new positions
+        grid_dependency_wait();
+        waited = true;
+      }
+    }
+    const int at = k % PER;
+    if (at == 0) {
+      if (k > 0 || !entry_ready) {
+        const int i = C::entry(warp, lane) + k * NP * W;
+        entry = i < n ? __ldg(bt + i) : 0;
+      }
+      check_entries(k);
+    }
+    copies.stage(stage0 + (u0 + k) % STAGES * C::STAGEB, entry, at * NP, pol);
+    copy_commit();
+  };
+
+  // (a group is committed for every stage, filled or not: the waits count groups)
+#pragma unroll
+  for (int k = 0; k < STAGES; ++k) {
+    if (k < nmine) issue(k);
+    else copy_commit();
+  }
+
+  const int end = min(len, pe * kBlock);
+  Fp4State<C, D, PLAIN> state;
+  state.place(stage0);
+  state.begin(p, cm, ng, pos0, end);
+  float *score_lane = nullptr;
+  if constexpr (ACC) score_lane = fp4_score_lane(p, s, blockIdx.y);
 
   for (int k = 0; k < nmine; ++k) {
     copy_wait<STAGES - 1>();  // this lane's copies of the stage, then the whole warp's
     __syncwarp();
-    if (end - (pb + NP * (warp + k * W)) * kBlock >= NP * kBlock) step(std::false_type{}, k);
-    else step(std::true_type{}, k);
+    const int tok0 = (pb + NP * (warp + k * W)) * kBlock;
+    state.template any_stage<ACC>(p, (u0 + k) % STAGES * C::STAGEB, tok0, end - tok0, score_lane);
     __syncwarp();  // every lane has read the stage
     if (k + STAGES < nmine) issue(k + STAGES);
     else copy_commit();
   }
   used = u0 + nmine;
   __syncwarp();
-  store_warp_state<C, D, STAGES>(sgen, m0, m1, l0, l1, acc);
+  store_warp_state<C, D, STAGES>(sgen, state.m0, state.m1, state.l0, state.l1, state.acc);
   return bad;
 }
 

@@ -96,10 +96,13 @@ struct MmaCfg {
   static __device__ __forceinline__ int entry(int warp, int lane) { return NP * (warp + (lane / NP) * W) + lane % NP; }
   static constexpr int KT = D / 16;            // k-steps of Q.K^T = d-tiles of P.V
   static constexpr int THREADS = W * 32;
+  // floats between a warp state's accumulator rows; 4-bit: 4 more than D, so that the fragments'
+  // 16-byte stores meet no bank twice (with D, and element by element, they cost 16 turns each)
+  static constexpr int SROW = FP4 ? D + 4 : D;
   static constexpr size_t SCRATCH_OFF = static_cast<size_t>(W) * STAGES * STAGEB + W * STAGES * 8;
   static constexpr size_t SMEM = 1024 + SCRATCH_OFF + kMmaScratch;
   static_assert(FP4 || ROWB % 128 == 0, "page rows must be whole 128-byte swizzle spans");
-  static_assert(STAGES * STAGEB >= 64 + 8 * D * 4, "warp region must hold the merge state");
+  static_assert(STAGES * STAGEB >= 64 + 8 * SROW * 4, "warp region must hold the merge state");
   static_assert(static_cast<size_t>(W) * STAGES * STAGEB >= 8 * kMergeSmemParts * 4, "merge weights");
   static_assert(kMmaScratch >= kLptScratchBytes, "ranking scratch");
   static_assert(kMmaScratch >= (kFlatMaxSeqs + 1) * 4, "balanced-split page offsets");
@@ -176,7 +179,7 @@ __device__ __forceinline__ void load_query(const DecodeParams &p, const Cols &cm
 }
 
 // A warp's state (running max, sum, accumulator) into its own region: its stage buffers, with no
-// copies in flight.  ml[8][2], then acc[8][D].
+// copies in flight.  ml[8][2], then acc[8][SROW].
 template <typename C, int D, int STAGES>
 __device__ __forceinline__ void store_warp_state(uint8_t *sgen, float m0, float m1, float l0, float l1,
                                                  const float (&acc)[C::KT][4]) {
@@ -194,6 +197,32 @@ __device__ __forceinline__ void store_warp_state(uint8_t *sgen, float m0, float 
     wml[2 * (2 * qc + 1)] = m1;
     wml[2 * (2 * qc + 1) + 1] = l1;
   }
+  if constexpr (C::FP4) {
+    // a lane holds RUN consecutive elements of a section: whole 16-byte stores, in an order turned by
+    // the fragment row
+    constexpr int RUN = D >= 128 ? 16 : 8;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int b = 0; b < C::QB; ++b) {
+#pragma unroll
+        for (int j = 0; j < RUN / 4; ++j) {
+          float4 v[RUN / 4];
+#pragma unroll
+          for (int i = 0; i < RUN / 4; ++i) {
+            const int t = b * 8 + 2 * i;
+            v[i] = make_float4(acc[t][c], acc[t][2 + c], acc[t + 1][c], acc[t + 1][2 + c]);
+          }
+          const int at = (j + ra) % (RUN / 4);
+          float4 w = v[0];
+#pragma unroll
+          for (int i = 1; i < RUN / 4; ++i) w = at == i ? v[i] : w;
+          *reinterpret_cast<float4 *>(wacc + (2 * qc + c) * C::SROW + 128 * b + RUN * ra + 4 * at) = w;
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < C::KT; ++t) {
 #pragma unroll
@@ -201,7 +230,6 @@ __device__ __forceinline__ void store_warp_state(uint8_t *sgen, float m0, float 
       const int head = 2 * qc + (i & 1);
       int d;
       if constexpr (!C::WIDEN) d = 16 * t + ra + 8 * (i >> 1);
-      else if constexpr (D == 64) d = 8 * ra + 2 * t + (i >> 1);
       else d = 128 * (t >> 3) + 16 * ra + 2 * (t & 7) + (i >> 1);
       wacc[head * D + d] = acc[t][i];
     }
@@ -531,6 +559,46 @@ template <int KIND, int D, int W, int STAGES, bool ACC, typename OutT, typename 
 __device__ __forceinline__ void write_cta_state(const DecodeParams &p, const uint8_t *sgen, const Cols &cm, int ng,
                                                 float vs, bool direct, RowFn rows) {
   using C = MmaCfg<KIND, D, W, STAGES>;
+  if constexpr (C::FP4) {  // four elements at a time
+    for (int i = threadIdx.x; i < ng * (D / 4); i += C::THREADS) {
+      const int hh = i / (D / 4), d = (i - hh * (D / 4)) * 4;
+      float2 ml[W];
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        ml[w] = *reinterpret_cast<const float2 *>(sgen + w * STAGES * C::STAGEB + hh * 8);
+        M = fmaxf(M, ml[w].x);
+      }
+      float den = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float4 v = *reinterpret_cast<const float4 *>(
+            reinterpret_cast<const float *>(sgen + w * STAGES * C::STAGEB) + 16 + hh * C::SROW + d);
+        const float sc = ex2(ml[w].x - M);
+        den += sc * ml[w].y;
+        num.x += sc * v.x;
+        num.y += sc * v.y;
+        num.z += sc * v.z;
+        num.w += sc * v.w;
+      }
+      if (direct) {
+        const float f = den > 0.f ? vs / den : 0.f;
+        OutT *o = static_cast<OutT *>(p.out) + cm.out_off(p, hh) + d;
+        *reinterpret_cast<uint2 *>(o) =
+            C::QBF16 ? make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f))
+                     : make_uint2(pack_f16(num.x * f, num.y * f), pack_f16(num.z * f, num.w * f));
+        if constexpr (ACC) {
+          if (d == 0) p.lse[cm.row(hh) * p.Hq + cm.head(hh)] = log_total(M, den);
+        }
+      } else {
+        const int64_t r = rows(hh);
+        *reinterpret_cast<float4 *>(p.part_acc + r * D + d) = num;
+        if (d == 0) p.part_ml[r] = make_float2(M, den);
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < ng * D; i += C::THREADS) {
     const int hh = i / D, d = i - hh * D;
     float M = -INFINITY;
@@ -722,20 +790,21 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
       const int zlen = __ldg(p.seq_lens + z);
       bool bad = true;
       if (!dead)
-        bad = run_pages<KIND, D, W, STAGES, PLAIN, false, false>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
+        bad = run_pages<KIND, D, W, STAGES, PLAIN, false, ACC>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
                                             x - ps, y - ps, 0, false, pol, kNoWaitPage);
       const bool any_bad = __syncthreads_or(bad);
       if (any_bad) dead = __syncthreads_or(stalled) || dead;
       if (x == ps && y == pn) {
-        if (!any_bad) write_cta_state<KIND, D, W, STAGES, false, OutT>(p, sgen, cm, ng, vs, true, [](int) { return int64_t{0}; });
+        if (!any_bad) write_cta_state<KIND, D, W, STAGES, ACC, OutT>(p, sgen, cm, ng, vs, true, [](int) { return int64_t{0}; });
+        else if (ACC) drop_lse(p, cm, ng);
       } else {
         const int j = x == a ? 0 : 1;  // this CTA's first or last range
         if (!any_bad)
-          write_cta_state<KIND, D, W, STAGES, false, OutT>(p, sgen, cm, ng, vs, false,
+          write_cta_state<KIND, D, W, STAGES, ACC, OutT>(p, sgen, cm, ng, vs, false,
                                                     [&](int hh) { return (my_row * 2 + j) * 8 + hh; });
         // a CTA with an error still counts itself, so the unit's counter returns to zero
         const int c0 = owner(ps);
-        merge_if_last<OutT, D, false>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * z, ng, owner(pn - 1) - c0 + 1,
+        merge_if_last<OutT, D, ACC>(p, cm, static_cast<int>(blockIdx.y) + p.Hkv * p.HG * z, ng, owner(pn - 1) - c0 + 1,
                                vs, any_bad, C::THREADS, smem_w,
                                FlatRows{static_cast<int64_t>(blockIdx.y) * p.flat + c0, range_start(c0) < ps ? 1 : 0});
       }
@@ -834,13 +903,13 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
           const float mw = ml[2 * hh];
           const float sc = (mw == -INFINITY) ? 0.f : ex2(mw - M);
           den += sc * ml[2 * hh + 1];
-          num += sc * ml[16 + hh * D + d];
+          num += sc * ml[16 + hh * C::SROW + d];
         }
-        cs[hh * D + d] = num;
+        cs[hh * C::SROW + d] = num;
         if (d == 0) cmd[hh] = make_float2(M, den);
       }
     }
-    cluster_merge_write<OutT, D>(p, cm, ng, vs, any_bad, cs, D, cmd, reinterpret_cast<int *>(cmd + 8),
+    cluster_merge_write<OutT, D>(p, cm, ng, vs, any_bad, cs, C::SROW, cmd, reinterpret_cast<int *>(cmd + 8),
                                  C::THREADS);
     return;
   }
@@ -862,6 +931,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
 // resident CTAs per SM.
 template <int KIND, int D>
 struct MmaLaunch {
+  static constexpr int kKind = KIND, kD = D;
   static constexpr int W = mma_warps(KIND, D), ST = mma_stages(KIND, D);
   using C = MmaCfg<KIND, D, W, ST>;
   static_assert(C::SMEM == mma_smem(KIND, D), "shape table out of sync");

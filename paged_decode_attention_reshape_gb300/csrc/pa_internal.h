@@ -109,7 +109,7 @@ struct DecodeParams {
   // writing any output.  0: wait for it first.
   int early;
   const int32_t *new_start;
-  int flat;                            // > 0: balanced split, this many CTAs per head row (S <= kFlatMaxSeqs)
+  int flat;                            // > 0: balanced split, this many CTAs (4-bit: or warps) per head row (S <= kFlatMaxSeqs)
   // Poll limit of the first pipeline wait (decode: each warp's first page; query tile: the
   // first K/V group): 0 = the normal limit, > 0 = that many polls, < 0 = give up at once.
   // Tests use it to make a bounded wait run out; every later wait and drain keeps the normal limit.
@@ -184,7 +184,7 @@ constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND
 constexpr int mma_warps(int kind, int D) { return D == 64 || (mma_fp4(kind) && D == 128) ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
-constexpr int mma_stages(int kind, int D) { return (void)kind, (void)D, 2; }
+constexpr int mma_stages(int kind, int D) { return mma_fp4(kind) && D == 256 ? 3 : 2; }
 // Resident CTAs per SM the register allocation must allow (ptxas launch bound): as
 // many as the shared memory admits, so registers never cut the occupancy, except
 // for the E4M3 head-size-128 kernel (6 by shared memory; held at 4 to avoid spills).
@@ -198,7 +198,7 @@ constexpr int mma_page_bytes(int kind, int D) {
 }
 // Pages of one stage.  4-bit pages are small (1152 bytes at head size 128) and cheap to multiply,
 // so several share a stage, and with it a barrier wait, the running maximum's vote and the loop.
-constexpr int mma_stage_pages(int kind, int D) { return !mma_fp4(kind) ? 1 : D == 64 ? 4 : 2; }
+constexpr int mma_stage_pages(int kind, int D) { return !mma_fp4(kind) || D == 256 ? 1 : D == 64 ? 4 : 2; }
 constexpr size_t kMmaScratch = 2048;  // sequence-order ranking scratch (after the barriers)
 constexpr size_t mma_smem(int kind, int D) {
   return 1024 + static_cast<size_t>(mma_warps(kind, D)) * mma_stages(kind, D) * (2 * mma_page_bytes(kind, D) * mma_stage_pages(kind, D) + 8) +
@@ -229,6 +229,8 @@ constexpr int kChunkTwoTileColumns = 128;
 int occupancy_decode_mma_16(int kind, int D);
 int occupancy_decode_mma_fp8(int kind, int D);
 int occupancy_decode_mma_fp4(int kind, int D);
+// 4-bit caches, the balanced split over the warps of `ctas` CTAs (p.flat warps per head row).
+cudaError_t launch_decode_fp4_warps(const DecodeParams &p, int kind, int ctas, cudaStream_t st);
 
 // Launch `kern` as a programmatic dependent of the previous work on `st`, in
 // thread-block clusters of `cluster_x` CTAs along x when cluster_x > 1.

@@ -135,7 +135,7 @@ def test_decode_and_accumulate_refusals(L):
     assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, ptr=0)) == -1
     assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, ptr=0x10002)) == -3
     assert _accumulate(L, out, q, page, page, bt, sl, H, _t([S, H, MB * 16], pa.PA_F32, strides=[999, 99, 2])) == -1
-    for P in (-2, -8, pa.PA_PARTITION_BALANCED):
+    for P in (-2, -8):
         none.partition_size = P
         assert _accumulate(L, out, q, page, page, bt, sl, H, w, none) == -7
     empty = _t([0, Hq, D], pa.PA_BF16)
@@ -155,6 +155,18 @@ def test_accumulate_workspace_size(L):
 
 
 def test_plan_of_a_4_bit_cache(L):
+    B = pa.PA_PARTITION_BALANCED
+    # many units: over the warps of a resident wave (152 SMs x 2 CTAs x 8 warps over 8 head rows)
+    assert pa.pa_decode_plan(256, 32, 8, 128, 256, pa.PA_FP4_E2M1, 152, 0) == (B, 152 * 16 // 8)
+    # fewer: whole, unless asked
     assert pa.pa_decode_plan(128, 64, 8, 128, 512, pa.PA_FP4_E2M1, 152, 0) == (0, 1)
-    P, n = pa.pa_decode_plan(4, 32, 8, 128, 8192, pa.PA_FP4_E2M1, 152, 0)
-    assert P >= 1024 and P % 16 == 0 and n == -(-8192 * 16 // P)
+    assert pa.pa_decode_plan(128, 64, 8, 128, 512, pa.PA_FP4_E2M1, 152, B) == (B, 152 * 16 // 8)
+    # few long ones: over CTAs
+    assert pa.pa_decode_plan(4, 32, 8, 128, 8192, pa.PA_FP4_E2M1, 152, 0)[0] == B
+    # few short ones: fixed partitions, of 512 tokens at least, or none
+    P, n = pa.pa_decode_plan(1, 32, 8, 128, 512, pa.PA_FP4_E2M1, 152, 0)
+    assert P == 512 and n == 16
+    assert pa.pa_decode_plan(2, 4, 4, 64, 3, pa.PA_FP4_E2M1, 152, 0) == (0, 1)
+    # batches past the balanced split's limit: unsplit
+    assert pa.pa_decode_plan(4096, 32, 8, 128, 256, pa.PA_FP4_E2M1, 152, 0) == (0, 1)
+    assert pa.pa_decode_plan(128, 64, 8, 128, 512, pa.PA_FP4_E2M1, 152, 512) == (512, 16)

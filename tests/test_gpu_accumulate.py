@@ -85,7 +85,7 @@ def test_weights_and_outputs(kind, Hq, Hkv, D, biased):
     before = np.exp(rng.randn(c.S, Hkv, W)).astype(np.float32)
     want, tol = expected(c, K, before)
     alibi = None if c.alibi is None else torch.from_numpy(np.asarray(c.alibi, np.float32)).cuda()
-    for P in (-1, 64, 0):
+    for P in (-1, 64, 0, pa.PA_PARTITION_BALANCED):
         outs = []
         for ws in (None, torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")):
             wide = torch.full((c.S, 2, Hkv, W), float("nan"), device="cuda")      # a strided array
@@ -130,7 +130,7 @@ def test_faults_add_nothing(kind):
     g.block_table[4, 5] = -3
     g.seq_lens[3] = W + 1
     g.seq_lens[1] = -1
-    for P in (-1, 64):
+    for P in (-1, 64, 0, pa.PA_PARTITION_BALANCED):
         weights = torch.zeros(c.S, 2, W, device="cuda")
         pa.pa_decode_accumulate(*_args(c, g), weights, partition_size=P, device_error=g.err, **_kw(kind, g))
         assert pa.pa_check_device_error(g.err) == (-6, pa.PA_DEVERR_BLOCK_RANGE | pa.PA_DEVERR_SEQLEN_RANGE)
@@ -166,3 +166,31 @@ def test_captured_after_a_first_call():
     torch.cuda.synchronize()
     want, tol = expected(c, K, np.zeros(weights.shape, np.float32))
     assert (np.abs(weights.double().cpu().numpy() - want) <= tol).all()
+
+
+def test_many_sequences_over_a_4_bit_cache():
+    """The decode's split over warps (parts of a sequence merged by the last warp to finish)."""
+    rng = np.random.RandomState(5)
+    lens = (rng.rand(60) ** 3 * 900).astype(int)
+    lens[:5] = [0, 1, 64, 65, 1300]
+    c = fp4_cases.make(60, 16, 8, 128, lens.tolist(), torch.bfloat16, seed=9)
+    B = pa.PA_PARTITION_BALANCED
+    ref, otol, _ = fp4_cases.reference(c)
+    g = fp4_cases.to_gpu(c)
+    W = c.width * 16
+    before = np.exp(rng.randn(60, 8, W)).astype(np.float32)
+    want, tol = expected(c, c.K, before)
+    size = pa.pa_decode_accumulate_workspace_size(60, 16, 8, 128, c.width, B)
+    for ws in (None, torch.zeros(size, dtype=torch.uint8, device="cuda")):
+        weights = torch.from_numpy(before).cuda()
+        pa.pa_decode_accumulate(*_args(c, g), weights, partition_size=B, workspace=ws, device_error=g.err)
+        assert pa.pa_check_device_error(g.err) == (0, 0)
+        fp4_cases.check(g.out, ref, otol, "outputs")
+        assert (np.abs(weights.double().cpu().numpy() - want) <= tol).all()
+    g.block_table[4, 50] = -1
+    g.block_table[2, 0] = -1
+    weights = torch.zeros(60, 8, W, device="cuda")
+    pa.pa_decode_accumulate(*_args(c, g), weights, partition_size=B, device_error=g.err)
+    assert pa.pa_check_device_error(g.err) == (-6, pa.PA_DEVERR_BLOCK_RANGE)
+    got = weights.double().cpu().numpy()
+    assert not got[[2, 4]].any() and got[3].any()

@@ -206,3 +206,111 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         fp4_cases.check(g.out, ref, tol, "replay")
+
+
+# ------------------------------------------------ the split over warps (many sequences and heads)
+
+def _many(Hq, Hkv, D, dt, S, seed, **kw):
+    rng = np.random.RandomState(seed)
+    lens = (rng.rand(S) ** 3 * 900).astype(int)      # most short, some long
+    lens[:8] = [0, 1, 16, 17, 63, 64, 65, 1500]
+    lens[-2:] = [700, 0]
+    return fp4_cases.make(S, Hq, Hkv, D, lens.tolist(), dt, seed=seed, **kw)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,S,dt", [(16, 8, 64, 60, torch.bfloat16), (8, 8, 128, 50, torch.float16),
+                                           (20, 10, 128, 40, torch.bfloat16), (36, 4, 64, 50, torch.bfloat16),
+                                           (12, 6, 256, 60, torch.float16)])
+def test_split_over_warps(Hq, Hkv, D, S, dt):
+    c = _many(Hq, Hkv, D, dt, S, seed=D + S, k_scale=0.7, v_scale=1.3, interleaved=D == 128)
+    B = pa.PA_PARTITION_BALANCED
+    assert pa.pa_decode_plan(S, Hq, Hkv, D, c.width, pa.PA_FP4_E2M1, partition_size=B)[1] % 4 == 0
+    ref, tol, _ = fp4_cases.reference(c)
+    g = fp4_cases.to_gpu(c)
+    first = None
+    for P, ws in ((B, True), (B, False), (B, True)):
+        assert _decode(c, g, P, ws=ws) == (0, 0)
+        fp4_cases.check(g.out, ref, tol, "partition %d" % P)
+        first = g.out.clone() if first is None else first
+        assert torch.equal(first, g.out)              # the parts merge in order, whoever merges them
+    size = pa.pa_decode_workspace_size(S, Hq, Hkv, D, c.width, pa.PA_PARTITION_BALANCED)
+    g.ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    assert _decode(c, g, B) == (0, 0) and torch.equal(first, g.out)
+    # the size also serves the same shape's other plans
+    slopes = torch.full((Hq,), 0.01, device="cuda")
+    g.ws.zero_()
+    pa.pa_decode_opt(g.out, g.q, g.k_cache, g.v_cache, g.block_table, g.seq_lens, c.scale, Hkv, alibi_slopes=slopes,
+                     workspace=g.ws, device_error=g.err)
+    assert pa.pa_check_device_error(g.err) == (0, 0)
+
+
+def test_split_over_warps_is_the_plan_of_many_units():
+    c = _many(8, 8, 64, torch.bfloat16, 210, seed=8)
+    assert pa.pa_decode_plan(210, 8, 8, 64, c.width, pa.PA_FP4_E2M1)[0] == pa.PA_PARTITION_BALANCED
+    ref, tol, _ = fp4_cases.reference(c)
+    g = fp4_cases.to_gpu(c)
+    assert _decode(c, g, 0, ws=False) == (0, 0)
+    fp4_cases.check(g.out, ref, tol)
+    first = g.out.clone()
+    assert _decode(c, g, pa.PA_PARTITION_BALANCED) == (0, 0)
+    assert torch.equal(first, g.out)
+
+
+def test_split_over_warps_faults_and_recovery():
+    c = _many(16, 8, 64, torch.bfloat16, 60, seed=77)
+    ref, tol, _ = fp4_cases.reference(c)
+    g = fp4_cases.to_gpu(c)
+    good = (g.block_table.clone(), g.seq_lens.clone())
+    long = int(np.argmax(c.lens))
+    g.block_table[long, 40] = -5                       # inside a sequence that several warps share
+    g.block_table[4, 0] = c.NB
+    g.seq_lens[20] = -1
+    for _ in range(2):
+        rc, bits = _decode(c, g, pa.PA_PARTITION_BALANCED)
+        assert rc == -6 and bits == pa.PA_DEVERR_BLOCK_RANGE | pa.PA_DEVERR_SEQLEN_RANGE
+        bad = [long, 4, 20]
+        assert bool(g.out[bad].isnan().all())
+        keep = [s for s in range(c.S) if s not in bad]
+        fp4_cases.check(g.out[keep], ref[keep], tol[keep], "sequences without a fault")
+    g.block_table, g.seq_lens = good
+    assert _decode(c, g, pa.PA_PARTITION_BALANCED) == (0, 0)                  # the counters are back at zero
+    fp4_cases.check(g.out, ref, tol, "after the faults")
+
+
+def test_split_over_warps_empty_and_equal_batches():
+    for lens in ([0] * 60, [1] * 60, [64] * 60, [5] + [0] * 58 + [3]):
+        c = fp4_cases.make(60, 8, 8, 64, lens, torch.bfloat16, seed=3)
+        ref, tol, _ = fp4_cases.reference(c)
+        g = fp4_cases.to_gpu(c)
+        assert _decode(c, g, pa.PA_PARTITION_BALANCED) == (0, 0)
+        fp4_cases.check(g.out, ref, tol, str(lens[:3]))
+
+
+def test_split_over_warps_in_two_graphs_of_one_workspace():
+    """Two captured calls of different shapes on the library's workspace, replayed in turn."""
+    cases = [_many(16, 8, 64, torch.bfloat16, 60, seed=1), _many(8, 8, 128, torch.bfloat16, 45, seed=2)]
+    stream, graphs, on = torch.cuda.Stream(), [], []
+    for c in cases:
+        g = fp4_cases.to_gpu(c)
+        assert _decode(c, g, pa.PA_PARTITION_BALANCED, ws=False) == (0, 0)
+        on.append((c, g, *fp4_cases.reference(c)[:2]))
+    for c, g, _, _ in on:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            pa.pa_decode_opt(g.out, g.q, g.k_cache, g.v_cache, g.block_table, g.seq_lens, c.scale, c.Hkv,
+                             k_scale=g.k_scale, v_scale=g.v_scale, partition_size=pa.PA_PARTITION_BALANCED)
+    for i in (0, 1, 1, 0):
+        c, g, ref, tol = on[i]
+        g.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        fp4_cases.check(g.out, ref, tol, "graph %d" % i)
+
+
+def test_more_sequences_than_the_balanced_split_takes():
+    c = fp4_cases.make(520, 2, 1, 64, [i % 40 for i in range(520)], torch.bfloat16, seed=4)
+    ref, tol, _ = fp4_cases.reference(c)
+    g = fp4_cases.to_gpu(c)
+    assert _decode(c, g, 0) == (0, 0)
+    fp4_cases.check(g.out, ref, tol, "520 sequences")
