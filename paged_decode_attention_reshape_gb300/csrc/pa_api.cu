@@ -439,10 +439,10 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
     f.T = T;
     f.Hkv = Hkv;
     f.D = D;
-    f.key_ts = key->stride[0];
-    f.key_hs = key->stride[1];
-    f.val_ts = value->stride[0];
-    f.val_hs = value->stride[1];
+    f.key_ts = key->stride[0] * ib;
+    f.key_hs = key->stride[1] * ib;
+    f.val_ts = value->stride[0] * ib;
+    f.val_hs = value->stride[1] * ib;
     f.kc_s0 = k_cache->stride[0];
     f.kc_s1 = k_cache->stride[1];
     f.vc_s0 = v_cache->stride[0];
@@ -452,6 +452,10 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
     f.v_scale = o.v_scale;
     f.scale_stride = o.scale_stride;
     f.err = o.device_error;
+    f.wide = rows_aligned32(key, ib) && rows_aligned32(value, ib);
+    f.i32 = T <= INT32_MAX;
+    for (const int64_t x : {f.key_ts, f.key_hs, f.val_ts, f.val_hs, f.kc_s0, f.kc_s1, f.vc_s0, f.vc_s1})
+      f.i32 &= x <= INT32_MAX;
     ProfScope ps(PA_KERNEL_WRITE, st);
     return launch_write_fp4(f, in_dt, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
@@ -552,10 +556,10 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
   p.T = T;
   p.Hkv = Hkv;
   p.D = D;
-  p.key_ts = key->stride[0];
-  p.key_hs = key->stride[1];
-  p.val_ts = value->stride[0];
-  p.val_hs = value->stride[1];
+  p.key_ts = key->stride[0] * ob;
+  p.key_hs = key->stride[1] * ob;
+  p.val_ts = value->stride[0] * ob;
+  p.val_hs = value->stride[1] * ob;
   p.kc_s0 = k_cache->stride[0] * cb;
   p.kc_s1 = k_cache->stride[1] * cb;
   p.kc_s2 = cache_dt == PA_FP4_E2M1 ? 0 : k_cache->stride[2] * cb;
@@ -567,6 +571,10 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
   p.v_scale = quantised ? o.v_scale : nullptr;
   p.scale_stride = o.scale_stride;
   p.err = o.device_error;
+  p.wide = rows_aligned32(key, ob) && rows_aligned32(value, ob);
+  p.i32 = T <= INT32_MAX;
+  for (const int64_t x : {p.key_ts, p.key_hs, p.val_ts, p.val_hs, p.kc_s0, p.kc_s1, p.kc_s2, p.vc_s0, p.vc_s1, p.vc_s2})
+    p.i32 &= x <= INT32_MAX;
   return launch_gather(p, cache_dt, out_dt, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

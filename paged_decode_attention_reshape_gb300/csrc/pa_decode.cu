@@ -211,6 +211,7 @@ cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
 // reads one 16- or 32-byte run per token and adjacent threads adjacent runs.  Keeping the
 // scores costs 4 bytes a (query head, token) each way, mostly served by L2, against a second
 // read of every K page (2 D bytes a (KV head, token) for a 16-bit cache).
+constexpr int kWeightTokens = 4;  // tokens in flight per thread (one: 32 us on 64 x 1k..8k tokens, 8 KV heads)
 template <int CW>
 __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
   const int s = blockIdx.z, g = blockIdx.y;
@@ -218,37 +219,53 @@ __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
   const int len = __ldg(p.seq_lens + s);
   if (len < 0 || len > p.max_tokens) return;  // reported by the decode
   float *w = p.weights + s * p.w_ss + g * p.w_hs;
-  for (int t = blockIdx.x * 256 + threadIdx.x; t < len; t += gridDim.x * 256) {
-    float sum = 0.f;
+  const int64_t unit0 = (static_cast<int64_t>(s) * p.Hkv + g) * p.HG;
+  for (int t0 = blockIdx.x * (256 * kWeightTokens) + threadIdx.x; t0 < len; t0 += gridDim.x * (256 * kWeightTokens)) {
+    float sum[kWeightTokens], old[kWeightTokens];
+#pragma unroll
+    for (int k = 0; k < kWeightTokens; ++k) {
+      sum[k] = 0.f;
+      old[k] = t0 + 256 * k < len ? w[t0 + 256 * k] : 0.f;
+    }
     for (int hg = 0; hg < p.HG; ++hg) {
-      const float *sc = p.scores + ((static_cast<int64_t>(s) * p.Hkv + g) * p.HG + hg) * static_cast<int64_t>(p.max_tokens) * CW +
-                        static_cast<int64_t>(t) * CW;
+      const float *sc = p.scores + (unit0 + hg) * p.max_tokens * CW;
       const float *lse = p.lse + static_cast<int64_t>(s) * p.Hkv * p.G + g * p.G + hg * 8;
       const int n = min(CW, p.G - hg * 8);
-      float v[CW];
-      if constexpr (CW >= 4) {
+      float v[kWeightTokens][CW], ls[CW];
 #pragma unroll
-        for (int i = 0; i < CW / 4; ++i) {
-          const float4 f = __ldcg(reinterpret_cast<const float4 *>(sc) + i);
-          v[4 * i] = f.x;
-          v[4 * i + 1] = f.y;
-          v[4 * i + 2] = f.z;
-          v[4 * i + 3] = f.w;
+      for (int k = 0; k < kWeightTokens; ++k) {
+        if (t0 + 256 * k >= len) continue;
+        const float *x = sc + static_cast<int64_t>(t0 + 256 * k) * CW;
+        if constexpr (CW >= 4) {
+#pragma unroll
+          for (int i = 0; i < CW / 4; ++i) {
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(x) + i);
+            v[k][4 * i] = f.x;
+            v[k][4 * i + 1] = f.y;
+            v[k][4 * i + 2] = f.z;
+            v[k][4 * i + 3] = f.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CW; ++i) v[k][i] = __ldcg(x + i);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < CW; ++i) v[i] = __ldcg(sc + i);
       }
 #pragma unroll
-      for (int i = 0; i < CW; ++i)
-        if (i < n) sum += ex2(v[i] - __ldcg(lse + i));
+      for (int i = 0; i < CW; ++i) ls[i] = i < n ? __ldcg(lse + i) : 0.f;
+#pragma unroll
+      for (int k = 0; k < kWeightTokens; ++k)
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+          if (i < n && t0 + 256 * k < len) sum[k] += ex2(v[k][i] - ls[i]);
     }
-    w[t] += sum;
+#pragma unroll
+    for (int k = 0; k < kWeightTokens; ++k)
+      if (t0 + 256 * k < len) w[t0 + 256 * k] = old[k] + sum[k];
   }
 }
 
 cudaError_t launch_weights(const WeightsParams &p, int cols, cudaStream_t st) {
-  const int64_t blocks = (static_cast<int64_t>(p.max_tokens) + 255) / 256;
+  const int64_t blocks = (static_cast<int64_t>(p.max_tokens) + 256 * kWeightTokens - 1) / (256 * kWeightTokens);
   const dim3 grid(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), p.Hkv, p.S);
   switch (cols) {
     case 1: return launch_pdl(weights_kernel<1>, grid, dim3(256), 0, st, 1, p);

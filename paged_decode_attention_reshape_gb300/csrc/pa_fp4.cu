@@ -8,12 +8,11 @@
 // above zero, so sg is never zero and the quotient always exists (a group of zeros gets codes
 // of zero).  A group that holds a NaN gets scale NaN (0x7F) and codes 0.
 //
-// Work split: one thread per group, K and V together (16 elements are 32 bytes of a 16-bit
-// row, two 16-byte loads, and 8 bytes of codes), a CTA over whole tokens, adjacent threads
-// on adjacent groups.  Bound by the bytes (2 read and 9/16 written an element) when T is
-// large, by the launch when it is small.  Both quotients of an element are the correctly
-// rounded ones of pa_quant.cuh (one reciprocal per scale, packed fused steps), about 12
-// operations an element.
+// Work split: one thread per group, K and V together (16 elements are 32 bytes of a 16-bit row, one
+// 32-byte load where it is aligned, and 8 bytes of codes).  Bound by the bytes (2 read and 9/16
+// written an element) and by the arithmetic when T is large, by the launch when it is small, so the
+// quotients are bracketed instead of taken (quantise_group): two products and two conversions an
+// element, and the definition's divisions only for a group that the bracket does not settle.
 //
 // Read back.  value = code * sg * s: code * sg has at most 6 significant bits (exact in f16),
 // the product with s and the conversion to the output's type round once each.  The same
@@ -24,25 +23,34 @@
 namespace pa {
 namespace {
 
-// Element i of the group: x[i] as fp32.
+// 16 elements of a row as its bytes (32 of a 16-bit row, 64 of an fp32 one).  wide: 32-byte aligned.
 template <int DT>
-__device__ __forceinline__ void load_group(const char *src, float (&x)[16]) {
+__device__ __forceinline__ void load_group(const char *src, bool wide, uint32_t (&w)[4 * In<DT>::bytes]) {
+#pragma unroll
+  for (int i = 0; i < In<DT>::bytes / 2; ++i) {
+    uint32_t v[8];
+    if (wide) {
+      ld32_once(src + 32 * i, v);
+    } else {
+      const uint4 a = ld_once(src + 32 * i), b = ld_once(src + 32 * i + 16);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[8 * i + j] = v[j];
+  }
+}
+template <int DT>
+__device__ __forceinline__ void group_values(const uint32_t (&w)[4 * In<DT>::bytes], float (&x)[16]) {
   if constexpr (DT == PA_F32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = ld_once(src + 16 * i);
-      x[4 * i] = __uint_as_float(v.x);
-      x[4 * i + 1] = __uint_as_float(v.y);
-      x[4 * i + 2] = __uint_as_float(v.z);
-      x[4 * i + 3] = __uint_as_float(v.w);
-    }
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float h[8];
-      unpack8<DT>(ld_once(src + 16 * i), h);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[8 * i + j] = h[j];
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = DT == PA_BF16 ? unpack_bf16(w[i]) : unpack_f16(w[i]);
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
     }
   }
 }
@@ -71,227 +79,318 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
   return r;
 }
 
-// The group's codes and scale.  `dv` divides by the head's scale; `unit` when that is 1.
-// Magnitudes are clamped to 2^80 and signs put back at the end, so the fused quotient steps
-// hold for every input (see store_fp8 in pa_write.cu): a larger magnitude saturates all the
-// same, a magnitude too small for exact steps rounds to code 0 under any scale >= 2^-9.
-__device__ __forceinline__ void quantise_group(float (&x)[16], const Divisor &dv, bool unit, uint2 &codes,
-                                               uint32_t &scale) {
-  float y[16];
-  if (unit) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = clamp_mag(x[i]);
-  } else if (dv.fast) {
-    const Divisor da{fabsf(dv.s), fabsf(dv.y), true};
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float2 r = da.div2_fast(clamp_mag(x[i]), clamp_mag(x[i + 1]));
-      y[i] = r.x;
-      y[i + 1] = r.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = clamp_mag(__fdiv_rn(x[i], fabsf(dv.s)));
+// The group's codes and scale, by the definition's own quotients (every one an IEEE division).  The
+// fast path below sends it what it cannot settle: about one group in a hundred thousand of
+// arbitrary values, those on the border of a code, out of range, or NaN.  s: the head's scale.
+__device__ __noinline__ uint3 quantise_exact(const float (&x)[16], float s) {
+  float y[16], top = 0.f;
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    y[i] = __fdiv_rn(x[i], s);
+    bad |= y[i] != y[i];
+    top = fmaxf(top, fabsf(y[i]));
   }
-  float top = y[0];
+  if (bad) return make_uint3(0u, 0u, 0x7Fu);
+  const uint32_t scale =
+      static_cast<uint32_t>(__nv_cvt_float_to_fp8(fmaxf(__fdiv_rn(top, 6.f), 0x1p-9f), __NV_SATFINITE, __NV_E4M3));
+  const float sg = unpack_f16(e4m3x2_to_f16x2(scale)).x;
+  const uint32_t flip = s < 0.f ? 0x80000000u : 0u;  // (a quotient that is zero has lost its sign for a zero x)
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll 1
+  for (int i = 0; i < 16; i += 8) {
+    float q[8];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) top = max_nan(top, y[i]);
-  const float want = max_nan(__fdiv_rn(top, 6.f), 0x1p-9f);
-  scale = static_cast<uint32_t>(__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3));
-  if (top != top) {
-    codes = make_uint2(0u, 0u);
-    return;
+    for (int j = 0; j < 8; ++j)
+      q[j] = with_sign(fabsf(__fdiv_rn(y[i + j], sg)), __uint_as_float(__float_as_uint(x[i + j]) ^ flip));
+    w[i >> 3] = e2m1x8(q);
   }
-  const uint32_t wide = e4m3x2_to_f16x2(scale);
-  const Divisor dg = make_divisor(unpack_f16(wide).x);  // in [2^-9, 448]
-  const float flip = dv.s < 0.f ? -1.f : 1.f;  // (the scale's sign: unit and zero scales have none)
-  float q[16];
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const float2 r = dg.div2_fast(y[i], y[i + 1]);
-    q[i] = with_sign(r.x, x[i] * flip);
-    q[i + 1] = with_sign(r.y, x[i + 1] * flip);
-  }
-  codes.x = e2m1x8(reinterpret_cast<float(&)[8]>(q[0]));
-  codes.y = e2m1x8(reinterpret_cast<float(&)[8]>(q[8]));
+  return make_uint3(w[0], w[1], scale);
 }
 
-template <int DT>
+__device__ __forceinline__ uint3 settle(const float (&x)[16], float s) {
+  float y[16];  // (a copy: the call takes an address, and x stays in registers)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = x[i];
+  return quantise_exact(y, s);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  uint64_t x, y;
+  float2 o;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(x));
+  return o;
+}
+
+// The same without a division.  Rounding never falls as its argument grows, so if a value a little
+// below the quotient and one a little above it have the same code, the quotient has it too.  With
+// r = (1 / s) (1 / sg) from two approximate reciprocals (2^-23 each) and three rounded products
+// (2^-24 each), x r is within 2^-21.1 of x / (s sg), and the definition's twice rounded quotient
+// within 2^-23: the codes of x r (1 - kNear) and x r (1 + kNear) enclose its code and, where they
+// agree, are it; the group's scale is settled alike from its largest |x|.  Products keep the signs
+// of zeros.
+// UNIT16: a 16-bit x and s = 1, where borders are hit often: x has at most 11 significant bits, a
+// border of the code 3 and sg 4, so x / sg is a border or 2^-18 of itself away from it, and a
+// quotient corrected once (exact where the true one is an fp32 number, else within 2^-22) decides.
+constexpr float kNear = 0x1p-20f;
+template <bool UNIT16>
+__device__ __forceinline__ uint3 quantise_group(const float (&x)[16], float s, float rs) {
+  float top = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) top = max_nan(top, fabsf(x[i]));
+  const float want = top * fabsf(rs) * (1.f / 6.f);
+  const uint32_t two = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+      make_float2(max_nan(want * (1.f - kNear), 0x1p-9f), max_nan(want * (1.f + kNear), 0x1p-9f)), __NV_SATFINITE,
+      __NV_E4M3));
+  const uint32_t scale = two & 0xffu;
+  // (false for a NaN; the bounds keep every product below from overflow, and a head scale whose
+  // reciprocal is not a plain number out of here)
+  const bool plain = top <= 0x1p80f && fabsf(rs) <= 0x1p40f && fabsf(rs) >= 0x1p-40f && scale == two >> 8;
+  if (!plain) return settle(x, s);
+  const float sg = unpack_f16(e4m3x2_to_f16x2(scale)).x, rg = rcp_approx(sg);
+  float q[16];
+  uint2 codes;
+  if constexpr (UNIT16) {
+    const Divisor d{sg, rg, true};
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 r = d.div2_near(x[i], x[i + 1]);  // (drops the sign of a zero)
+      q[i] = with_sign(r.x, x[i]);
+      q[i + 1] = with_sign(r.y, x[i + 1]);
+    }
+    codes.x = e2m1x8(reinterpret_cast<float(&)[8]>(q[0]));
+    codes.y = e2m1x8(reinterpret_cast<float(&)[8]>(q[8]));
+  } else {
+    const float r = rs * rg;
+    uint2 above;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 v = mul2(make_float2(x[i], x[i + 1]), r * (1.f - kNear));
+      q[i] = v.x;
+      q[i + 1] = v.y;
+    }
+    codes.x = e2m1x8(reinterpret_cast<float(&)[8]>(q[0]));
+    codes.y = e2m1x8(reinterpret_cast<float(&)[8]>(q[8]));
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 v = mul2(make_float2(x[i], x[i + 1]), r * (1.f + kNear));
+      q[i] = v.x;
+      q[i + 1] = v.y;
+    }
+    above.x = e2m1x8(reinterpret_cast<float(&)[8]>(q[0]));
+    above.y = e2m1x8(reinterpret_cast<float(&)[8]>(q[8]));
+    if (codes.x != above.x || codes.y != above.y) return settle(x, s);
+  }
+  return make_uint3(codes.x, codes.y, scale);
+}
+
+// A product of an index and a stride, in one widening multiply when both are below 2^31 (I32).
+template <bool I32>
+__device__ __forceinline__ int64_t times(int64_t i, int64_t stride) {
+  if constexpr (I32) return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(i)) * static_cast<uint32_t>(stride));
+  else return i * stride;
+}
+
+// Blocks of (groups of a row, heads, tokens) threads: no thread divides to find its place.
+template <int DT, bool I32>
 __global__ void __launch_bounds__(256) write_fp4_kernel(const Fp4WriteParams p) {
   // the decode that usually follows waits for this grid's completion before its first read
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int IB = In<DT>::bytes;
-  const int per_row = p.D >> 4;           // groups per (token, head) row
-  const int per_tok = p.Hkv * per_row;    // groups per token
-  const int width = min(per_tok, 256);
-  const int rows = 256 / width;
-  const int tl = threadIdx.x / width;
-  const int j0 = threadIdx.x - tl * width;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * rows + tl;
-  if (tl >= rows || t >= p.T) return;
-  const int64_t slot = __ldg(p.slot_mapping + t);
-  if (slot < 0) return;  // padding row: no destination
-  if (slot >= p.num_slots) {
-    if (p.err && j0 == 0) atomicOr(p.err, kErrSlot);
-    return;
-  }
-  const int64_t blk = slot / kBlock;
-  const int off = static_cast<int>(slot % kBlock);
-  for (int j = j0; j < per_tok; j += 256) {  // one turn unless a token is wider than the block
-    const int h = j / per_row, gi = j - h * per_row;
-    const float ks = p.k_scale ? __ldg(p.k_scale + h * p.scale_stride) : 1.f;
-    const float vs = p.v_scale ? __ldg(p.v_scale + h * p.scale_stride) : 1.f;
-    float xk[16], xv[16];
-    load_group<DT>(static_cast<const char *>(p.key) + (t * p.key_ts + h * p.key_hs + gi * 16) * IB, xk);
-    load_group<DT>(static_cast<const char *>(p.value) + (t * p.val_ts + h * p.val_hs + gi * 16) * IB, xv);
-    const int co = fp4_code_off(p.D, off, gi * 8), so = fp4_scale_off(p.D, off, gi);
-    uint2 codes;
-    uint32_t sc;
-    quantise_group(xk, make_divisor(ks), ks == 1.f, codes, sc);
-    char *page = p.k_cache + blk * p.kc_s0 + h * p.kc_s1;
-    *reinterpret_cast<uint2 *>(page + co) = codes;
-    *reinterpret_cast<uint8_t *>(page + so) = static_cast<uint8_t>(sc);
-    quantise_group(xv, make_divisor(vs), vs == 1.f, codes, sc);
-    page = p.v_cache + blk * p.vc_s0 + h * p.vc_s1;
-    *reinterpret_cast<uint2 *>(page + co) = codes;
-    *reinterpret_cast<uint8_t *>(page + so) = static_cast<uint8_t>(sc);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
+  if (t >= p.T) return;
+  const int64_t slot = __ldg(p.slot_mapping + t);  // (not waited for before the rows are asked for)
+  const char *key = static_cast<const char *>(p.key) + times<I32>(t, p.key_ts), *value = static_cast<const char *>(p.value) + times<I32>(t, p.val_ts);
+  for (int h = threadIdx.y; h < p.Hkv; h += blockDim.y) {
+    for (int gi = threadIdx.x; gi < p.D >> 4; gi += blockDim.x) {
+      uint32_t wk[4 * IB], wv[4 * IB];
+      load_group<DT>(key + times<I32>(h, p.key_hs) + gi * (16 * IB), p.wide, wk);
+      load_group<DT>(value + times<I32>(h, p.val_hs) + gi * (16 * IB), p.wide, wv);
+      const float ks = p.k_scale ? __ldg(p.k_scale + h * p.scale_stride) : 1.f;
+      const float vs = p.v_scale ? __ldg(p.v_scale + h * p.scale_stride) : 1.f;
+      if (slot < 0) return;  // padding row: no destination
+      if (slot >= p.num_slots) {
+        if (p.err && threadIdx.x == 0 && threadIdx.y == 0) atomicOr(p.err, kErrSlot);
+        return;
+      }
+      const int64_t blk = slot >> 4;
+      const int off = static_cast<int>(slot) & (kBlock - 1);
+      const int co = fp4_code_off(p.D, off, gi * 8), so = fp4_scale_off(p.D, off, gi);
+      auto store = [&](char *page, const uint3 &c) {
+        *reinterpret_cast<uint2 *>(page + co) = make_uint2(c.x, c.y);
+        *reinterpret_cast<uint8_t *>(page + so) = static_cast<uint8_t>(c.z);
+      };
+      auto quantised = [&](const uint32_t (&w)[4 * IB], float s) {
+        float x[16];
+        group_values<DT>(w, x);
+        if (DT != PA_F32 && s == 1.f) return quantise_group<true>(x, 1.f, 1.f);
+        return quantise_group<false>(x, s, rcp_approx(s));
+      };
+      store(p.k_cache + times<I32>(blk, p.kc_s0) + times<I32>(h, p.kc_s1), quantised(wk, ks));
+      store(p.v_cache + times<I32>(blk, p.vc_s0) + times<I32>(h, p.vc_s1), quantised(wv, vs));
+    }
   }
 }
 
 // ------------------------------------------------------------------- read back
 
-// One group of 16 elements of a cache row -> fp32 values (without the head's scale).
+// One group of 16 elements of a cache row as it lies there (OB: bytes of an element of a 16- or
+// 32-bit cache), and as fp32 values, its head's scale times theirs.
 template <int CT>
-__device__ __forceinline__ void load_cached(const char *c, int64_t s0, int64_t s1, int64_t s2, int D, int64_t blk,
-                                            int off, int h, int gi, float (&x)[16]) {
-  if constexpr (CT == PA_FP4_E2M1) {
-    const char *page = c + blk * s0 + h * s1;
-    const uint2 w = *reinterpret_cast<const uint2 *>(page + fp4_code_off(D, off, gi * 8));
-    const uint32_t s = *reinterpret_cast<const uint8_t *>(page + fp4_scale_off(D, off, gi));
-    const uint32_t sg = e4m3x2_to_f16x2(s | (s << 8));
-    uint32_t v[8];
-    e2m1x8_to_f16x2x4(w.x, v[0], v[1], v[2], v[3]);
-    e2m1x8_to_f16x2x4(w.y, v[4], v[5], v[6], v[7]);
+struct Cached {
+  static constexpr int N = CT == PA_FP4_E2M1 || CT == PA_FP8_E4M3 ? 1 : In<CT == PA_FP4_E2M1 || CT == PA_FP8_E4M3 ? PA_F32 : CT>::bytes;
+  uint4 w[N];  // (4-bit: x, y the codes, z the scale)
+  // src: the row's start (4-bit: its page's)
+  __device__ __forceinline__ void load(const char *src, int D, int off, int gi) {
+    if constexpr (CT == PA_FP4_E2M1) {
+      const char *page = src;
+      const uint2 v = *reinterpret_cast<const uint2 *>(page + fp4_code_off(D, off, gi * 8));
+      const uint32_t s = *reinterpret_cast<const uint8_t *>(page + fp4_scale_off(D, off, gi));
+      w[0] = make_uint4(v.x, v.y, s, 0u);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = unpack_f16(mul_f16x2(v[i], sg));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + gi * (16 * N) + 16 * i);
     }
-  } else if constexpr (CT == PA_FP8_E4M3) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(c + blk * s0 + h * s1 + off * s2 + gi * 16);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  }
+  __device__ __forceinline__ void values(float scale, float (&x)[16]) const {
+    if constexpr (CT == PA_FP4_E2M1) {
+      const uint32_t sg = e4m3x2_to_f16x2(w[0].z | (w[0].z << 8));
+      uint32_t v[8];
+      e2m1x8_to_f16x2x4(w[0].x, v[0], v[1], v[2], v[3]);
+      e2m1x8_to_f16x2x4(w[0].y, v[4], v[5], v[6], v[7]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t lo, hi;
-      e4m3x4_to_f16x2x2(ww[i], lo, hi);
-      const float2 a = unpack_f16(lo), b = unpack_f16(hi);
-      x[4 * i] = a.x;
-      x[4 * i + 1] = a.y;
-      x[4 * i + 2] = b.x;
-      x[4 * i + 3] = b.y;
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = mul2(unpack_f16(mul_f16x2(v[i], sg)), scale);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    } else if constexpr (CT == PA_FP8_E4M3) {
+      const uint32_t ww[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2x2(ww[i], lo, hi);
+        const float2 a = mul2(unpack_f16(lo), scale), b = mul2(unpack_f16(hi), scale);
+        x[4 * i] = a.x;
+        x[4 * i + 1] = a.y;
+        x[4 * i + 2] = b.x;
+        x[4 * i + 3] = b.y;
+      }
+    }
+  }
+};
+
+// N packs of 16 bytes (2 of a 16-bit group, 4 of an fp32 one).  wide: 32-byte aligned.
+template <int N>
+__device__ __forceinline__ void store_packs(char *dst, bool wide, const uint32_t (&w)[4 * N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (wide) {
+      const uint32_t v[8] = {w[8 * i],     w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                             w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+      st32(dst + 32 * i, v);
+    } else {
+      *reinterpret_cast<uint4 *>(dst + 32 * i) = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
+      *reinterpret_cast<uint4 *>(dst + 32 * i + 16) = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
     }
   }
 }
-
 template <int OT>
-__device__ __forceinline__ void store_group(char *dst, const float (&x)[16]) {
+__device__ __forceinline__ void store_group(char *dst, bool wide, const float (&x)[16]) {
+  constexpr int N = In<OT>::bytes;
+  uint32_t w[4 * N];
   if constexpr (OT == PA_F32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4 *>(dst + 16 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
   } else {
-    uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = OT == PA_BF16 ? pack_bf16(x[2 * i], x[2 * i + 1]) : pack_f16(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
   }
+  store_packs<N>(dst, wide, w);
 }
 
-// CT == OT (a cache of the output's own type): bit copies.
-template <int CT, int OT>
+// One thread per group, K and V.  CT == OT (a cache of the output's own type): bit copies.
+// (Two or four tokens per thread, for more loads in flight, leave room for fewer threads: 36.6 and
+// 38.8 us against 34.1 on 32768 rows of 8 x 128, HBM alone 24.)
+template <int CT, int OT, bool I32>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int OB = In<OT>::bytes;
-  const int per_row = p.D >> 4, per_tok = p.Hkv * per_row;
-  const int width = min(per_tok, 256);
-  const int rows = 256 / width;
-  const int tl = threadIdx.x / width;
-  const int j0 = threadIdx.x - tl * width;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * rows + tl;
-  if (tl >= rows || t >= p.T) return;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
+  if (t >= p.T) return;
   const int64_t slot = __ldg(p.slot_mapping + t);
   if (slot < 0) return;  // no source: the output row keeps what it holds
   if (slot >= p.num_slots) {
-    if (p.err && j0 == 0) atomicOr(p.err, kErrSlot);
+    if (p.err && threadIdx.x == 0 && threadIdx.y == 0) atomicOr(p.err, kErrSlot);
     return;
   }
-  const int64_t blk = slot / kBlock;
-  const int off = static_cast<int>(slot % kBlock);
-  for (int j = j0; j < per_tok; j += 256) {
-    const int h = j / per_row, gi = j - h * per_row;
-    char *kd = p.key + (t * p.key_ts + h * p.key_hs + gi * 16) * OB;
-    char *vd = p.value + (t * p.val_ts + h * p.val_hs + gi * 16) * OB;
-    if constexpr (CT == OT) {
-      const char *ks = p.k_cache + blk * p.kc_s0 + h * p.kc_s1 + off * p.kc_s2 + gi * 16 * OB;
-      const char *vs = p.v_cache + blk * p.vc_s0 + h * p.vc_s1 + off * p.vc_s2 + gi * 16 * OB;
-      uint4 a[OB], b[OB];  // 16 elements of OB bytes are OB packs of 16 bytes
-#pragma unroll
-      for (int i = 0; i < OB; ++i) {
-        a[i] = *reinterpret_cast<const uint4 *>(ks + 16 * i);
-        b[i] = *reinterpret_cast<const uint4 *>(vs + 16 * i);
+  const int64_t blk = slot >> 4;
+  const int off = static_cast<int>(slot) & (kBlock - 1);
+  const char *const kc = p.k_cache + times<I32>(blk, p.kc_s0) + times<I32>(off, p.kc_s2);
+  const char *const vc = p.v_cache + times<I32>(blk, p.vc_s0) + times<I32>(off, p.vc_s2);
+  char *const key = p.key + times<I32>(t, p.key_ts), *const value = p.value + times<I32>(t, p.val_ts);
+  for (int h = threadIdx.y; h < p.Hkv; h += blockDim.y) {
+    for (int gi = threadIdx.x; gi < p.D >> 4; gi += blockDim.x) {
+      Cached<CT> ck, cv;
+      ck.load(kc + times<I32>(h, p.kc_s1), p.D, off, gi);
+      cv.load(vc + times<I32>(h, p.vc_s1), p.D, off, gi);
+      char *kd = key + times<I32>(h, p.key_hs) + gi * (16 * OB);
+      char *vd = value + times<I32>(h, p.val_hs) + gi * (16 * OB);
+      if constexpr (CT == OT) {
+        store_packs<OB>(kd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(ck.w));
+        store_packs<OB>(vd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(cv.w));
+      } else {
+        const float ks = p.k_scale ? __ldg(p.k_scale + h * p.scale_stride) : 1.f;
+        const float vs = p.v_scale ? __ldg(p.v_scale + h * p.scale_stride) : 1.f;
+        float x[16];
+        ck.values(ks, x);
+        store_group<OT>(kd, p.wide, x);
+        cv.values(vs, x);
+        store_group<OT>(vd, p.wide, x);
       }
-#pragma unroll
-      for (int i = 0; i < OB; ++i) {
-        *reinterpret_cast<uint4 *>(kd + 16 * i) = a[i];
-        *reinterpret_cast<uint4 *>(vd + 16 * i) = b[i];
-      }
-    } else {
-      const float ks = p.k_scale ? __ldg(p.k_scale + h * p.scale_stride) : 1.f;
-      const float vs = p.v_scale ? __ldg(p.v_scale + h * p.scale_stride) : 1.f;
-      float xk[16], xv[16];
-      load_cached<CT>(p.k_cache, p.kc_s0, p.kc_s1, p.kc_s2, p.D, blk, off, h, gi, xk);
-      load_cached<CT>(p.v_cache, p.vc_s0, p.vc_s1, p.vc_s2, p.D, blk, off, h, gi, xv);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        xk[i] *= ks;
-        xv[i] *= vs;
-      }
-      store_group<OT>(kd, xk);
-      store_group<OT>(vd, xv);
     }
   }
 }
 
-// Grid of a kernel whose CTAs take whole tokens of `per_tok` groups.
-cudaError_t token_grid(int64_t T, int per_tok, unsigned *blocks) {
-  const int rows = 256 / (per_tok < 256 ? per_tok : 256);
-  const int64_t n = (T + rows - 1) / rows;
-  if (n > INT32_MAX) return cudaErrorInvalidValue;
-  *blocks = static_cast<unsigned>(n);
-  return cudaSuccess;
-}
-
+// A block of 256 threads or fewer: groups of a row, heads, tokens.
 template <typename P>
 cudaError_t launch_tokens(void (*kern)(P), const P &p, cudaStream_t st) {
-  unsigned blocks = 0;
-  cudaError_t e = token_grid(p.T, p.Hkv * (p.D / 16), &blocks);
-  if (e != cudaSuccess) return e;
+  const int x = p.D / 16 < 32 ? p.D / 16 : 32, y = p.Hkv < 256 / x ? p.Hkv : 256 / x, fit = 256 / (x * y);
+  const int z = fit < 64 ? fit : 64;
+  const int64_t blocks = (p.T + z - 1) / z;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   // the SM's shared / L1 split stays what the decode kernels ask for (see pa_write.cu)
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  kern<<<blocks, 256, 0, st>>>(p);
+  kern<<<static_cast<unsigned>(blocks), dim3(x, y, z), 0, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+template <int DT>
+cudaError_t launch_write_one(const Fp4WriteParams &p, cudaStream_t st) {
+  return p.i32 ? launch_tokens(write_fp4_kernel<DT, true>, p, st) : launch_tokens(write_fp4_kernel<DT, false>, p, st);
+}
+
+template <int CT, int OT>
+cudaError_t launch_gather_one(const GatherParams &p, cudaStream_t st) {
+  return p.i32 ? launch_tokens(gather_kernel<CT, OT, true>, p, st) : launch_tokens(gather_kernel<CT, OT, false>, p, st);
+}
+
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st) {
   switch (in_dtype) {
-    case PA_F32: return launch_tokens(write_fp4_kernel<PA_F32>, p, st);
-    case PA_BF16: return launch_tokens(write_fp4_kernel<PA_BF16>, p, st);
-    case PA_F16: return launch_tokens(write_fp4_kernel<PA_F16>, p, st);
+    case PA_F32: return launch_write_one<PA_F32>(p, st);
+    case PA_BF16: return launch_write_one<PA_BF16>(p, st);
+    case PA_F16: return launch_write_one<PA_F16>(p, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -300,9 +399,9 @@ cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype,
   auto by_out = [&](auto ct) -> cudaError_t {
     constexpr int CT = decltype(ct)::value;
     switch (out_dtype) {
-      case PA_F32: return launch_tokens(gather_kernel<CT, PA_F32>, p, st);
-      case PA_BF16: return launch_tokens(gather_kernel<CT, PA_BF16>, p, st);
-      case PA_F16: return launch_tokens(gather_kernel<CT, PA_F16>, p, st);
+      case PA_F32: return launch_gather_one<CT, PA_F32>(p, st);
+      case PA_BF16: return launch_gather_one<CT, PA_BF16>(p, st);
+      case PA_F16: return launch_gather_one<CT, PA_F16>(p, st);
       default: return cudaErrorInvalidValue;
     }
   };
@@ -310,9 +409,9 @@ cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype,
   if (cache_dtype == PA_FP8_E4M3) return by_out(std::integral_constant<int, PA_FP8_E4M3>{});
   if (cache_dtype != out_dtype) return cudaErrorInvalidValue;
   switch (out_dtype) {
-    case PA_F32: return launch_tokens(gather_kernel<PA_F32, PA_F32>, p, st);
-    case PA_BF16: return launch_tokens(gather_kernel<PA_BF16, PA_BF16>, p, st);
-    case PA_F16: return launch_tokens(gather_kernel<PA_F16, PA_F16>, p, st);
+    case PA_F32: return launch_gather_one<PA_F32, PA_F32>(p, st);
+    case PA_BF16: return launch_gather_one<PA_BF16, PA_BF16>(p, st);
+    case PA_F16: return launch_gather_one<PA_F16, PA_F16>(p, st);
     default: return cudaErrorInvalidValue;
   }
 }

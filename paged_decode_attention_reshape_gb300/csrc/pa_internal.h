@@ -41,7 +41,7 @@ struct WriteParams {
                                                     // within a block below 2^31 bytes
 };
 
-// The 4-bit cache write (pa_fp4.cu): source strides in elements, cache strides in bytes.
+// The 4-bit cache write (pa_fp4.cu); strides in bytes.
 struct Fp4WriteParams {
   const void *key, *value;
   char *k_cache, *v_cache;
@@ -54,10 +54,12 @@ struct Fp4WriteParams {
   const float *k_scale, *v_scale;  // nullable (1.0)
   int64_t scale_stride;
   int *err;
+  bool wide;                       // every group of 16 elements of the rows is 32-byte aligned
+  bool i32;                        // T, block count and every stride below 2^31
 };
 
-// The read back of cache rows (pa_fp4.cu): output strides in elements, cache strides in bytes
-// (s2, the token stride, is not used by the 4-bit cache).
+// The read back of cache rows (pa_fp4.cu); strides in bytes (s2, the token stride, 0 for the
+// 4-bit cache).
 struct GatherParams {
   char *key, *value;
   const char *k_cache, *v_cache;
@@ -70,6 +72,8 @@ struct GatherParams {
   const float *k_scale, *v_scale;  // nullable (1.0)
   int64_t scale_stride;
   int *err;
+  bool wide;                       // every group of 16 elements of the outputs is 32-byte aligned
+  bool i32;                        // T, block count and every stride below 2^31
 };
 
 struct DecodeParams {

@@ -78,6 +78,19 @@ struct Divisor {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(q));
     return o;
   }
+  // The first correction only: within one ulp, and exact where the quotient is an fp32 number.
+  __device__ __forceinline__ float2 div2_near(float a, float b) const {
+    uint64_t x, sy, ns, q, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(sy) : "f"(y));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ns) : "f"(-s));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(sy));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(ns), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q) : "l"(r), "l"(sy));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(q));
+    return o;
+  }
 };
 
 __device__ __forceinline__ Divisor make_divisor(float s) {

@@ -20,6 +20,11 @@ inline int elem_bytes(int dt) {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Rows [T, H, D] whose every 32-byte piece is 32-byte aligned (element size eb).
+inline bool rows_aligned32(const pa_tensor *t, int eb) {
+  return (reinterpret_cast<uintptr_t>(t->data) & 31u) == 0 && (t->stride[0] * eb) % 32 == 0 && (t->stride[1] * eb) % 32 == 0;
+}
+
 // Descriptor sanity: non-null, rank, element type, positive extents.
 inline int check_desc(const pa_tensor *t, int ndim) {
   if (!t || t->ndim != ndim) return PA_ERR_INVALID_ARG;

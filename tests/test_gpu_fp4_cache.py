@@ -209,3 +209,55 @@ def test_copy_blocks_of_pages():
         ref = ref.clone()
         ref[4], ref[5] = ref[1], ref[0]
         assert torch.equal(ref, got.cpu())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rows_aligned_to_16_bytes_only(dt):
+    """Source and output rows that start 16 bytes off a 32-byte boundary give the same bytes."""
+    T, H, D, NB = 50, 3, 64, 5
+    x = _rows(T, H, D, dt, 4, True)
+    pad = 16 // x.element_size()
+    slots = torch.randperm(NB * 16, generator=torch.Generator().manual_seed(1))[:T].cuda()
+
+    def shifted(fill):
+        flat = torch.full((T * H * D + pad,), fill, dtype=dt, device="cuda")
+        return flat[pad:].view(T, H, D)
+    src = shifted(0.0)
+    src.copy_(x)
+    assert src.data_ptr() % 32 == 16
+    pages = []
+    for rows in (x.cuda(), src):
+        kc = torch.zeros(NB, H, 9 * D, dtype=torch.uint8, device="cuda")
+        vc = torch.zeros_like(kc)
+        assert _write(rows, rows, kc, vc, slots) == (0, 0)
+        assert torch.equal(kc, vc)
+        pages.append(kc)
+    assert torch.equal(*pages)
+    outs = []
+    for make in (lambda: torch.zeros(T, H, D, dtype=dt, device="cuda"), lambda: shifted(0.0)):
+        key, value = make(), make()
+        pa.pa_gather_cache(key, value, pages[0], pages[0], slots)
+        outs += [key, value]
+    for o in outs[1:]:
+        assert torch.equal(outs[0].nan_to_num(7.0), o.nan_to_num(7.0))
+
+
+def test_read_back_of_many_rows():
+    """More rows than one wave of threads."""
+    T, H, D, NB = 20011, 8, 128, 40
+    g = torch.Generator().manual_seed(11)
+    x = _rows(NB * 16, H, D, torch.float32, 3, False)
+    code, sg = oracle.fp4_quantize(x.numpy(), 0.7)
+    pages = np.zeros((NB, H, 9 * D), dtype=np.uint8)
+    oracle.fp4_store(pages, np.arange(NB * 16), code, sg)
+    cache = torch.from_numpy(pages).cuda()
+    slots = torch.randint(-3, NB * 16, (T,), generator=g)
+    want = torch.from_numpy(oracle.fp4_values(code, sg, 0.7)).cuda()[slots.clamp(min=0).cuda()]
+    key = torch.full((T, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    value = key.clone()
+    pa.pa_gather_cache(key, value, cache, cache, slots.cuda(), k_scale=torch.tensor([0.7], device="cuda"),
+                       v_scale=torch.tensor([0.7], device="cuda"))
+    gone = (slots < 0).cuda()
+    for got in (key, value):
+        assert bool((got[gone] == 5.0).all())
+        assert bool(((got.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -24))[~gone].all())
