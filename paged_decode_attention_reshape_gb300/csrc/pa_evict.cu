@@ -11,14 +11,15 @@
 // select_kernel, one CTA per (s, g): the weight of the last token to stay is found digit by
 // digit (radix select on the floats' ordered bit patterns, 11 + 11 + 10 bits: a histogram in
 // shared memory, then the digit in which the count from the top passes what is still wanted),
-// which is exact for any distribution and needs no sort; then one ordered pass writes the
-// kept positions and their weights.  The row is re-read from L2 by each pass.  Bound: 4 bytes
-// a token from HBM once.
+// which is exact for any distribution and needs no sort; then every warp counts and writes its own
+// stretch of the kept positions and their weights, in order.  The passes work on registers for
+// the first 8192 tokens, on L2 behind them.  Bound: 4 bytes a token from HBM once; in fact the
+// passes' latency.
 //
 // move_kernel, one or more CTAs per (s, g) and cache: rows p_0 < p_1 < ... move to rows
 // 0, 1, ....  p_i >= i, so in ascending order a row is only ever overwritten after it has been
 // read, and rows of a later stretch never lie where an earlier one writes: a CTA reads a stretch
-// into registers, meets at a barrier, and writes it.  Rows at the front that stay where they
+// into registers, meets at a barrier, and writes it, with the next one's reads in flight.  Rows at the front that stay where they
 // are (p_i = i) are not touched.  CTAs of one (s, g) take different bytes of the rows.  Bound:
 // every kept row read and written once.
 #include "pa_fp4.cuh"
@@ -49,7 +50,9 @@ struct EvictParams {
 };
 
 constexpr int kSelectThreads = 512;
+constexpr int kWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kHeld = 16;  // tiles of 32 weights that a warp keeps in registers (8192 tokens a CTA)
 
 // Bit patterns that order as the floats do (-0 as +0, NaN below everything).
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
@@ -58,33 +61,11 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Inclusive sum over the block of one value per thread; `scratch` holds a value per warp.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T *scratch, T *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  __syncthreads();  // the scratch may still be read from the scan before
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  T before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    const T t = scratch[w];
-    before += w < warp ? t : 0;
-    all += t;
-  }
-  *total = all;
-  return before + v;
-}
-
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
   __shared__ uint32_t hist[kBins];
-  __shared__ unsigned long long scratch[kSelectThreads / 32];
+  __shared__ uint32_t s_sum[kWarps], s_above[kWarps], s_equal[kWarps];
   __shared__ uint32_t s_digit, s_left;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
   grid_dependency_wait();
   const int len = __ldg(p.seq_lens + s);
@@ -111,6 +92,23 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   const int tail = min(p.recent, p.budget);
   const int cand = len - tail;             // candidates: positions 0 .. cand - 1
   const int want = p.budget - tail;        // of which this many stay (< cand)
+  // Warp w has the candidates [w per, (w + 1) per): `tiles` rows of 32, the first kHeld of them in
+  // registers as ordered bits, the others read again by each pass.
+  const int per = ((cand + kWarps - 1) / kWarps + 31) / 32 * 32, tiles = per / 32;
+  const int first = warp * per + lane;
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    held[j] = j < tiles && first + 32 * j < cand ? ordered_bits(__ldg(w + first + 32 * j)) : 0u;
+  auto each = [&](auto f) {  // f(position, ordered bits, a candidate), whole warps
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (j < tiles) f(first + 32 * j, held[j], first + 32 * j < cand);
+    for (int j = kHeld; j < tiles; ++j) {
+      const int t = first + 32 * j;
+      f(t, t < cand ? ordered_bits(__ldg(w + t)) : 0u, t < cand);
+    }
+  };
   // the threshold: `prefix` holds its leading `done` bits, `left` of the candidates that share
   // them are still wanted
   uint32_t prefix = 0, left = want;
@@ -121,10 +119,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
       for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < cand; i += kSelectThreads) {
-        const uint32_t u = ordered_bits(__ldg(w + i));
-        if (done == 0 || (u >> (32 - done)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      each([&](int, uint32_t u, bool in) {
+        if (in && (done == 0 || (u >> (32 - done)) == prefix)) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+      });
       __syncthreads();
       // counts from the top: thread i holds bins 2047 - 4i .. 2044 - 4i
       uint32_t c[4], sum = 0;
@@ -133,8 +130,17 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
         c[j] = hist[kBins - 1 - 4 * tid - j];
         sum += c[j];
       }
-      unsigned long long total;
-      uint32_t before = static_cast<uint32_t>(block_scan<unsigned long long>(sum, scratch, &total)) - sum;
+      uint32_t before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+      }
+      if (lane == 31) s_sum[warp] = before;
+      before -= sum;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) before += k < warp ? s_sum[k] : 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (before < left && left <= before + c[j]) {
@@ -147,30 +153,38 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       prefix = (prefix << bits) | s_digit;
       left = s_left;
       done += bits;
-      __syncthreads();
     }
-  }
-  // kept candidates in order: all above the threshold, and the first `left` equal to it
-  uint32_t above = 0, equal = 0;  // so far, over the tiles before this one
-  if (want > 0) {
-    for (int t0 = 0; t0 < cand; t0 += kSelectThreads) {
-      const int t = t0 + tid;
-      const float x = t < cand ? __ldg(w + t) : 0.f;
-      const uint32_t u = ordered_bits(x);
-      const bool gt = t < cand && u > prefix, eq = t < cand && u == prefix;
-      const unsigned long long mine = (gt ? 1ull : 0ull) | (eq ? 1ull << 32 : 0ull);
-      unsigned long long total;
-      const unsigned long long incl = block_scan(mine, scratch, &total);
-      const uint32_t a = above + static_cast<uint32_t>(incl) - (gt ? 1u : 0u);
-      const uint32_t e = equal + static_cast<uint32_t>(incl >> 32) - (eq ? 1u : 0u);
+    // kept candidates in order: all above the threshold, and the first `left` equal to it.  Counts per
+    // warp first, then every warp writes its own.
+    uint32_t above = 0, equal = 0;
+    each([&](int, uint32_t u, bool in) {
+      above += __popc(__ballot_sync(0xffffffffu, in && u > prefix));
+      equal += __popc(__ballot_sync(0xffffffffu, in && u == prefix));
+    });
+    if (lane == 0) {
+      s_above[warp] = above;
+      s_equal[warp] = equal;
+    }
+    __syncthreads();
+    above = equal = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      above += k < warp ? s_above[k] : 0u;
+      equal += k < warp ? s_equal[k] : 0u;
+    }
+    each([&](int t, uint32_t u, bool in) {
+      const bool gt = in && u > prefix, eq = in && u == prefix;
+      const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+      const uint32_t lower = (1u << lane) - 1;
+      const uint32_t e = equal + __popc(me & lower);
       if (gt || (eq && e < left)) {
-        const uint32_t at = a + min(e, left);
+        const uint32_t at = above + __popc(mg & lower) + min(e, left);
         kept[at] = t;
-        nw[at] = x;
+        nw[at] = __ldg(w + t);
       }
-      above += static_cast<uint32_t>(total);
-      equal += static_cast<uint32_t>(total >> 32);
-    }
+      above += __popc(mg);
+      equal += __popc(me);
+    });
   }
   for (int i = tid; i < tail; i += kSelectThreads) {
     kept[want + i] = cand + i;
@@ -180,11 +194,12 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   if (g == 0 && tid == 0) p.new_lens[s] = p.budget;
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
+constexpr int kMoveThreads = 256;  // at most: (pieces of a row, rows)
+constexpr int kMoveUnroll = 4;     // rows of a thread in a stretch
 
 // V: the piece of a row that one thread moves at a time (16 bytes, or D / 16 of a 4-bit page: 8
-// pieces of a token's codes and its scales as the ninth).
+// pieces of a token's codes and its scales as the ninth).  The next stretch is read while the
+// last one is written, and its positions one stretch ahead of that.
 template <typename V, bool FP4>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
   const int which = blockIdx.x / p.slices, slice = blockIdx.x - which * p.slices;
@@ -195,18 +210,15 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   const int32_t *bt = p.block_table + s * p.bt_ss;
   char *base = p.cache[which] + g * p.s1[which];
   const int64_t s0 = p.s0[which], s2 = p.s2[which];
-  const int q0 = slice * p.pieces / p.slices, nq = (slice + 1) * p.pieces / p.slices - q0;
-  const int rows = kMoveThreads / nq;  // rows per turn
-  const int r = threadIdx.x / nq, q = q0 + threadIdx.x - r * nq;
-  const bool on = r < rows;
+  const int rows = blockDim.y, r = threadIdx.y, q = slice * blockDim.x + threadIdx.x;
   auto place = [&](int pos) {
     const int64_t blk = __ldg(bt + pos / kBlock);
     const int t = pos % kBlock;
     if constexpr (FP4) {
       const int off = q < 8 ? fp4_code_off(p.D, t, q * static_cast<int>(sizeof(V))) : fp4_scale_off(p.D, t, 0);
-      return base + blk * s0 + off;
+      return reinterpret_cast<V *>(base + blk * s0 + off);
     } else {
-      return base + blk * s0 + t * s2 + q * 16;
+      return reinterpret_cast<V *>(base + blk * s0 + t * s2 + q * 16);
     }
   };
   // the first row that moves: kept[i] - i never falls
@@ -216,25 +228,41 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
     if (__ldcg(kept + mid) == mid) lo = mid + 1;
     else hi = mid;
   }
-  for (int i0 = lo; i0 < p.budget; i0 += rows * kMoveUnroll) {
-    V v[kMoveUnroll];
+  const int stretch = rows * kMoveUnroll;
+  V v[kMoveUnroll], next[kMoveUnroll];
+  int pos[kMoveUnroll];
+  auto positions = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kMoveUnroll; ++k) {
       const int i = i0 + k * rows + r;
-      if (on && i < p.budget) v[k] = __ldcg(reinterpret_cast<const V *>(place(__ldcg(kept + i))));
+      pos[k] = i < p.budget ? __ldcg(kept + i) : -1;
     }
-    __syncthreads();  // every read of the stretch is done before its first write
+  };
+  auto read = [&](V (&to)[kMoveUnroll]) {
+#pragma unroll
+    for (int k = 0; k < kMoveUnroll; ++k)
+      if (pos[k] >= 0) to[k] = __ldcg(place(pos[k]));
+  };
+  positions(lo);
+  read(v);
+  positions(lo + stretch);
+  for (int i0 = lo; i0 < p.budget; i0 += stretch) {
+    read(next);  // of rows behind everything this stretch writes
+    positions(i0 + 2 * stretch);
+    __syncthreads();  // every read of this stretch is done before its first write
 #pragma unroll
     for (int k = 0; k < kMoveUnroll; ++k) {
       const int i = i0 + k * rows + r;
-      if (on && i < p.budget) *reinterpret_cast<V *>(place(i)) = v[k];
+      if (i < p.budget) *place(i) = v[k];
+      v[k] = next[k];
     }
   }
 }
 
 template <typename V, bool FP4>
 cudaError_t launch_move(const EvictParams &p, int S, cudaStream_t st) {
-  return launch_pdl(move_kernel<V, FP4>, dim3(2 * p.slices, p.Hkv, S), dim3(kMoveThreads), 0, st, 1, p);
+  const int x = p.pieces / p.slices;
+  return launch_pdl(move_kernel<V, FP4>, dim3(2 * p.slices, p.Hkv, S), dim3(x, kMoveThreads / x), 0, st, 1, p);
 }
 
 }  // namespace
@@ -313,9 +341,10 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
   if (sm <= 0) return PA_ERR_CUDA;
   // few (sequence, head) pairs: several CTAs share their rows, down to 64 bytes of a row each
   const int64_t units = S * Hkv * 2;
-  const int most = fp4 ? 3 : p.pieces / 4 > 0 ? p.pieces / 4 : 1;
+  const int least = fp4 ? 3 : 4;  // pieces
   p.slices = 1;
-  while (p.slices < most && units * p.slices < 2 * sm) ++p.slices;
+  for (int n = 2; n * least <= p.pieces && units * p.slices < 4 * sm; ++n)
+    if (p.pieces % n == 0) p.slices = n;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(select_kernel, dim3(Hkv, static_cast<unsigned>(S)), dim3(kSelectThreads), 0, st, 1, p);
