@@ -575,7 +575,9 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
   p.i32 = T <= INT32_MAX;
   for (const int64_t x : {p.key_ts, p.key_hs, p.val_ts, p.val_hs, p.kc_s0, p.kc_s1, p.kc_s2, p.vc_s0, p.vc_s1, p.vc_s2})
     p.i32 &= x <= INT32_MAX;
-  return launch_gather(p, cache_dt, out_dt, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const int sm = device_sm_count();
+  if (sm <= 0) return PA_ERR_CUDA;
+  return launch_gather(p, cache_dt, out_dt, sm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API int pa_decode_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_blocks_per_seq,

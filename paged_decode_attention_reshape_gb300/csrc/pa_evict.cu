@@ -13,7 +13,7 @@
 // shared memory, then the digit in which the count from the top passes what is still wanted),
 // which is exact for any distribution and needs no sort; then every warp counts and writes its own
 // stretch of the kept positions and their weights, in order.  The passes work on registers for
-// the first 8192 tokens, on L2 behind them.  Bound: 4 bytes a token from HBM once; in fact the
+// the first 4096 tokens, on L2 behind them.  Bound: 4 bytes a token from HBM once; in fact the
 // passes' latency.
 //
 // move_kernel, one or more CTAs per (s, g) and cache: rows p_0 < p_1 < ... move to rows
@@ -49,10 +49,11 @@ struct EvictParams {
   int *err;
 };
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256;
 constexpr int kWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeld = 16;  // tiles of 32 weights that a warp keeps in registers (8192 tokens a CTA)
+constexpr int kHeld = 16;  // tiles of 32 weights that a warp keeps in registers (4096 tokens a CTA)
+constexpr int kPerThread = kBins / kSelectThreads;
 
 // Bit patterns that order as the floats do (-0 as +0, NaN below everything).
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
@@ -61,7 +62,7 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictParams p) {
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t s_sum[kWarps], s_above[kWarps], s_equal[kWarps];
   __shared__ uint32_t s_digit, s_left;
@@ -123,11 +124,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
         if (in && (done == 0 || (u >> (32 - done)) == prefix)) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
       });
       __syncthreads();
-      // counts from the top: thread i holds bins 2047 - 4i .. 2044 - 4i
-      uint32_t c[4], sum = 0;
+      // counts from the top: thread i holds the kPerThread bins from the i-th group down
+      uint32_t c[kPerThread], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] = hist[kBins - 1 - 4 * tid - j];
+      for (int j = 0; j < kPerThread; ++j) {
+        c[j] = hist[kBins - 1 - kPerThread * tid - j];
         sum += c[j];
       }
       uint32_t before = sum;
@@ -142,9 +143,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) before += k < warp ? s_sum[k] : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kPerThread; ++j) {
         if (before < left && left <= before + c[j]) {
-          s_digit = kBins - 1 - 4 * tid - j;
+          s_digit = kBins - 1 - kPerThread * tid - j;
           s_left = left - before;
         }
         before += c[j];

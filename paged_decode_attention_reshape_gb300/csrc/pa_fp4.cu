@@ -209,7 +209,9 @@ __global__ void __launch_bounds__(256) write_fp4_kernel(const Fp4WriteParams p) 
   if (t >= p.T) return;
   const int64_t slot = __ldg(p.slot_mapping + t);  // (not waited for before the rows are asked for)
   const char *key = static_cast<const char *>(p.key) + times<I32>(t, p.key_ts), *value = static_cast<const char *>(p.value) + times<I32>(t, p.val_ts);
+#pragma unroll 1  // (one turn for most shapes)
   for (int h = threadIdx.y; h < p.Hkv; h += blockDim.y) {
+#pragma unroll 1
     for (int gi = threadIdx.x; gi < p.D >> 4; gi += blockDim.x) {
       uint32_t wk[4 * IB], wv[4 * IB];
       load_group<DT>(key + times<I32>(h, p.key_hs) + gi * (16 * IB), p.wide, wk);
@@ -317,55 +319,80 @@ __device__ __forceinline__ void store_group(char *dst, bool wide, const float (&
   store_packs<N>(dst, wide, w);
 }
 
-// One thread per group, K and V.  CT == OT (a cache of the output's own type): bit copies.
-// (Two or four tokens per thread, for more loads in flight, leave room for fewer threads: 36.6 and
-// 38.8 us against 34.1 on 32768 rows of 8 x 128, HBM alone 24.)
+// CT == OT (a cache of the output's own type): bit copies.  A thread keeps its group of a row and
+// goes over tokens, K and V, the next token's bytes and the slot after that in flight while it
+// widens and stores: a slot and then a row are two trips to memory, and 9 bytes a group keep too
+// little of it busy when every thread makes them once.  32768 rows of 8 x 128 at random slots: 34.6 us;
+// 64 bytes of codes and 8 of scales a row are two bursts of memory, 201 MB in all, 30 us at its rate.
+constexpr int kGatherCtas = 3;  // per SM (4 or 5: 39.1, 37.6 us against 34.6)
 template <int CT, int OT, bool I32>
-__global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(256, kGatherCtas) gather_kernel(const GatherParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int OB = In<OT>::bytes;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
-  if (t >= p.T) return;
-  const int64_t slot = __ldg(p.slot_mapping + t);
-  if (slot < 0) return;  // no source: the output row keeps what it holds
-  if (slot >= p.num_slots) {
-    if (p.err && threadIdx.x == 0 && threadIdx.y == 0) atomicOr(p.err, kErrSlot);
-    return;
-  }
-  const int64_t blk = slot >> 4;
-  const int off = static_cast<int>(slot) & (kBlock - 1);
-  const char *const kc = p.k_cache + times<I32>(blk, p.kc_s0) + times<I32>(off, p.kc_s2);
-  const char *const vc = p.v_cache + times<I32>(blk, p.vc_s0) + times<I32>(off, p.vc_s2);
-  char *const key = p.key + times<I32>(t, p.key_ts), *const value = p.value + times<I32>(t, p.val_ts);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.z;
+#pragma unroll 1  // (one turn for most shapes)
   for (int h = threadIdx.y; h < p.Hkv; h += blockDim.y) {
+#pragma unroll 1
     for (int gi = threadIdx.x; gi < p.D >> 4; gi += blockDim.x) {
+      const char *const kc = p.k_cache + times<I32>(h, p.kc_s1), *const vc = p.v_cache + times<I32>(h, p.vc_s1);
+      char *const key = p.key + times<I32>(h, p.key_hs) + gi * (16 * OB);
+      char *const value = p.value + times<I32>(h, p.val_hs) + gi * (16 * OB);
+      float ks = 1.f, vs = 1.f;
+      if constexpr (CT != OT) {
+        if (p.k_scale) ks = __ldg(p.k_scale + h * p.scale_stride);
+        if (p.v_scale) vs = __ldg(p.v_scale + h * p.scale_stride);
+      }
+      auto slot_of = [&](int64_t t) {  // -1: nothing to read (the output row keeps what it holds)
+        if (t >= p.T) return static_cast<int64_t>(-1);
+        const int64_t slot = __ldg(p.slot_mapping + t);
+        if (slot < p.num_slots) return slot;
+        if (p.err && h == 0 && gi == 0) atomicOr(p.err, kErrSlot);
+        return static_cast<int64_t>(-1);
+      };
+      auto load = [&](int64_t slot, Cached<CT> &ck, Cached<CT> &cv) {
+        if (slot < 0) return;
+        const int64_t blk = slot >> 4;
+        const int off = static_cast<int>(slot) & (kBlock - 1);
+        ck.load(kc + times<I32>(blk, p.kc_s0) + times<I32>(off, p.kc_s2), p.D, off, gi);
+        cv.load(vc + times<I32>(blk, p.vc_s0) + times<I32>(off, p.vc_s2), p.D, off, gi);
+      };
+      int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.z + threadIdx.z;
+      int64_t slot = slot_of(t), slot1 = slot_of(t + stride);
       Cached<CT> ck, cv;
-      ck.load(kc + times<I32>(h, p.kc_s1), p.D, off, gi);
-      cv.load(vc + times<I32>(h, p.vc_s1), p.D, off, gi);
-      char *kd = key + times<I32>(h, p.key_hs) + gi * (16 * OB);
-      char *vd = value + times<I32>(h, p.val_hs) + gi * (16 * OB);
-      if constexpr (CT == OT) {
-        store_packs<OB>(kd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(ck.w));
-        store_packs<OB>(vd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(cv.w));
-      } else {
-        const float ks = p.k_scale ? __ldg(p.k_scale + h * p.scale_stride) : 1.f;
-        const float vs = p.v_scale ? __ldg(p.v_scale + h * p.scale_stride) : 1.f;
-        float x[16];
-        ck.values(ks, x);
-        store_group<OT>(kd, p.wide, x);
-        cv.values(vs, x);
-        store_group<OT>(vd, p.wide, x);
+      load(slot, ck, cv);
+      for (; t < p.T; t += stride) {
+        const int64_t slot2 = slot_of(t + 2 * stride);
+        Cached<CT> nk = ck, nv = cv;
+        load(slot1, nk, nv);
+        if (slot >= 0) {
+          char *kd = key + times<I32>(t, p.key_ts), *vd = value + times<I32>(t, p.val_ts);
+          if constexpr (CT == OT) {
+            store_packs<OB>(kd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(ck.w));
+            store_packs<OB>(vd, p.wide, reinterpret_cast<const uint32_t(&)[4 * OB]>(cv.w));
+          } else {
+            float x[16];
+            ck.values(ks, x);
+            store_group<OT>(kd, p.wide, x);
+            cv.values(vs, x);
+            store_group<OT>(vd, p.wide, x);
+          }
+        }
+        slot = slot1;
+        slot1 = slot2;
+        ck = nk;
+        cv = nv;
       }
     }
   }
 }
 
-// A block of 256 threads or fewer: groups of a row, heads, tokens.
+// Blocks of 256 threads or fewer: groups of a row, heads, tokens; at most `most` of them (0: any).
 template <typename P>
-cudaError_t launch_tokens(void (*kern)(P), const P &p, cudaStream_t st) {
+cudaError_t launch_tokens(void (*kern)(P), const P &p, int64_t most, cudaStream_t st) {
   const int x = p.D / 16 < 32 ? p.D / 16 : 32, y = p.Hkv < 256 / x ? p.Hkv : 256 / x, fit = 256 / (x * y);
   const int z = fit < 64 ? fit : 64;
-  const int64_t blocks = (p.T + z - 1) / z;
+  int64_t blocks = (p.T + z - 1) / z;
+  if (most > 0 && blocks > most) blocks = most;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   // the SM's shared / L1 split stays what the decode kernels ask for (see pa_write.cu)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
@@ -378,12 +405,13 @@ cudaError_t launch_tokens(void (*kern)(P), const P &p, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_write_one(const Fp4WriteParams &p, cudaStream_t st) {
-  return p.i32 ? launch_tokens(write_fp4_kernel<DT, true>, p, st) : launch_tokens(write_fp4_kernel<DT, false>, p, st);
+  return p.i32 ? launch_tokens(write_fp4_kernel<DT, true>, p, 0, st) : launch_tokens(write_fp4_kernel<DT, false>, p, 0, st);
 }
 
 template <int CT, int OT>
-cudaError_t launch_gather_one(const GatherParams &p, cudaStream_t st) {
-  return p.i32 ? launch_tokens(gather_kernel<CT, OT, true>, p, st) : launch_tokens(gather_kernel<CT, OT, false>, p, st);
+cudaError_t launch_gather_one(const GatherParams &p, int sm_count, cudaStream_t st) {
+  const int64_t wave = static_cast<int64_t>(sm_count) * kGatherCtas;
+  return p.i32 ? launch_tokens(gather_kernel<CT, OT, true>, p, wave, st) : launch_tokens(gather_kernel<CT, OT, false>, p, wave, st);
 }
 
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st) {
@@ -395,13 +423,13 @@ cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t
   }
 }
 
-cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, cudaStream_t st) {
+cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, int sm_count, cudaStream_t st) {
   auto by_out = [&](auto ct) -> cudaError_t {
     constexpr int CT = decltype(ct)::value;
     switch (out_dtype) {
-      case PA_F32: return launch_gather_one<CT, PA_F32>(p, st);
-      case PA_BF16: return launch_gather_one<CT, PA_BF16>(p, st);
-      case PA_F16: return launch_gather_one<CT, PA_F16>(p, st);
+      case PA_F32: return launch_gather_one<CT, PA_F32>(p, sm_count, st);
+      case PA_BF16: return launch_gather_one<CT, PA_BF16>(p, sm_count, st);
+      case PA_F16: return launch_gather_one<CT, PA_F16>(p, sm_count, st);
       default: return cudaErrorInvalidValue;
     }
   };
@@ -409,9 +437,9 @@ cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype,
   if (cache_dtype == PA_FP8_E4M3) return by_out(std::integral_constant<int, PA_FP8_E4M3>{});
   if (cache_dtype != out_dtype) return cudaErrorInvalidValue;
   switch (out_dtype) {
-    case PA_F32: return launch_gather_one<PA_F32, PA_F32>(p, st);
-    case PA_BF16: return launch_gather_one<PA_BF16, PA_BF16>(p, st);
-    case PA_F16: return launch_gather_one<PA_F16, PA_F16>(p, st);
+    case PA_F32: return launch_gather_one<PA_F32, PA_F32>(p, sm_count, st);
+    case PA_BF16: return launch_gather_one<PA_BF16, PA_BF16>(p, sm_count, st);
+    case PA_F16: return launch_gather_one<PA_F16, PA_F16>(p, sm_count, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -175,7 +175,7 @@ cudaError_t launch_write(const WriteParams &p, int in_dtype, int cache_dtype, in
                          cudaStream_t st);
 
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st);
-cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, cudaStream_t st);
+cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, int sm_count, cudaStream_t st);
 
 constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND_FP4_F16Q; }
 // Tensor-core kernel shape per (kind, head size): warps per CTA and pipeline
