@@ -131,7 +131,8 @@ typedef struct {
  *   slot_mapping  PA_I64 [T].  Row t goes to cache slot slot_mapping[t];
  *                 a negative entry writes nothing for row t.  Entries
  *                 >= num_blocks * 16 write nothing and set PA_DEVERR_SLOT_RANGE.
- *                 Two rows naming the same slot: which one lands is unspecified.
+ *                 Two rows naming the same slot: which one lands is unspecified (piece by
+ *                 piece, so what lies there then need not be one of them).
  *   kv_dtype      PA_KV_AUTO: bit-exact copy.  PA_KV_FP8_E4M3: each element x is
  *                 stored as E4M3(fp32(x) / scale) -- one IEEE fp32 division
  *                 rounded to nearest, then round-to-nearest-even to E4M3 with
@@ -215,7 +216,8 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  *   q             [S, Hq, D], PA_F32 / PA_BF16 / PA_F16, innermost stride 1.
  *   k_cache,      [num_blocks, Hkv, 16, D]; element type == q's, or PA_FP8_E4M3
  *   v_cache       with a PA_BF16 / PA_F16 query; or [num_blocks, Hkv, 9 D] 4-bit pages
- *                 (PA_FP4_E2M1) with a PA_BF16 / PA_F16 query.
+ *                 (PA_FP4_E2M1) with a PA_BF16 / PA_F16 query. 4-bit caches: at least one
+ *                 block, block strides below 4 GiB.
  *   block_table   PA_I32 [S, max_blocks_per_seq], innermost stride 1.  Only the
  *                 first ceil(seq_lens[s] / 16) entries of row s are used; the
  *                 rest may hold any value (padding).
@@ -362,6 +364,7 @@ size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_
  *   block_table       PA_I32 [S, max_blocks_per_seq]; the first ceil(L / 16) entries of a row
  *   seq_lens          are used.  PA_I32 [S].
  *   weights           PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16.  Read only.
+ *   budget, recent    host ints; 1 <= budget <= 2^30, recent >= 0.
  *   kept              PA_I32 [S, Hkv, budget], written: the positions kept, ascending, then
  *                     -1 where the sequence is shorter than the budget.
  *   new_seq_lens      PA_I32 [S], written: min(L, budget).  Not the memory of seq_lens.
@@ -592,7 +595,9 @@ const char *pa_status_string(int status);
  * pair of CUDA events recorded on its launch stream.  pa_profile_read
  * synchronises on the recorded events, returns the summed device time (ms) and
  * the launch count for one kernel kind since the last read, and clears them.
- *   kind: 0 = cache write, 1 = decode (attention with the fused split-KV merge).
+ *   kind: 0 = cache write, 1 = decode (attention with the fused split-KV merge; the second
+ *   kernel of pa_decode_accumulate counts here too).  pa_gather_cache, pa_evict and
+ *   pa_copy_blocks are not bracketed.
  */
 #define PA_KERNEL_WRITE 0
 #define PA_KERNEL_DECODE 1

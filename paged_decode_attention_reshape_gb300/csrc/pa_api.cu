@@ -342,7 +342,10 @@ int internal_workspace(size_t counters, size_t data, cudaStream_t st, DevWorkspa
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return PA_ERR_CUDA;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
   std::lock_guard<std::mutex> g(g_ws_mu);
   DevWorkspace &w = g_ws[dev];
   if (w.counters < counters || w.bytes - w.counters < data) {
@@ -864,7 +867,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
       e = launch_decode_mma_fp8(p, kind, tmK, tmV, st);
     }
   }
-  if (e == cudaSuccess && weights) {
+  if (e == cudaSuccess && weights && maxNB > 0) {
     WeightsParams w{};
     w.seq_lens = p.seq_lens;
     w.scores = p.scores;

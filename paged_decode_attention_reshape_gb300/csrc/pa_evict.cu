@@ -293,7 +293,7 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
     return PA_ERR_INVALID_ARG;
   if (weights->shape[1] != Hkv || kept->shape[1] != Hkv || new_weights->shape[1] != Hkv) return PA_ERR_INVALID_ARG;
   if (kept->shape[2] != budget || new_weights->shape[2] != W) return PA_ERR_INVALID_ARG;
-  if (S > 65535 || MB > INT32_MAX / kBlock || W > INT32_MAX) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (S > 65535 || MB > INT32_MAX / kBlock || W > INT32_MAX || budget > (1 << 30)) return PA_ERR_UNSUPPORTED_SHAPE;
   if (W < MB * kBlock) return PA_ERR_INVALID_ARG;
   if (block_table->stride[1] != 1 || seq_lens->stride[0] != 1 || weights->stride[2] != 1 || kept->stride[2] != 1 ||
       new_seq_lens->stride[0] != 1 || new_weights->stride[2] != 1)
@@ -301,12 +301,11 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
   const int eb = elem_bytes(cdt);
   if (!fp4 && (D <= 0 || (static_cast<int64_t>(D) * eb) % 16 || static_cast<int64_t>(D) * eb > 16 * kMoveThreads))
     return PA_ERR_UNSUPPORTED_SHAPE;
-  if (S == 0 || Hkv == 0 || MB == 0) return PA_OK;
-  if (!block_table->data || !seq_lens->data || !weights->data || !kept->data || !new_seq_lens->data ||
-      !new_weights->data)
-    return PA_ERR_INVALID_ARG;
+  if (S == 0 || Hkv == 0) return PA_OK;
+  if ((MB > 0 && !block_table->data) || !seq_lens->data || !kept->data || !new_seq_lens->data) return PA_ERR_INVALID_ARG;
+  if (W > 0 && (!weights->data || !new_weights->data)) return PA_ERR_INVALID_ARG;
   // read by every CTA of a sequence while others write the new ones
-  if (new_weights->data == weights->data || new_seq_lens->data == seq_lens->data) return PA_ERR_INVALID_ARG;
+  if ((W > 0 && new_weights->data == weights->data) || new_seq_lens->data == seq_lens->data) return PA_ERR_INVALID_ARG;
 
   EvictParams p{};
   const pa_tensor *c[2] = {k_cache, v_cache};

@@ -59,6 +59,7 @@ def test_refusals(L):
     assert _evict(L, k=big, v=big) == -7
     page = _t([NB, H, 9 * 96], pa.PA_FP4_E2M1)
     assert _evict(L, k=page, v=page) == -7
+    assert _evict(L, budget=(1 << 30) + 1, kept=_t([S, H, (1 << 30) + 1], I, ptr=0x20000)) == -7
     none = dict(bt=_t([0, MB], I), sl=_t([0], I), w=_t([0, H, MB * 16], F), kept=_t([0, H, B], I),
                 nl=_t([0], I), nw=_t([0, H, MB * 16], F))
     assert _evict(L, **none) == 0                                            # an empty batch

@@ -126,6 +126,10 @@ def test_decode_and_accumulate_refusals(L):
     assert _decode(L, out, q, page, _t([NB, H, 16, D], pa.PA_BF16), bt, sl, H) == -1
     assert _decode(L, out, q, _t([NB, H, 16, D], pa.PA_FP4_E2M1), page, bt, sl, H) == -1
     assert _decode(L, out, q, page, page, bt, sl, 3) == -1
+    none_at_all = _t([0, H, 9 * D], pa.PA_FP4_E2M1)
+    assert _decode(L, out, q, none_at_all, none_at_all, bt, sl, H) == -1            # no block to stand in
+    wide = _t([NB, H, 9 * D], pa.PA_FP4_E2M1, strides=[1 << 32, 9 * D, 1])
+    assert _decode(L, out, q, wide, page, bt, sl, H) == -7                          # block stride of 4 GiB
     w = _t([S, H, MB * 16], pa.PA_F32)
     none = pa.PaDecodeOptions()
     assert _accumulate(L, out, q, page, page, bt, sl, H, None) == -1

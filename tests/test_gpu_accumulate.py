@@ -194,3 +194,16 @@ def test_many_sequences_over_a_4_bit_cache():
     assert pa.pa_check_device_error(g.err) == (-6, pa.PA_DEVERR_BLOCK_RANGE)
     got = weights.double().cpu().numpy()
     assert not got[[2, 4]].any() and got[3].any()
+
+
+def test_one_column_tables_and_tokens():
+    """The shortest call: one sequence of one token, whose weight is 1 for every query head."""
+    for kind in ("fp4", "bf16"):
+        c = fp4_cases.make(1, 4, 2, 64, [1], torch.bfloat16, seed=1) if kind == "fp4" else make_case(
+            1, 4, 2, 64, [1], seed=1)
+        g = fp4_cases.to_gpu(c) if kind == "fp4" else to_gpu(c)
+        weights = torch.full((1, 2, g.block_table.shape[1] * 16), 0.25, device="cuda")
+        pa.pa_decode_accumulate(*_args(c, g), weights, device_error=g.err)
+        assert pa.pa_check_device_error(g.err) == (0, 0)
+        assert torch.allclose(weights[:, :, 0], torch.full((1, 2), 2.25, device="cuda"), atol=1e-6)
+        assert bool((weights[:, :, 1:] == 0.25).all())

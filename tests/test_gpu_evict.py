@@ -247,3 +247,20 @@ def test_generation_under_a_budget(D):
             evictions += 1
         assert pa.pa_check_device_error(err) == (0, 0)
     assert evictions >= 4 and G == 4
+
+
+def test_empty_tables():
+    """A batch whose table has no columns: every length is 0 and every output is written."""
+    kc = torch.zeros(2, 3, 16, 64, dtype=torch.bfloat16, device="cuda")
+    sl = torch.tensor([0, 0, 5], dtype=torch.int32, device="cuda")
+    kept = torch.full((3, 3, 4), 9, dtype=torch.int32, device="cuda")
+    nl = torch.full((3,), 9, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for W in (0, 7):
+        w = torch.ones(3, 3, W, device="cuda")
+        nw = torch.full_like(w, 9.0)
+        pa.pa_evict(kc, kc.clone(), torch.zeros(3, 0, dtype=torch.int32, device="cuda"), sl, w, 4, 1, kept, nl, nw,
+                    device_error=err)
+        assert pa.pa_check_device_error(err) == (-6, pa.PA_DEVERR_SEQLEN_RANGE)
+        assert bool((kept == -1).all()) and nl.tolist() == [0, 0, 5]
+        assert not bool(nw[:2].any()) and bool((nw[2] == 1).all())

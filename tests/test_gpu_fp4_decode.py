@@ -314,3 +314,68 @@ def test_more_sequences_than_the_balanced_split_takes():
     g = fp4_cases.to_gpu(c)
     assert _decode(c, g, 0) == (0, 0)
     fp4_cases.check(g.out, ref, tol, "520 sequences")
+
+
+# ------------------------------------------------------------------------- far offsets
+
+def _far_case(c, kc, vc, base):
+    """Case c's pages moved to blocks base .. of larger caches."""
+    kc[base:base + c.NB] = torch.from_numpy(c.pool[0]).cuda()
+    vc[base:base + c.NB] = torch.from_numpy(c.pool[1]).cuda()
+    return torch.from_numpy(np.where(c.table >= 0, c.table + base, -1).astype(np.int32)).cuda()
+
+
+def test_caches_past_4_gib():
+    """Pages, rows read back, rows written and rows moved at byte offsets above 2^32."""
+    D, Hkv = 128, 8
+    c = fp4_cases.make(3, 16, Hkv, D, [300, 40, 1], seed=12)
+    base = (1 << 32) // (Hkv * 9 * D) + 1000
+    NB = base + c.NB
+    kc = torch.empty(NB, Hkv, 9 * D, dtype=torch.uint8, device="cuda")
+    vc = torch.empty_like(kc)
+    g = fp4_cases.to_gpu(c)
+    g.block_table = _far_case(c, kc, vc, base)
+    g.k_cache, g.v_cache = kc, vc
+    ref, tol, _ = fp4_cases.reference(c)
+    for P in (-1, 64):
+        assert _decode(c, g, P) == (0, 0)
+        fp4_cases.check(g.out, ref, tol, "partition %d" % P)
+    slots = (g.block_table[0, :3].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()
+    key = torch.zeros(48, Hkv, D, device="cuda")
+    value = torch.zeros_like(key)
+    pa.pa_gather_cache(key, value, kc, vc, slots)
+    assert np.array_equal(key.double().cpu().numpy(), c.K[0][:48])
+    assert np.array_equal(value.double().cpu().numpy(), c.V[0][:48])
+    pa.pa_reshape_and_cache(value, key, kc, vc, slots, pa.PA_KV_FP4_E2M1)      # swapped: values of the format stay
+    pa.pa_gather_cache(key, value, kc, vc, slots)
+    assert np.abs(key.double().cpu().numpy() - c.V[0][:48]).max() <= 0.5 * np.abs(c.V[0][:48]).max()
+    w = torch.arange(c.width * 16, device="cuda", dtype=torch.float32).expand(3, Hkv, -1).contiguous()
+    kept = torch.zeros(3, Hkv, 100, dtype=torch.int32, device="cuda")
+    nl, nw = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros_like(w)
+    pa.pa_evict(kc, vc, g.block_table, g.seq_lens, w, 100, 0, kept, nl, nw)
+    assert kept[0, 0, 0] == 200 and nl.tolist() == [100, 40, 1]
+    pa.pa_gather_cache(key, value, kc, vc, slots)
+    assert np.array_equal(key.double().cpu().numpy(), c.K[0][200:248])
+    assert np.array_equal(value.double().cpu().numpy(), c.V[0][200:248])
+
+
+def test_block_stride_past_2_gib():
+    """Strides that a 32-bit number does not hold (the write's and the read back's other variant)."""
+    D, far = 64, (1 << 31) + 4096
+    c = fp4_cases.make(1, 2, 1, D, [30], seed=13)
+    raw = torch.empty(far + c.NB * 9 * D, dtype=torch.uint8, device="cuda")
+    kc = raw.as_strided((2, 1, 9 * D), (far, 9 * D, 1))
+    rows = torch.from_numpy(np.random.RandomState(1).randn(32, 1, D).astype(np.float32)).cuda()
+    slots = torch.arange(32, device="cuda")
+    vc = torch.zeros(2, 1, 9 * D, dtype=torch.uint8, device="cuda")
+    pa.pa_reshape_and_cache(rows, rows, kc, vc, slots, pa.PA_KV_FP4_E2M1)
+    assert torch.equal(kc[0], vc[0]) and torch.equal(kc[1], vc[1])
+    a, b = torch.zeros_like(rows), torch.zeros_like(rows)
+    pa.pa_gather_cache(a, b, kc, vc, slots)
+    assert torch.equal(a, b) and bool(a.any())
+    out, ref = torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda")
+    bt, sl = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), torch.tensor([30], dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, D, device="cuda").to(torch.bfloat16)
+    pa.pa_decode(out, q, kc, kc, bt, sl, 0.1, 1)
+    pa.pa_decode(ref, q, vc, vc, bt, sl, 0.1, 1)
+    assert torch.equal(out, ref)
