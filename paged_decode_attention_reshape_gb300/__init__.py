@@ -14,6 +14,7 @@ slot_mapping int64.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -179,21 +180,26 @@ def desc(t: torch.Tensor, dtype_code: int | None = None) -> PaTensor:
 # A call's descriptors and options go to the library as packed bytes of the C structs (native
 # layout), whose addresses ctypes passes on: an order of magnitude less work per call than filling
 # ctypes structures element by element, which is what a small call's time is made of.
-_TENSOR = struct.Struct("@Pii10q")
+_POINTER = struct.Struct("@P")
+_SHAPE = struct.Struct("@ii10q")
 _WRITE_OPTIONS = struct.Struct("@PPqP")
 _DECODE_OPTIONS = struct.Struct("@PPqPiPNPi0P")
 _PAD = ((0,) * 5, (0,) * 4, (0,) * 3, (0,) * 2, (0,), ())  # extents behind the rank
 
 
-def _desc(t: torch.Tensor, dtype_code: int | None = None) -> bytes:
-    """The pa_tensor of a torch tensor as the struct's bytes."""
-    shape = t.shape
+@functools.lru_cache(maxsize=4096)
+def _geometry(dtype_code: int, shape, stride) -> bytes:
+    """The part of a pa_tensor behind its pointer."""
     n = len(shape)
     if n > 5:
         raise ValueError("rank > 5")
-    pad = _PAD[n]
-    return _TENSOR.pack(t.data_ptr() if t.numel() else 0, _DT[t.dtype] if dtype_code is None else dtype_code, n,
-                        *shape, *pad, *t.stride(), *pad)
+    return _SHAPE.pack(dtype_code, n, *shape, *_PAD[n], *stride, *_PAD[n])
+
+
+def _desc(t: torch.Tensor, dtype_code: int | None = None) -> bytes:
+    """The pa_tensor of a torch tensor as the struct's bytes."""
+    return _POINTER.pack(t.data_ptr() if t.numel() else 0) + _geometry(
+        _DT[t.dtype] if dtype_code is None else dtype_code, t.shape, t.stride())
 
 
 def _cache(t: torch.Tensor) -> bytes:

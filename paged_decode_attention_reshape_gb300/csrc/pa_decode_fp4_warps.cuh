@@ -367,9 +367,12 @@ struct Fp4WarpsLaunch {
   template <bool ACC>
   static cudaError_t launch_variant(const DecodeParams &p, int ctas, cudaStream_t st) {
     auto kern = decode_fp4_warps_kernel<KIND, D, W, ST, ACC>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [kern] {
+      cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
+      if (r != cudaSuccess) return r;
+      return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    });
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, 1, p);
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -938,11 +938,14 @@ struct MmaLaunch {
 
   template <bool PLAIN, bool EARLY, bool ACC>
   static cudaError_t attrs() {
-    auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
-    if (e != cudaSuccess) return e;
-    // same shared/L1 split as the cache write that usually precedes it (no reconfiguration)
-    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    static std::atomic<uint64_t> done{0};
+    return once_per_device(done, [] {
+      auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>;
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
+      if (e != cudaSuccess) return e;
+      // same shared/L1 split as the cache write that usually precedes it (no reconfiguration)
+      return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    });
   }
   template <bool PLAIN, bool EARLY, bool ACC>
   static cudaError_t launch_variant(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,

@@ -387,15 +387,18 @@ __global__ void __launch_bounds__(256, kGatherCtas) gather_kernel(const GatherPa
 }
 
 // Blocks of 256 threads or fewer: groups of a row, heads, tokens; at most `most` of them (0: any).
-template <typename P>
-cudaError_t launch_tokens(void (*kern)(P), const P &p, int64_t most, cudaStream_t st) {
+template <auto kern, typename P>
+cudaError_t launch_tokens(const P &p, int64_t most, cudaStream_t st) {
   const int x = p.D / 16 < 32 ? p.D / 16 : 32, y = p.Hkv < 256 / x ? p.Hkv : 256 / x, fit = 256 / (x * y);
   const int z = fit < 64 ? fit : 64;
   int64_t blocks = (p.T + z - 1) / z;
   if (most > 0 && blocks > most) blocks = most;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   // the SM's shared / L1 split stays what the decode kernels ask for (see pa_write.cu)
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  });
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(blocks), dim3(x, y, z), 0, st>>>(p);
   return cudaGetLastError();
@@ -405,13 +408,14 @@ cudaError_t launch_tokens(void (*kern)(P), const P &p, int64_t most, cudaStream_
 
 template <int DT>
 cudaError_t launch_write_one(const Fp4WriteParams &p, cudaStream_t st) {
-  return p.i32 ? launch_tokens(write_fp4_kernel<DT, true>, p, 0, st) : launch_tokens(write_fp4_kernel<DT, false>, p, 0, st);
+  return p.i32 ? launch_tokens<write_fp4_kernel<DT, true>>(p, 0, st) : launch_tokens<write_fp4_kernel<DT, false>>(p, 0, st);
 }
 
 template <int CT, int OT>
 cudaError_t launch_gather_one(const GatherParams &p, int sm_count, cudaStream_t st) {
   const int64_t wave = static_cast<int64_t>(sm_count) * kGatherCtas;
-  return p.i32 ? launch_tokens(gather_kernel<CT, OT, true>, p, wave, st) : launch_tokens(gather_kernel<CT, OT, false>, p, wave, st);
+  return p.i32 ? launch_tokens<gather_kernel<CT, OT, true>>(p, wave, st)
+               : launch_tokens<gather_kernel<CT, OT, false>>(p, wave, st);
 }
 
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st) {

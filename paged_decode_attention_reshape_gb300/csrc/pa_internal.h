@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/pa.h"
@@ -235,6 +236,19 @@ int occupancy_decode_mma_fp8(int kind, int D);
 int occupancy_decode_mma_fp4(int kind, int D);
 // 4-bit caches, the balanced split over the warps of `ctas` CTAs (p.flat warps per head row).
 cudaError_t launch_decode_fp4_warps(const DecodeParams &p, int kind, int ctas, cudaStream_t st);
+
+// Runs `set` (a kernel's function attributes) once per device; `done` is the kernel's own mask.  The
+// attributes are the device's, and setting them takes about as long on the host as the launch.
+template <typename Set>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, Set set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if ((e = set()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Launch `kern` as a programmatic dependent of the previous work on `st`, in
 // thread-block clusters of `cluster_x` CTAs along x when cluster_x > 1.
