@@ -1,14 +1,14 @@
 // pa_decode_fp4.cuh -- the page loop of the tensor-core decode over 4-bit (E2M1) pages; the work
 // split, the merges and the variants are pa_decode_mma.cuh's.
 //
-// A stage is NP pages of K and of V (two, four at head size 64), brought by 16-byte asynchronous
+// A stage is NP pages of K and of V (two; four at head size 64, one at 256), brought by 16-byte asynchronous
 // copies: a page's codes are whole 512-byte runs of the warp, and the scales of the stage's 2 NP
 // pages share the last ones, so a stage of head size 128 costs nine copies and five addresses.
-// (One bulk copy per page and a barrier per stage cost about 30 more instructions a page, in one
-// lane: 147.5 against 126 us on 128 x 1k..8k tokens, 64/8 heads.)  At HBM rate an SM has to
-// take 23 bytes, 41 elements, a clock, and the widening alone is half a conversion an element on a
-// pipe that does 64 lanes a clock (measured: 43 elements' worth of conversions and as many other
-// operations in the same pipe already saturate it), so the loop is built to do little else:
+// (One bulk copy per page and a barrier per stage: 147.5 against 135.6 us on 128 x 1k..8k tokens,
+// 64/8 heads.)  At HBM rate an SM has to take 23 bytes, 41 elements, a clock, and the widening
+// alone is half a conversion an element on a pipe that does 64 lanes a clock (measured, and shared
+// with bit selects and shuffles of bytes), so the loop is built to do little else, 272 warp
+// instructions a page pair at head size 128:
 //
 //   K: lane (r, c) holds a run of 32 (D = 64: 16) elements of tokens r and r + 8, whole scale
 //      groups.  Codes are widened to f16x2 (cvt e2m1x2), each pair multiplied by its group's

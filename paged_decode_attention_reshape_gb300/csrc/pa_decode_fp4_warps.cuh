@@ -14,10 +14,9 @@
 // depend on which it is).  The warps of a CTA have neighbouring ranges, and where all of a unit's
 // parts are its own they meet in shared memory: a part that ends a warp's range lies in the
 // warp's stage buffers, free by then, and the one that begins a range and is followed by others
-// in the workspace.  Parts of several CTAs all go through the workspace, which costs a warp about
-// 2 us a part (store, release, counter) and the last one 2 more: the split pays where most units
-// stay whole.  Measured: 304 x 256 tokens 21.6 us; 256 x 512..4096 124.0 us against 139.3 for a CTA
-// per unit, HBM alone 101; but 64 x 0..2048 (head size 64, five parts a unit) 26.4 against 18.5.
+// in the workspace.  Parts of several CTAs all go through the workspace (store, release, counter,
+// and a merge by the last): the split pays where most units stay whole.
+// Measured: 304 x 256 tokens 21.4 us; 256 x 512..4096 122.6 us against 139.0 for a CTA per unit, HBM alone 101; but 64 x 0..2048 (head size 64, five parts a unit) 26.4 against 18.5.
 #pragma once
 
 #include "pa_decode_mma.cuh"

@@ -185,10 +185,12 @@ constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND
 // (measured on GB300: one 2 KiB K+V page pair per warp about every 0.5 us with the
 // page math, 2 to 4 stages alike), so the warps per CTA set how fast one long
 // sequence streams.  Head size 64: 8 warps (3 CTAs per SM); 128 and 256: 4 warps,
-// whose larger pages already fill HBM with 3 CTAs per SM.
+// whose larger pages already fill HBM with 3 CTAs per SM.  4-bit pages are smaller: 8 warps at
+// head size 128 too (2, 4, 16 warps: 180, 138, 150 us against 125 on 128 x 1k..8k, 64/8 heads).
 constexpr int mma_warps(int kind, int D) { return D == 64 || (mma_fp4(kind) && D == 128) ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
+// (4-bit pages at head size 256, one to a stage: three; at 128 three measured 156 us against 148.)
 constexpr int mma_stages(int kind, int D) { return mma_fp4(kind) && D == 256 ? 3 : 2; }
 // Resident CTAs per SM the register allocation must allow (ptxas launch bound): as
 // many as the shared memory admits, so registers never cut the occupancy, except
@@ -202,7 +204,7 @@ constexpr int mma_page_bytes(int kind, int D) {
   return mma_fp4(kind) ? 9 * D : kBlock * D * (mma_fp8(kind) ? 1 : 2);
 }
 // Pages of one stage.  4-bit pages are small (1152 bytes at head size 128) and cheap to multiply,
-// so several share a stage, and with it a barrier wait, the running maximum's vote and the loop.
+// so several share a stage, and with it a wait, the running maximum's vote and the loop.
 constexpr int mma_stage_pages(int kind, int D) { return !mma_fp4(kind) || D == 256 ? 1 : D == 64 ? 4 : 2; }
 constexpr size_t kMmaScratch = 2048;  // sequence-order ranking scratch (after the barriers)
 constexpr size_t mma_smem(int kind, int D) {

@@ -16,7 +16,7 @@
 // The E4M3 path divides by the tensor's scale, or its KV head's
 // (Part 2: kv_scale_stride == 0 shares one scale, otherwise head h uses
 // scale[h * kv_scale_stride]), with a reciprocal-based, correctly rounded quotient
-// (Divisor below), the same value as an IEEE division.
+// (Divisor in pa_quant.cuh), the same value as an IEEE division.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_quant.cuh"
