@@ -217,7 +217,7 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  *   k_cache,      [num_blocks, Hkv, 16, D]; element type == q's, or PA_FP8_E4M3
  *   v_cache       with a PA_BF16 / PA_F16 query; or [num_blocks, Hkv, 9 D] 4-bit pages
  *                 (PA_FP4_E2M1) with a PA_BF16 / PA_F16 query. 4-bit caches: at least one
- *                 block, block strides below 4 GiB.
+ *                 block, block strides below 4 GiB, at most 2^26 blocks a sequence.
  *   block_table   PA_I32 [S, max_blocks_per_seq], innermost stride 1.  Only the
  *                 first ceil(seq_lens[s] / 16) entries of row s are used; the
  *                 rest may hold any value (padding).
@@ -259,8 +259,8 @@ int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, cons
  *                     split: the pages of all sequences, concatenated, cut into equal
  *                     ranges over one resident wave of CTAs per (kv head, head group),
  *                     the parts of a cut sequence merged through the workspace
- *                     (batches of at most 511 sequences, else
- *                     PA_ERR_UNSUPPORTED_SHAPE; the fp32 cache runs it unsplit; over a
+ *                     (batches of at most 511 sequences and, over a 4-bit cache, 2^31 - 1
+ *                     table entries, else PA_ERR_UNSUPPORTED_SHAPE; the fp32 cache runs it unsplit; over a
  *                     4-bit cache the ranges belong to single warps where the batch has
  *                     many (sequence, KV head) pairs, and 0 chooses this split too).
  *   workspace,        device memory for split-KV partition states; at least

@@ -248,6 +248,7 @@ bool plan_fp4(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool d
   const int64_t ctas = static_cast<int64_t>(std::max(sm, 1)) * mma_min_ctas(kind, D);
   const int64_t workers = ctas * mma_warps(kind, D);
   if (S > kFlatMaxSeqs || varlen) return false;
+  if (static_cast<int64_t>(S) * maxNB > INT32_MAX) return false;  // stages are numbered in 32 bits
   if (plain && (balanced ? units * 8 >= workers : units * 3 >= workers * 2) && rows <= ctas) {
     pl->warps = 1;
     pl->flat = static_cast<int>(ctas / rows) * mma_warps(kind, D);
@@ -268,7 +269,8 @@ Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool 
     return pl;
   if (request == PA_PARTITION_BALANCED) {
     if (kind == KIND_F32) return pl;  // the CUDA-core kernel runs it unsplit
-    if (S > kFlatMaxSeqs) pl.status = PA_ERR_UNSUPPORTED_SHAPE;
+    if (S > kFlatMaxSeqs || (mma_fp4(kind) && static_cast<int64_t>(S) * maxNB > INT32_MAX))
+      pl.status = PA_ERR_UNSUPPORTED_SHAPE;
     else if (mma_fp4(kind) && plan_fp4(S, Hq, Hkv, D, maxNB, kind, sm, device, varlen, plain, true, &pl)) return pl;
     else pl.flat = balanced_ctas(Hq, Hkv, D, kind, sm, device);
     return pl;
@@ -700,6 +702,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   if (mma_fp4(kind)) {  // block 0 stands in for entries behind a sequence; 32-bit block strides
     if (NB == 0 && S64 > 0) return PA_ERR_INVALID_ARG;
     if (k_cache->stride[0] > UINT32_MAX || v_cache->stride[0] > UINT32_MAX) return PA_ERR_UNSUPPORTED_SHAPE;
+    if (block_table->shape[1] > (1 << 26)) return PA_ERR_UNSUPPORTED_SHAPE;  // lengths rounded up to stages of 64 tokens
   }
   if (S64 > 65535 || Hq64 > 65535 || block_table->shape[1] > (INT32_MAX / kBlock)) return PA_ERR_UNSUPPORTED_SHAPE;
   if (early && new_rows_start) {
