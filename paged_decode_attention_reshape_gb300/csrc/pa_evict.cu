@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
   }
   const int tail = min(p.recent, p.budget);
   const int cand = len - tail;             // candidates: positions 0 .. cand - 1
-  const int want = p.budget - tail;        // of which this many stay (< cand)
+  const uint32_t want = p.budget - tail;   // of which this many stay (< cand)
   // Warp w has the candidates [w per, (w + 1) per): `tiles` rows of 32, the first kHeld of them in
   // registers as ordered bits, the others read again by each pass.
   const int per = ((cand + kWarps - 1) / kWarps + 31) / 32 * 32, tiles = per / 32;
@@ -180,8 +180,10 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
       const uint32_t e = equal + __popc(me & lower);
       if (gt || (eq && e < left)) {
         const uint32_t at = above + __popc(mg & lower) + min(e, left);
-        kept[at] = t;
-        nw[at] = __ldg(w + t);
+        if (at < want) {  // always, unless the weights change during the call
+          kept[at] = t;
+          nw[at] = __ldg(w + t);
+        }
       }
       above += __popc(mg);
       equal += __popc(me);
@@ -207,13 +209,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
   const int g = blockIdx.y, s = blockIdx.z;
   grid_dependency_wait();
   const int32_t *kept = p.kept + s * p.k_ss + g * p.k_hs;
-  if (__ldg(p.seq_lens + s) <= p.budget || __ldcg(kept) < 0) return;  // nothing moves (kept[0] < 0: a fault)
+  const int len = __ldg(p.seq_lens + s);
+  if (len <= p.budget || __ldcg(kept) < 0) return;  // nothing moves (kept[0] < 0: a fault)
+  // Positions and blocks are select_kernel's, checked there.  A caller that writes the inputs during
+  // the call gets wrong rows, but none outside the caches: what is read again is bounded again.
+  const unsigned last_block = p.num_blocks - 1;
+  if (len > p.max_blocks * kBlock || p.num_blocks <= 0) return;
   const int32_t *bt = p.block_table + s * p.bt_ss;
   char *base = p.cache[which] + g * p.s1[which];
   const int64_t s0 = p.s0[which], s2 = p.s2[which];
   const int rows = blockDim.y, r = threadIdx.y, q = slice * blockDim.x + threadIdx.x;
   auto place = [&](int pos) {
-    const int64_t blk = __ldg(bt + pos / kBlock);
+    const int64_t blk = min(static_cast<unsigned>(__ldg(bt + pos / kBlock)), last_block);
     const int t = pos % kBlock;
     if constexpr (FP4) {
       const int off = q < 8 ? fp4_code_off(p.D, t, q * static_cast<int>(sizeof(V))) : fp4_scale_off(p.D, t, 0);
@@ -237,6 +244,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
     for (int k = 0; k < kMoveUnroll; ++k) {
       const int i = i0 + k * rows + r;
       pos[k] = i < p.budget ? __ldcg(kept + i) : -1;
+      if (pos[k] >= len) pos[k] = -1;
     }
   };
   auto read = [&](V (&to)[kMoveUnroll]) {
