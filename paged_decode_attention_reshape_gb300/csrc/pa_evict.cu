@@ -8,12 +8,12 @@
 //
 // Two kernels.
 //
-// select_kernel, one CTA per (s, g): the weight of the last token to stay is found digit by
+// select_kernel, one CTA (of 256 threads; 1024 for few long rows) per (s, g): the weight of the last token to stay is found digit by
 // digit (radix select on the floats' ordered bit patterns, 11 + 11 + 10 bits: a histogram in
 // shared memory, then the digit in which the count from the top passes what is still wanted),
 // which is exact for any distribution and needs no sort; then every warp counts and writes its own
 // stretch of the kept positions and their weights, in order.  The passes work on registers for
-// the first 4096 tokens, on L2 behind them.  Bound: 4 bytes a token from HBM once; in fact the
+// the first 16 a thread, on L2 behind them.  Bound: 4 bytes a token from HBM once; in fact the
 // passes' latency.
 //
 // move_kernel, one or more CTAs per (s, g) and cache: rows p_0 < p_1 < ... move to rows
@@ -49,11 +49,8 @@ struct EvictParams {
   int *err;
 };
 
-constexpr int kSelectThreads = 256;
-constexpr int kWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kHeld = 16;  // tiles of 32 weights that a warp keeps in registers (4096 tokens a CTA)
-constexpr int kPerThread = kBins / kSelectThreads;
+constexpr int kHeld = 16;  // tiles of 32 weights that a warp keeps in registers (16 T tokens a CTA)
 
 // Bit patterns that order as the floats do (-0 as +0, NaN below everything).
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
@@ -62,7 +59,9 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictParams p) {
+template <int T>
+__global__ void __launch_bounds__(T, T == 256 ? 4 : 1) select_kernel(const EvictParams p) {
+  constexpr int kWarps = T / 32, kPerThread = kBins / T;
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t s_sum[kWarps], s_above[kWarps], s_equal[kWarps];
   __shared__ uint32_t s_digit, s_left;
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
   bool bad = !len_ok;
   if (len_ok) {
     const int32_t *bt = p.block_table + s * p.bt_ss;
-    for (int b = tid; b < (len + kBlock - 1) / kBlock; b += kSelectThreads) {
+    for (int b = tid; b < (len + kBlock - 1) / kBlock; b += T) {
       const int id = __ldg(bt + b);
       bad |= id < 0 || id >= p.num_blocks;
     }
@@ -85,8 +84,8 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
   bad = __syncthreads_or(bad);
   if (bad && g == 0 && tid == 0 && p.err) atomicOr(p.err, len_ok ? kErrBlock : kErrSeqLen);
   if (bad || len <= p.budget) {  // nothing to evict, or nothing that may be touched
-    for (int i = tid; i < p.budget; i += kSelectThreads) kept[i] = !bad && i < len ? i : -1;
-    for (int i = tid; i < p.W; i += kSelectThreads) nw[i] = bad || i < len ? __ldg(w + i) : 0.f;
+    for (int i = tid; i < p.budget; i += T) kept[i] = !bad && i < len ? i : -1;
+    for (int i = tid; i < p.W; i += T) nw[i] = bad || i < len ? __ldg(w + i) : 0.f;
     if (g == 0 && tid == 0) p.new_lens[s] = len;
     return;
   }
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
-      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
       each([&](int, uint32_t u, bool in) {
         if (in && (done == 0 || (u >> (32 - done)) == prefix)) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
@@ -189,22 +188,21 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const EvictPa
       equal += __popc(me);
     });
   }
-  for (int i = tid; i < tail; i += kSelectThreads) {
+  for (int i = tid; i < tail; i += T) {
     kept[want + i] = cand + i;
     nw[want + i] = __ldg(w + cand + i);
   }
-  for (int i = p.budget + tid; i < p.W; i += kSelectThreads) nw[i] = 0.f;
+  for (int i = p.budget + tid; i < p.W; i += T) nw[i] = 0.f;
   if (g == 0 && tid == 0) p.new_lens[s] = p.budget;
 }
 
-constexpr int kMoveThreads = 256;  // at most: (pieces of a row, rows)
 constexpr int kMoveUnroll = 4;     // rows of a thread in a stretch
 
 // V: the piece of a row that one thread moves at a time (16 bytes, or D / 16 of a 4-bit page: 8
 // pieces of a token's codes and its scales as the ninth).  The next stretch is read while the
 // last one is written, and its positions one stretch ahead of that.
-template <typename V, bool FP4>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
+template <typename V, bool FP4, int T>
+__global__ void __launch_bounds__(T) move_kernel(const EvictParams p) {
   const int which = blockIdx.x / p.slices, slice = blockIdx.x - which * p.slices;
   const int g = blockIdx.y, s = blockIdx.z;
   grid_dependency_wait();
@@ -269,9 +267,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
 }
 
 template <typename V, bool FP4>
-cudaError_t launch_move(const EvictParams &p, int S, cudaStream_t st) {
+cudaError_t launch_move(const EvictParams &p, int S, bool wide, cudaStream_t st) {
   const int x = p.pieces / p.slices;
-  return launch_pdl(move_kernel<V, FP4>, dim3(2 * p.slices, p.Hkv, S), dim3(x, kMoveThreads / x), 0, st, 1, p);
+  const dim3 grid(2 * p.slices, p.Hkv, S);
+  return wide ? launch_pdl(move_kernel<V, FP4, 1024>, grid, dim3(x, 1024 / x), 0, st, 1, p)
+                     : launch_pdl(move_kernel<V, FP4, 256>, grid, dim3(x, 256 / x), 0, st, 1, p);
 }
 
 }  // namespace
@@ -307,7 +307,7 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
       new_seq_lens->stride[0] != 1 || new_weights->stride[2] != 1)
     return PA_ERR_INVALID_ARG;
   const int eb = elem_bytes(cdt);
-  if (!fp4 && (D <= 0 || (static_cast<int64_t>(D) * eb) % 16 || static_cast<int64_t>(D) * eb > 16 * kMoveThreads))
+  if (!fp4 && (D <= 0 || (static_cast<int64_t>(D) * eb) % 16 || static_cast<int64_t>(D) * eb > 16 * 256))
     return PA_ERR_UNSUPPORTED_SHAPE;
   if (S == 0 || Hkv == 0) return PA_OK;
   if ((MB > 0 && !block_table->data) || !seq_lens->data || !kept->data || !new_seq_lens->data) return PA_ERR_INVALID_ARG;
@@ -347,21 +347,29 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
   p.pieces = fp4 ? 9 : D * eb / 16;
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
-  // few (sequence, head) pairs: several CTAs share their rows, down to 64 bytes of a row each
+  // Few (sequence, head) pairs: several CTAs share their rows, down to 64 bytes of a row each, or 32
+  // where even so the CTAs are few (1 x 32768 tokens, one head, 16384 to stay: 57.2 us against 65.1;
+  // with 8 heads 74.7 against 83.4; but 8 x 8..16k, 8 heads, 128 against 109).  There a CTA of 1024
+  // threads moves longer stretches (64-byte slices, 256 threads: 82.9 and 108.6 us), and where there are no more pairs
+  // than SMs, selects faster from more tokens than 256 threads hold (with 256: 118.7 and 161.3).
   const int64_t units = S * Hkv * 2;
-  const int least = fp4 ? 3 : 4;  // pieces
   p.slices = 1;
-  for (int n = 2; n * least <= p.pieces && units * p.slices < 4 * sm; ++n)
+  for (int n = 2; n * (fp4 ? 3 : 4) <= p.pieces && units * p.slices < 4 * sm; ++n)
     if (p.pieces % n == 0) p.slices = n;
+  if (!fp4 && p.pieces % (2 * p.slices) == 0 && units * p.slices * 2 <= 2 * sm) p.slices *= 2;
+  const bool wide_select = S * Hkv <= sm && MB * kBlock > 4096;
+  const bool wide_move = units * p.slices <= 2 * sm && budget > 1024;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(select_kernel, dim3(Hkv, static_cast<unsigned>(S)), dim3(kSelectThreads), 0, st, 1, p);
+  const dim3 grid(Hkv, static_cast<unsigned>(S));
+  cudaError_t e = wide_select ? launch_pdl(select_kernel<1024>, grid, dim3(1024), 0, st, 1, p)
+                              : launch_pdl(select_kernel<256>, grid, dim3(256), 0, st, 1, p);
   if (e == cudaSuccess) {
     const int n = static_cast<int>(S);
-    e = !fp4 ? launch_move<uint4, false>(p, n, st)
-        : D == 64  ? launch_move<uint32_t, true>(p, n, st)
-        : D == 128 ? launch_move<uint2, true>(p, n, st)
-                   : launch_move<uint4, true>(p, n, st);
+    e = !fp4 ? launch_move<uint4, false>(p, n, wide_move, st)
+        : D == 64  ? launch_move<uint32_t, true>(p, n, wide_move, st)
+        : D == 128 ? launch_move<uint2, true>(p, n, wide_move, st)
+                   : launch_move<uint4, true>(p, n, wide_move, st);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -264,3 +264,20 @@ def test_empty_tables():
         assert pa.pa_check_device_error(err) == (-6, pa.PA_DEVERR_SEQLEN_RANGE)
         assert bool((kept == -1).all()) and nl.tolist() == [0, 0, 5]
         assert not bool(nw[:2].any()) and bool((nw[2] == 1).all())
+
+
+@pytest.mark.parametrize("kind,H,D", [("bf16", 1, 128), ("f32", 2, 64), ("e4m3", 1, 128), ("fp4", 2, 128), ("fp4", 1, 64), ("fp4", 1, 256)])
+@pytest.mark.parametrize("lens,budget,recent", [([20011, 4100], 6000, 100), ([16385], 1025, 1024), ([9000, 8191, 0, 1], 4097, 0)])
+def test_few_long_sequences(kind, H, D, lens, budget, recent):
+    """More tokens than a thread's registers hold, few CTAs: the wide forms of both kernels."""
+    s = Setup(kind, H, D, lens, seed=11)
+    s.weights[:, :, 17:9000:3] = np.float32(0.25)               # many equal weights around the threshold
+    s.weights[0, 0, 5:50] = [np.nan, np.inf, -np.inf, 0.0, -0.0] * 9
+    s.check(budget, recent, s.run(budget, recent))
+
+
+def test_few_long_sequences_stay_below_the_wide_forms():
+    """As many pairs as SMs and more: 256 threads again, same answer."""
+    for H, lens in ((8, [5000] * 3), (8, [5000] * 24)):
+        s = Setup("bf16", H, 64, lens, seed=12)
+        s.check(1500, 64, s.run(1500, 64))
