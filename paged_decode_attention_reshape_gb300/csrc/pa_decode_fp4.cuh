@@ -21,9 +21,11 @@
 //   Softmax: as pa_decode_mma.cuh, in log2 units, one vote per stage.  The running maximum is kept
 //      2^kLift below the largest score, so p reaches 2^15 (f16 holds 65504) and the smallest p
 //      an f16 tells from zero is 2^-24 of 2^7, not of 1.
-//   P: f16.  With an f16 query in two halves (22 bits; the second product adds the rest).  With a
-//      bf16 query in one, 11 bits: each p is off by at most 2^-11 of itself, with a sign that
-//      varies over the tokens, against the 2^-8 of rounding the output to bf16.
+//   P: f16, in two halves (22 bits; a second product adds the rest), as the 16-bit caches' kernels
+//      hold it.  One half, 11 bits, would do without that product (128 x 1k..8k tokens, 64/8 heads:
+//      121 us against 136), but moves every weight by up to 2^-12 of itself: the outputs of that case
+//      were 8e-4 of their norm from a plain fp32 form's instead of 7e-5, and where large terms
+//      cancel the error is all there is.
 //
 // Tokens behind the end exist only in a range's last stage, which takes a branch of its own:
 // scores -inf, p = 0 and V scales 0 (codes are always finite), so nothing stale is summed.
@@ -255,12 +257,9 @@ struct Fp4State {
       l1 += x[j][1] + x[j][3];
       const uint32_t ha = pack_f16(x[j][0], x[j][1]), hb = pack_f16(x[j][2], x[j][3]);
       const uint32_t bh0 = movmatrix_trans(ha), bh1 = movmatrix_trans(hb);
-      uint32_t bl0 = 0u, bl1 = 0u;
-      if constexpr (!C::QBF16) {
-        const float2 fa = unpack_f16(ha), fb = unpack_f16(hb);
-        bl0 = movmatrix_trans(pack_f16(x[j][0] - fa.x, x[j][1] - fa.y));
-        bl1 = movmatrix_trans(pack_f16(x[j][2] - fb.x, x[j][3] - fb.y));
-      }
+      const float2 fa = unpack_f16(ha), fb = unpack_f16(hb);
+      const uint32_t bl0 = movmatrix_trans(pack_f16(x[j][0] - fa.x, x[j][1] - fa.y));
+      const uint32_t bl1 = movmatrix_trans(pack_f16(x[j][2] - fb.x, x[j][3] - fb.y));
       const uint32_t va = vcode0 + sto + j * C::PAGEB, vq = vscale0 + sto + j * C::PAGEB;
       constexpr int VW = Runs::NW;
 #pragma unroll
@@ -291,7 +290,7 @@ struct Fp4State {
                                    mul_f16x2(o23[m], s23)};
             const int t = b * 8 + 4 * i + m;
             mma_f16(acc[t], a, bh0, bh1);
-            if constexpr (!C::QBF16) mma_f16(acc[t], a, bl0, bl1);
+            mma_f16(acc[t], a, bl0, bl1);
           }
         }
       }
