@@ -207,7 +207,8 @@ cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
 // weights[s, g, t] += sum over the query heads h of KV head g of 2^(score_h,t - lse_h), the
 // attention weight of token t: the decode kernels have left every score (log2 units) and
 // every head's log2 of the softmax sum, which is known only after the last page, in the
-// workspace.  Scores are stored token by token, the group's columns together, so a thread
+// workspace (+inf for a head without a positive sum, or after an error: it adds nothing).  Scores are
+// stored token by token, the group's columns together, so a thread
 // reads one 16- or 32-byte run per token and adjacent threads adjacent runs.  Keeping the
 // scores costs 4 bytes a (query head, token) each way, mostly served by L2, against a second
 // read of every K page (2 D bytes a (KV head, token) for a 16-bit cache).
@@ -251,12 +252,14 @@ __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < CW; ++i) ls[i] = i < n ? __ldcg(lse + i) : 0.f;
+      for (int i = 0; i < CW; ++i) ls[i] = i < n ? __ldcg(lse + i) : INFINITY;
+      // a column without a sum is left out here, not by the exponent: its scores may be NaN or +inf, and
+      // those of a unit that wrote nothing after an error whatever the workspace held
 #pragma unroll
       for (int k = 0; k < kWeightTokens; ++k)
 #pragma unroll
         for (int i = 0; i < CW; ++i)
-          if (i < n && t0 + 256 * k < len) sum[k] += ex2(v[k][i] - ls[i]);
+          if (ls[i] < INFINITY && t0 + 256 * k < len) sum[k] += ex2(v[k][i] - ls[i]);
     }
 #pragma unroll
     for (int k = 0; k < kWeightTokens; ++k)

@@ -53,7 +53,7 @@ constexpr int kUnitBad = 0x40000000;
 constexpr int kArrivalMask = kUnitBad - 1;
 
 // log2 of a column's whole softmax sum, sum_t 2^score_t = 2^M den, for pa_decode_accumulate;
-// +inf (every weight 2^(score - inf) = 0) for a column without any weight.
+// +inf (such a column adds nothing) where the sum is no positive number.
 __device__ __forceinline__ float log_total(float M, float den) { return den > 0.f ? M + log2f(den) : INFINITY; }
 // The same for the columns of a unit that wrote nothing after an error.
 __device__ __forceinline__ void drop_lse(const DecodeParams &p, const Cols &cm, int ng) {
