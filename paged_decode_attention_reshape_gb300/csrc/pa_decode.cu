@@ -207,9 +207,10 @@ cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
 // weights[s, g, t] += sum over the query heads h of KV head g of 2^(score_h,t - lse_h), the
 // attention weight of token t: the decode kernels have left every score (log2 units) and
 // every head's log2 of the softmax sum, which is known only after the last page, in the
-// workspace (+inf for a head without a positive sum, or after an error: it adds nothing).  Scores are
-// stored token by token, the group's columns together, so a thread
-// reads one 16- or 32-byte run per token and adjacent threads adjacent runs.  Keeping the
+// workspace (+inf for a head without a positive sum, which adds nothing; NaN for one whose unit set an
+// error, as a timed-out wait may in one KV head alone: the sequence adds nothing).  Scores are stored
+// token by token, the group's columns together, so a thread reads one 16- or 32-byte run per token and
+// adjacent threads adjacent runs.  Keeping the
 // scores costs 4 bytes a (query head, token) each way, mostly served by L2, against a second
 // read of every K page (2 D bytes a (KV head, token) for a 16-bit cache).
 constexpr int kWeightTokens = 4;  // tokens in flight per thread (one: 32 us on 64 x 1k..8k tokens, 8 KV heads)
@@ -218,10 +219,18 @@ __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
   const int s = blockIdx.z, g = blockIdx.y;
   grid_dependency_wait();
   const int len = __ldg(p.seq_lens + s);
-  if (len < 0 || len > p.max_tokens) return;  // reported by the decode
+  if (len <= 0 || len > p.max_tokens) return;  // (out of range: reported by the decode)
+  const float *row = p.lse + static_cast<int64_t>(s) * p.Hkv * p.G;
+  bool failed = false;
+  for (int h = threadIdx.x; h < p.Hkv * p.G; h += 256) {
+    const float x = __ldcg(row + h);
+    failed |= x != x;
+  }
   float *w = p.weights + s * p.w_ss + g * p.w_hs;
   const int64_t unit0 = (static_cast<int64_t>(s) * p.Hkv + g) * p.HG;
-  for (int t0 = blockIdx.x * (256 * kWeightTokens) + threadIdx.x; t0 < len; t0 += gridDim.x * (256 * kWeightTokens)) {
+  const int first = blockIdx.x * (256 * kWeightTokens);
+  for (int b0 = first; b0 < len; b0 += gridDim.x * (256 * kWeightTokens)) {
+    const int t0 = b0 + threadIdx.x;
     float sum[kWeightTokens], old[kWeightTokens];
 #pragma unroll
     for (int k = 0; k < kWeightTokens; ++k) {
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
     }
     for (int hg = 0; hg < p.HG; ++hg) {
       const float *sc = p.scores + (unit0 + hg) * p.max_tokens * CW;
-      const float *lse = p.lse + static_cast<int64_t>(s) * p.Hkv * p.G + g * p.G + hg * 8;
+      const float *lse = row + g * p.G + hg * 8;
       const int n = min(CW, p.G - hg * 8);
       float v[kWeightTokens][CW], ls[CW];
 #pragma unroll
@@ -253,14 +262,14 @@ __global__ void __launch_bounds__(256) weights_kernel(const WeightsParams p) {
       }
 #pragma unroll
       for (int i = 0; i < CW; ++i) ls[i] = i < n ? __ldcg(lse + i) : INFINITY;
-      // a column without a sum is left out here, not by the exponent: its scores may be NaN or +inf, and
-      // those of a unit that wrote nothing after an error whatever the workspace held
+      // a column without a sum is left out here, not by the exponent: its scores may be NaN or +inf
 #pragma unroll
       for (int k = 0; k < kWeightTokens; ++k)
 #pragma unroll
         for (int i = 0; i < CW; ++i)
           if (ls[i] < INFINITY && t0 + 256 * k < len) sum[k] += ex2(v[k][i] - ls[i]);
     }
+    if (b0 == first && __syncthreads_or(failed)) return;  // (here: behind the loads)
 #pragma unroll
     for (int k = 0; k < kWeightTokens; ++k)
       if (t0 + 256 * k < len) w[t0 + 256 * k] = old[k] + sum[k];

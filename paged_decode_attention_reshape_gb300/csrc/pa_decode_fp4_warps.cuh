@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D)) decode_fp4_warp
       }
       if constexpr (ACC) {
         if (ra == 0) {
-          if (2 * qc < ng) p.lse[cm.row(2 * qc) * p.Hq + cm.head(2 * qc)] = bad ? INFINITY : log_total(state.m0, l0);
+          if (2 * qc < ng) p.lse[cm.row(2 * qc) * p.Hq + cm.head(2 * qc)] = bad ? log_failed() : log_total(state.m0, l0);
           if (2 * qc + 1 < ng)
-            p.lse[cm.row(2 * qc + 1) * p.Hq + cm.head(2 * qc + 1)] = bad ? INFINITY : log_total(state.m1, l1);
+            p.lse[cm.row(2 * qc + 1) * p.Hq + cm.head(2 * qc + 1)] = bad ? log_failed() : log_total(state.m1, l1);
         }
       }
     } else {
@@ -344,9 +344,9 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D)) decode_fp4_warp
         }
         if constexpr (ACC) {
           if (ra == 0) {
-            if (2 * qc < ng) p.lse[cm.row(2 * qc) * p.Hq + cm.head(2 * qc)] = unit_bad ? INFINITY : log_total(M0, den0);
+            if (2 * qc < ng) p.lse[cm.row(2 * qc) * p.Hq + cm.head(2 * qc)] = unit_bad ? log_failed() : log_total(M0, den0);
             if (2 * qc + 1 < ng)
-              p.lse[cm.row(2 * qc + 1) * p.Hq + cm.head(2 * qc + 1)] = unit_bad ? INFINITY : log_total(M1, den1);
+              p.lse[cm.row(2 * qc + 1) * p.Hq + cm.head(2 * qc + 1)] = unit_bad ? log_failed() : log_total(M1, den1);
           }
         }
       }

@@ -55,10 +55,12 @@ constexpr int kArrivalMask = kUnitBad - 1;
 // log2 of a column's whole softmax sum, sum_t 2^score_t = 2^M den, for pa_decode_accumulate;
 // +inf (such a column adds nothing) where the sum is no positive number.
 __device__ __forceinline__ float log_total(float M, float den) { return den > 0.f ? M + log2f(den) : INFINITY; }
-// The same for the columns of a unit that wrote nothing after an error.
+// The mark of a unit that wrote nothing after an error (no sum's log is NaN): its whole sequence
+// then adds nothing.
+__device__ __forceinline__ float log_failed() { return __int_as_float(0x7fffffff); }
 __device__ __forceinline__ void drop_lse(const DecodeParams &p, const Cols &cm, int ng) {
   if (threadIdx.x < static_cast<unsigned>(ng))
-    p.lse[cm.row(threadIdx.x) * p.Hq + cm.head(threadIdx.x)] = INFINITY;
+    p.lse[cm.row(threadIdx.x) * p.Hq + cm.head(threadIdx.x)] = log_failed();
 }
 
 // smem_w: shared memory for 8 * kMergeSmemParts floats, free for reuse by now.
