@@ -337,6 +337,8 @@ int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, 
  *                    workspace (pa_decode_accumulate_workspace_size bytes, used by every
  *                    call, split or not) holds one fp32 score per (query head, token):
  *                    4 bytes against the 2 head_size * (element bytes) of a token's K and V.
+ *                    Zero-filled once, a caller's serves the split and unsplit calls of one
+ *                    shape, of pa_decode_opt too, in any order.
  * Two kernels: the decode, which stores its scores, and a second one that turns them into
  * weights once every head's softmax sum is known.
  */

@@ -293,14 +293,16 @@ struct WsLayout {
   size_t ml_off, acc_off, total;
 };
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+size_t arrival_counter_bytes(int S, int Hq, int Hkv) {
+  return round256(static_cast<size_t>(S) * Hkv * ((Hq / Hkv + 7) / 8) * sizeof(int));
+}
 WsLayout workspace_layout(int S, int Hq, int Hkv, int D, int maxNB, int P, int flat) {
   WsLayout L{0, 0, 0};
   if (P <= 0 && flat <= 0) return L;
   const int64_t head_rows = static_cast<int64_t>(Hkv) * ((Hq / Hkv + 7) / 8);
   const int64_t rows = flat > 0 ? head_rows * flat * 16
                                 : static_cast<int64_t>(S) * Hq * ((static_cast<int64_t>(maxNB) * kBlock + P - 1) / P);
-  const int64_t units = static_cast<int64_t>(S) * head_rows;
-  L.ml_off = round256(static_cast<size_t>(units) * sizeof(int));
+  L.ml_off = arrival_counter_bytes(S, Hq, Hkv);
   L.acc_off = L.ml_off + round256(static_cast<size_t>(rows) * sizeof(float2));
   L.total = L.acc_off + static_cast<size_t>(rows) * D * sizeof(float);
   return L;
@@ -807,6 +809,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     }
     return PA_OK;
   }
+  size_t to_clear = 0;
   if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0 || weights) {
     const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, maxNB, max_parts > 1 ? P : 0, pl.flat);
     const ScoreLayout sc = weights ? score_layout(S, Hq, Hkv, maxNB) : ScoreLayout{0, 0, 0};
@@ -820,6 +823,13 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     } else {
       if (!workspace || workspace_bytes < total) return PA_ERR_WORKSPACE;
       if (!aligned16(workspace)) return PA_ERR_ALIGNMENT;
+      if (weights && lay.total == 0) {
+        // an unsplit call has no arrival counters, but the next call may: its scores lie behind their
+        // place where there is room, else that place is cleared afterwards
+        const size_t counters = arrival_counter_bytes(S, Hqv, Hkv);
+        if (workspace_bytes - total >= counters) ml_off = counters;
+        else to_clear = counters;
+      }
     }
     if (weights) {
       char *base = static_cast<char *>(workspace) + ml_off + (round256(lay.total) - lay.ml_off);
@@ -886,6 +896,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     ProfScope ps(PA_KERNEL_DECODE, st);
     e = launch_weights(w, p.score_cols, st);
   }
+  if (e == cudaSuccess && to_clear) e = cudaMemsetAsync(workspace, 0, to_clear, st);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
