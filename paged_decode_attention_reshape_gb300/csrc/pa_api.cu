@@ -979,9 +979,15 @@ PA_API int pa_decode_step(pa_tensor *out, const pa_tensor *q, const pa_tensor *k
   if (!new_rows_start && key->shape[0] != q->shape[0]) return PA_ERR_INVALID_ARG;  // one new row per sequence
   if (new_rows_start && ((r = check_desc(new_rows_start, 1)) || new_rows_start->shape[0] != q->shape[0] + 1))
     return r ? r : PA_ERR_INVALID_ARG;
-  // every argument of both halves is checked before anything is launched
+  // every argument of both halves is checked before anything is launched, and the library's workspace
+  // is there (an allocation may fail)
+  size_t need = 0, counters = 0;
   if ((r = decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
-                       nullptr, 1, new_rows_start, true, true)))
+                       nullptr, 1, new_rows_start, true, true, &need, &counters)))
+    return r;
+  DevWorkspace w;
+  if (internal && need > 0 &&
+      (r = internal_workspace(counters, need - counters, static_cast<cudaStream_t>(stream), &w)))
     return r;
   const pa_write_options wo{o.k_scale, o.v_scale, o.scale_stride, o.device_error};
   const int kv = k_cache->dtype == PA_FP8_E4M3   ? PA_KV_FP8_E4M3
