@@ -796,6 +796,14 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   }
   if (!mma_fp8(kind) && !mma_fp4(kind)) p.k_scale = p.v_scale = nullptr;
   if (static_cast<int64_t>(p.Hkv) * p.HG > 65535) return PA_ERR_UNSUPPORTED_SHAPE;
+  // (made before a dry run ends: a layout or a stride that a map cannot take is a refusal too)
+  CUtensorMap tmK{}, tmV{};
+  if (kind != KIND_F32 && !mma_fp4(kind)) {
+    int nhd_k = 0, nhd_v = 0;
+    if ((r = make_cache_map(k_cache, &tmK, &nhd_k)) || (r = make_cache_map(v_cache, &tmV, &nhd_v))) return r;
+    if (nhd_k != nhd_v) return PA_ERR_INVALID_ARG;  // K and V in different layouts
+    p.nhd = nhd_k;
+  }
 
   if (dry) {  // validation only (pa_decode_step checks everything before its first launch)
     if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0) {
@@ -864,11 +872,6 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     ProfScope ps(PA_KERNEL_DECODE, st);
     e = pl.warps ? launch_decode_fp4_warps(p, kind, sm * mma_min_ctas(kind, D), st) : launch_decode_mma_fp4(p, kind, st);
   } else {
-    CUtensorMap tmK, tmV;
-    int nhd_k = 0, nhd_v = 0;
-    if ((r = make_cache_map(k_cache, &tmK, &nhd_k)) || (r = make_cache_map(v_cache, &tmV, &nhd_v))) return r;
-    if (nhd_k != nhd_v) return PA_ERR_INVALID_ARG;  // K and V in different layouts
-    p.nhd = nhd_k;
     ProfScope ps(PA_KERNEL_DECODE, st);
     if (chunk) {
       CUtensorMap tmQ{};

@@ -39,3 +39,12 @@ def test_workspace_that_cannot_be_had():
     table = torch.zeros(64, 1 << 21, dtype=torch.int32, device="cuda")
     assert pa.pa_decode_workspace_size(64, 64, 8, 128, 1 << 21, 16) > 1 << 42
     refused(c, g.k_cache, g.v_cache, g, table, -5, 16)
+
+
+@pytest.mark.parametrize("P", [0, -1, 16])
+def test_caches_in_different_layouts(P):
+    """K head-major and V token-major within a block: the decode takes one layout for both."""
+    c = make_case(3, 8, 4, 64, [40, 17, 100], seed=2)
+    g = to_gpu(c)
+    v_nhd = g.v_cache.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    refused(c, g.k_cache, v_nhd, g, g.block_table, -1, P)
