@@ -228,9 +228,10 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  * Head sizes built: 64, 128, 256 (E4M3 caches: 128, 256).
  * Uses a library-held workspace on the current device (grown on demand with
  * cudaMallocAsync and zero-filled on `stream`); calls that use it on different
- * streams must not overlap.  A stream capture cannot grow it (PA_ERR_WORKSPACE): run a call
- * of the shape once before capturing it.  FP8 scales are 1.0 here; use pa_decode_ex for scales, a caller-owned
- * workspace, an explicit partition size or a device error word.
+ * streams must not overlap.  A call in a stream capture that needs it larger has the new one
+ * allocated beside the graph; memory whose address a graph holds stays until the process ends,
+ * so capture the largest shape first.  FP8 scales are 1.0 here; use pa_decode_ex for scales, a
+ * caller-owned workspace, an explicit partition size or a device error word.
  */
 int pa_decode(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
               const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads,
