@@ -146,7 +146,7 @@ typedef struct {
  *   device_error  device int to OR error bits into, or NULL.
  * Alignment: key/value/cache base pointers and all strides in bytes must be
  * multiples of 16 bytes, and D * element size a multiple of 16.
- * T == 0 is a no-op.
+ * T == 0 or Hkv == 0 is a no-op.
  */
 int pa_reshape_and_cache(const pa_tensor *key, const pa_tensor *value, pa_tensor *k_cache,
                          pa_tensor *v_cache, const pa_tensor *slot_mapping, int kv_dtype,

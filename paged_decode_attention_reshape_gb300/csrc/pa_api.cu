@@ -454,8 +454,8 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
     return PA_ERR_INVALID_ARG;
   if (key->stride[2] != 1 || value->stride[2] != 1 || slot_mapping->stride[0] != 1) return PA_ERR_INVALID_ARG;
   const int ib = elem_bytes(in_dt);
-  if ((static_cast<int64_t>(D) * ib) % 16) return PA_ERR_UNSUPPORTED_SHAPE;
-  if (T == 0) return PA_OK;
+  if (D <= 0 || (static_cast<int64_t>(D) * ib) % 16) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || Hkv == 0) return PA_OK;
   if (!key->data || !value->data || !slot_mapping->data) return PA_ERR_INVALID_ARG;
   if (!aligned16(key->data) || !aligned16(value->data)) return PA_ERR_ALIGNMENT;
   for (int i = 0; i < 2; ++i)
