@@ -327,7 +327,8 @@ int pa_decode_opt(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, 
  * pa_decode_accumulate -- pa_decode_opt that also adds the attention weight of every cached
  * token to an array: the statistics by which pa_evict shortens a sequence.
  *
- *   weights          PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16, innermost stride 1.  For
+ *   weights          PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16 (at most 2^26 blocks a
+ *                    sequence, whatever the cache), innermost stride 1.  For
  *                    every sequence s, KV head g and token t < seq_lens[s], weights[s, g, t]
  *                    grows by the sum over the Hq / Hkv query heads of g of their softmax
  *                    weight of t (so by Hq / Hkv over the whole row).  Other entries are not
@@ -366,7 +367,7 @@ size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_
  *   k_cache, v_cache  any cache type (as pa_reshape_and_cache); rows of at most 4096 bytes.
  *   block_table       PA_I32 [S, max_blocks_per_seq]; the first ceil(L / 16) entries of a row
  *   seq_lens          are used.  PA_I32 [S].
- *   weights           PA_F32 [S, Hkv, W], W >= max_blocks_per_seq * 16.  Read only.
+ *   weights           PA_F32 [S, Hkv, W], max_blocks_per_seq * 16 <= W < 2^31 - 4096.  Read only.
  *   budget, recent    host ints; 1 <= budget <= 2^30, recent >= 0.
  *   kept              PA_I32 [S, Hkv, budget], written: the positions kept, ascending, then
  *                     -1 where the sequence is shorter than the budget.

@@ -747,6 +747,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
       return PA_ERR_INVALID_ARG;
     if (o.partition_size < -1 && o.partition_size != PA_PARTITION_BALANCED)
       return PA_ERR_UNSUPPORTED_SHAPE;  // cluster splits
+    // (the second kernel counts tokens in 32 bits, up to a grid's stride past the last)
+    if (block_table->shape[1] > (1 << 26)) return PA_ERR_UNSUPPORTED_SHAPE;
   }
   if (S64 == 0 || q->shape[0] == 0) return PA_OK;
   if (weights && block_table->shape[1] > 0 && !weights->data) return PA_ERR_INVALID_ARG;

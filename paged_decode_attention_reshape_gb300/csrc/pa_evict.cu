@@ -301,7 +301,8 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
     return PA_ERR_INVALID_ARG;
   if (weights->shape[1] != Hkv || kept->shape[1] != Hkv || new_weights->shape[1] != Hkv) return PA_ERR_INVALID_ARG;
   if (kept->shape[2] != budget || new_weights->shape[2] != W) return PA_ERR_INVALID_ARG;
-  if (S > 65535 || MB > INT32_MAX / kBlock || W > INT32_MAX || budget > (1 << 30)) return PA_ERR_UNSUPPORTED_SHAPE;
+  // (the kernels count positions in 32 bits, to less than 4096 past the last)
+  if (S > 65535 || MB > INT32_MAX / kBlock || W > INT32_MAX - 4096 || budget > (1 << 30)) return PA_ERR_UNSUPPORTED_SHAPE;
   if (W < MB * kBlock) return PA_ERR_INVALID_ARG;
   if (block_table->stride[1] != 1 || seq_lens->stride[0] != 1 || weights->stride[2] != 1 || kept->stride[2] != 1 ||
       new_seq_lens->stride[0] != 1 || new_weights->stride[2] != 1)
