@@ -46,6 +46,8 @@
  *    lin = t * r + b % 64, at (b / 64) * 1024 + (lin ^ (((lin >> 7) & 3) << 5)); scale j of
  *    token t (elements 16 j .. 16 j + 15) lies at 8 * head_size + t * head_size / 16 + j.
  *    The element's value is code * scale * k_scale (v_scale).
+ *  - Every pointer is a multiple of its element's size (arrays, scales, error words), data
+ *    pointers of rows and caches of 16 bytes: PA_ERR_ALIGNMENT otherwise.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *    default stream) and never synchronise, except pa_check_device_error and
  *    pa_profile_read.
@@ -90,7 +92,8 @@ typedef enum {
     PA_OK = 0,
     PA_ERR_INVALID_ARG = -1,       /* null pointer, rank/extent mismatch, Hq % Hkv != 0 ... */
     PA_ERR_UNSUPPORTED_DTYPE = -2, /* element type (combination) not provided */
-    PA_ERR_ALIGNMENT = -3,         /* a base pointer or stride breaks the 16-byte rule */
+    PA_ERR_ALIGNMENT = -3,         /* a base pointer or stride breaks the 16-byte rule, or a pointer
+                                      its element's size */
     PA_ERR_WORKSPACE = -4,         /* workspace missing or smaller than required */
     PA_ERR_CUDA = -5,              /* a CUDA runtime/driver call or launch failed */
     PA_ERR_DEVICE_BOUNDS = -6,     /* device error word: slot / block id / length out of range */

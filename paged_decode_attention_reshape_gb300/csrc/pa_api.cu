@@ -413,7 +413,7 @@ PA_API const char *pa_status_string(int status) {
     case PA_OK: return "ok";
     case PA_ERR_INVALID_ARG: return "invalid argument";
     case PA_ERR_UNSUPPORTED_DTYPE: return "unsupported element type";
-    case PA_ERR_ALIGNMENT: return "pointer or stride not 16-byte aligned";
+    case PA_ERR_ALIGNMENT: return "pointer or stride not aligned (rows and caches: 16 bytes)";
     case PA_ERR_WORKSPACE: return "workspace missing or too small";
     case PA_ERR_CUDA: return "CUDA call or launch failed";
     case PA_ERR_DEVICE_BOUNDS: return "device reported an out-of-range slot, block id or sequence length";
@@ -457,7 +457,8 @@ static int write_impl(const pa_tensor *key, const pa_tensor *value, pa_tensor *k
   if (D <= 0 || (static_cast<int64_t>(D) * ib) % 16) return PA_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || Hkv == 0) return PA_OK;
   if (!key->data || !value->data || !slot_mapping->data) return PA_ERR_INVALID_ARG;
-  if (!aligned16(key->data) || !aligned16(value->data)) return PA_ERR_ALIGNMENT;
+  if (!aligned16(key->data) || !aligned16(value->data) || !on_elements(slot_mapping)) return PA_ERR_ALIGNMENT;
+  if (!aligned4(o.k_scale) || !aligned4(o.v_scale) || !aligned4(o.device_error)) return PA_ERR_ALIGNMENT;
   for (int i = 0; i < 2; ++i)
     if ((key->stride[i] * ib) % 16 || (value->stride[i] * ib) % 16) return PA_ERR_ALIGNMENT;
 
@@ -577,7 +578,8 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
   if (T == 0 || Hkv == 0) return PA_OK;
   if (!key->data || !value->data || !slot_mapping->data) return PA_ERR_INVALID_ARG;
   const int ob = elem_bytes(out_dt), cb = elem_bytes(cache_dt);
-  if (!aligned16(key->data) || !aligned16(value->data)) return PA_ERR_ALIGNMENT;
+  if (!aligned16(key->data) || !aligned16(value->data) || !on_elements(slot_mapping)) return PA_ERR_ALIGNMENT;
+  if (!aligned4(o.k_scale) || !aligned4(o.v_scale) || !aligned4(o.device_error)) return PA_ERR_ALIGNMENT;
   for (int i = 0; i < 2; ++i)
     if ((key->stride[i] * ob) % 16 || (value->stride[i] * ob) % 16) return PA_ERR_ALIGNMENT;
   GatherParams p{};
@@ -752,8 +754,13 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   }
   if (S64 == 0 || q->shape[0] == 0) return PA_OK;
   if (weights && block_table->shape[1] > 0 && !weights->data) return PA_ERR_INVALID_ARG;
-  if (weights && reinterpret_cast<uintptr_t>(weights->data) % 4) return PA_ERR_ALIGNMENT;
   if (!q->data || !out->data || !block_table->data || !seq_lens->data) return PA_ERR_INVALID_ARG;
+  for (const pa_tensor *t : {block_table, seq_lens, query_start_loc, early ? new_rows_start : nullptr,
+                             static_cast<const pa_tensor *>(weights)})
+    if (t && !on_elements(t)) return PA_ERR_ALIGNMENT;
+  for (const void *x : {static_cast<const void *>(k_scale), static_cast<const void *>(v_scale),
+                        static_cast<const void *>(o.alibi_slopes), static_cast<const void *>(device_error)})
+    if (!aligned4(x)) return PA_ERR_ALIGNMENT;
   const int qb = elem_bytes(q->dtype);
   if (!aligned16(q->data) || !aligned16(out->data)) return PA_ERR_ALIGNMENT;
   for (int i = 0; i < 2; ++i)

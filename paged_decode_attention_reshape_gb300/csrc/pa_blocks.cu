@@ -215,7 +215,9 @@ PA_API int pa_copy_blocks(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tenso
   const int row_bytes = static_cast<int>(k_cache->shape[rank - 1]) * eb;
   if (k_cache->stride[rank - 1] != 1 || v_cache->stride[rank - 1] != 1 || row_bytes % 16) return PA_ERR_INVALID_ARG;
   const uintptr_t kb = reinterpret_cast<uintptr_t>(k_cache->data), vb = reinterpret_cast<uintptr_t>(v_cache->data);
-  if (kb % 16 || vb % 16) return PA_ERR_ALIGNMENT;
+  if (kb % 16 || vb % 16 || reinterpret_cast<uintptr_t>(block_pairs->data) % 8 ||
+      reinterpret_cast<uintptr_t>(device_error) % 4)
+    return PA_ERR_ALIGNMENT;
   for (int i = 0; i < rank - 1; ++i)
     if ((k_cache->stride[i] * eb) % 16 || (v_cache->stride[i] * eb) % 16) return PA_ERR_ALIGNMENT;
   copy_blocks_kernel<<<static_cast<unsigned>(2 * n), 256, 0, static_cast<cudaStream_t>(stream)>>>(

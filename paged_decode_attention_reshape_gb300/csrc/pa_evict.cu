@@ -313,6 +313,10 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
   if (S == 0 || Hkv == 0) return PA_OK;
   if ((MB > 0 && !block_table->data) || !seq_lens->data || !kept->data || !new_seq_lens->data) return PA_ERR_INVALID_ARG;
   if (W > 0 && (!weights->data || !new_weights->data)) return PA_ERR_INVALID_ARG;
+  for (const pa_tensor *t : {block_table, seq_lens, weights, static_cast<const pa_tensor *>(kept),
+                             static_cast<const pa_tensor *>(new_seq_lens), static_cast<const pa_tensor *>(new_weights)})
+    if (!on_elements(t)) return PA_ERR_ALIGNMENT;
+  if (!aligned4(device_error)) return PA_ERR_ALIGNMENT;
   // read by every CTA of a sequence while others write the new ones
   if ((W > 0 && new_weights->data == weights->data) || new_seq_lens->data == seq_lens->data) return PA_ERR_INVALID_ARG;
 

@@ -20,6 +20,13 @@ inline int elem_bytes(int dt) {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether a tensor's elements lie on multiples of their size.
+inline bool on_elements(const pa_tensor *t) {
+  return reinterpret_cast<uintptr_t>(t->data) % static_cast<uintptr_t>(elem_bytes(t->dtype)) == 0;
+}
+
 // Rows [T, H, D] whose every 32-byte piece is 32-byte aligned (element size eb).
 inline bool rows_aligned32(const pa_tensor *t, int eb) {
   return (reinterpret_cast<uintptr_t>(t->data) & 31u) == 0 && (t->stride[0] * eb) % 32 == 0 && (t->stride[1] * eb) % 32 == 0;
