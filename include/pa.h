@@ -313,7 +313,8 @@ typedef struct {
      * many polls; < 0 = give up without polling.  For testing the timeout path: a wait that
      * gives up first waits (with the normal limit) for the copies it had in flight, sets
      * PA_DEVERR_WAIT_TIMEOUT and writes no output for its work item (nor for a split-KV unit
-     * that any of its parts gave up on).  Every later wait keeps the normal limit. */
+     * that any of its parts gave up on).  Every later wait keeps the normal limit.  Decodes over a
+     * 4-bit or fp32 cache have no such wait and ignore it. */
     int first_wait_limit;
 } pa_decode_options;
 

@@ -287,7 +287,8 @@ def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float,
     """pa_decode with every option: per-head FP8 scales (KV head h uses k_scale[h * scale_stride]),
     ALiBi slopes (fp32 [Hq]: logit += slope_h * (t - (seq_len - 1))), partition size, caller
     workspace (None: the library's internal one) and device error word.  first_wait_limit: poll
-    limit of the first pipeline wait (0 normal, < 0 give up at once), for testing the timeout path."""
+    limit of the first pipeline wait (0 normal, < 0 give up at once), for testing the timeout path (4-bit caches:
+    no wait gives up)."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
     args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
@@ -301,8 +302,10 @@ def pa_decode_accumulate(out, q, k_cache, v_cache, block_table, seq_lens, scale:
                          partition_size: int = 0, workspace=None, device_error=None, stream=None,
                          first_wait_limit: int = 0) -> None:
     """pa_decode_opt that also adds every cached token's attention weight, summed over the query heads of
-    its KV head, to weights (fp32 [S, Hkv, W >= max blocks * 16]).  Options as pa_decode_opt (no cluster
-    or balanced split); the workspace size is pa_decode_accumulate_workspace_size."""
+    its KV head, to weights (fp32 [S, Hkv, W >= max blocks * 16]).  Options as pa_decode_opt, without the
+    cluster splits.  A caller's workspace needs pa_decode_accumulate_workspace_size bytes for the split that
+    the call ends up with: for partition_size 0, the one that pa_decode_plan reports (over a 4-bit cache it
+    may be PA_PARTITION_BALANCED)."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
     args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
@@ -338,7 +341,7 @@ def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_tab
     decode over the updated cache in one call; the decode reads everything but the new
     positions while the write runs.  new_rows_start: None (row s = sequence s's newest token)
     or int32 [S+1] (rows of sequence s, its newest tokens in order).  Options as pa_decode_opt;
-    the scales also quantise the rows written to an FP8 cache."""
+    the scales also quantise the rows written to an FP8 or 4-bit cache."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
     nrs = None if new_rows_start is None else _desc(new_rows_start)

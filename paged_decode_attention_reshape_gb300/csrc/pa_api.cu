@@ -238,10 +238,10 @@ int balanced_ctas(int Hq, int Hkv, int D, int kind, int sm, bool device) {
 // for every three warps of a resident wave (on request: one for eight), and the balanced split over
 // CTAs where there are too few units for the CTAs and a CTA still gets 128 pages or more; else whole
 // units or fixed partitions.  Measured on GB300 (2432 warps, 304 CTAs; us over warps / unsplit or
-// over CTAs / fixed partitions): 304 x 256 tokens, 2432 units, 21.6 / 41.5 / -; 256 x 512..4096,
-// 2048 units, 124.0 / 139.3 / -; 128 x 1k..8k, 1024 units, 124.3 / 121.6 / -; 64 x 0..2048, 512
-// units, 26.4 / 18.5 / - (the parts of cut units cost more than the waves); 16 x 4k..32k, 128
-// units, - / 66.8 / 87.3; 4 x 32k..128k, 32 units, - / 73.1 / 92.7; 1 x 8k, 8 units, - / 17.2 / 10.4.
+// over CTAs / fixed partitions of one wave): 304 x 256 tokens, 2432 units, 22.1 / 42.1 / -; 256 x
+// 512..4096, 2048 units, 135.6 / 156.8 / -; 128 x 1k..8k, 1024 units, 137.7 / 136.3 / -; 64 x 0..2048,
+// 512 units, 23.1 / 18.2 / - (the parts of cut units cost more than the waves); 16 x 4k..32k, 128 units,
+// - / 75.0 / 115.3; 4 x 32k..128k, 32 units, - / 82.6 / 115.7; 1 x 8k, 8 units, - / 17.1 / 10.0.
 bool plan_fp4(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, bool varlen, bool plain,
               bool balanced, Plan *pl) {
   const int64_t rows = static_cast<int64_t>(Hkv) * ((Hq / Hkv + 7) / 8), units = S * rows;

@@ -5,9 +5,9 @@
 // copies: a page's codes are whole 512-byte runs of the warp, and the scales of the stage's 2 NP
 // pages share the last ones, so a stage of head size 128 costs nine copies and five addresses.
 // (One bulk copy per page and a barrier per stage: 147.5 against 135.6 us on 128 x 1k..8k tokens,
-// 64/8 heads.)  At HBM rate an SM has to take 23 bytes, 41 elements, a clock, and the widening
-// alone is half a conversion an element on a pipe that does 64 lanes a clock (measured, and shared
-// with bit selects and shuffles of bytes), so the loop is built to do little else, 272 warp
+// 64/8 heads, when P had one half.)  At HBM rate an SM has to take 23 bytes, 41 elements, a clock, and
+// the widening alone is half a conversion an element on a pipe that does 64 lanes a clock (measured, and shared
+// with bit selects and shuffles of bytes), so the loop is built to do little else, 292 warp
 // instructions a page pair at head size 128:
 //
 //   K: lane (r, c) holds a run of 32 (D = 64: 16) elements of tokens r and r + 8, whole scale

@@ -3,7 +3,7 @@
 //
 // A 4-bit page pair takes an SM 100 clocks at HBM rate, so a CTA per (sequence, KV head) spends
 // much of its life not reading: waiting for its length, its table and its first pages, and
-// leaving its slot to the next (304 x 256 tokens, 8 KV heads of 128, eight waves of CTAs: 41.5 us,
+// leaving its slot to the next (304 x 256 tokens, 8 KV heads of 128, eight waves of CTAs: 42.1 us,
 // where HBM alone takes 14).  Here every warp works by itself.  The stages (pa_decode_fp4.cuh) of all sequences,
 // concatenated, are cut into equal ranges, one per warp of each head row (KV head and group of 8
 // query heads); a range may begin and end inside sequences.  Copies run ahead over the whole
@@ -16,7 +16,8 @@
 // warp's stage buffers, free by then, and the one that begins a range and is followed by others
 // in the workspace.  Parts of several CTAs all go through the workspace (store, release, counter,
 // and a merge by the last): the split pays where most units stay whole.
-// Measured: 304 x 256 tokens 21.4 us; 256 x 512..4096 122.6 us against 139.0 for a CTA per unit, HBM alone 101; but 64 x 0..2048 (head size 64, five parts a unit) 26.4 against 18.5.
+// Measured: 304 x 256 tokens 22.1 us; 256 x 512..4096 135.6 us against 156.8 for a CTA per unit, HBM
+// alone 101; but 64 x 0..2048 (head size 64, five parts a unit) 23.1 against 18.2.
 #pragma once
 
 #include "pa_decode_mma.cuh"

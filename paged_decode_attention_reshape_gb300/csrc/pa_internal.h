@@ -186,11 +186,13 @@ constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND
 // page math, 2 to 4 stages alike), so the warps per CTA set how fast one long
 // sequence streams.  Head size 64: 8 warps (3 CTAs per SM); 128 and 256: 4 warps,
 // whose larger pages already fill HBM with 3 CTAs per SM.  4-bit pages are smaller: 8 warps at
-// head size 128 too (2, 4, 16 warps: 180, 138, 150 us against 125 on 128 x 1k..8k, 64/8 heads).
+// head size 128 too (2, 4, 16 warps: 180, 138, 150 us against 125 on 128 x 1k..8k, 64/8 heads, when P
+// had one half).
 constexpr int mma_warps(int kind, int D) { return D == 64 || (mma_fp4(kind) && D == 128) ? 8 : 4; }
 // Two stages per warp: pages of 2-8 KiB give 35-131 KiB per CTA.  Measured on
 // GB300: 3-4 stages with fewer CTAs per SM were slower on every benchmark workload.
-// (4-bit pages at head size 256, one to a stage: three; at 128 three measured 156 us against 148.)
+// (4-bit pages at head size 256, one to a stage: three; at 128 three measured 156 us against 148, when
+// P had one half.)
 constexpr int mma_stages(int kind, int D) { return mma_fp4(kind) && D == 256 ? 3 : 2; }
 // Resident CTAs per SM the register allocation must allow (ptxas launch bound): as
 // many as the shared memory admits, so registers never cut the occupancy, except
