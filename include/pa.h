@@ -48,6 +48,8 @@
  *    The element's value is code * scale * k_scale (v_scale).
  *  - Every pointer is a multiple of its element's size (arrays, scales, error words), data
  *    pointers of rows and caches of 16 bytes: PA_ERR_ALIGNMENT otherwise.
+ *  - Rows of pa_gather_cache's, pa_decode_accumulate's and pa_evict's outputs may not share memory
+ *    (as a broadcast tensor's do): PA_ERR_INVALID_ARG.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *    default stream) and never synchronise, except pa_check_device_error and
  *    pa_profile_read.

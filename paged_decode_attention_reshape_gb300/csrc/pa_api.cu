@@ -575,6 +575,7 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
     return PA_ERR_INVALID_ARG;
   if (key->stride[2] != 1 || value->stride[2] != 1 || slot_mapping->stride[0] != 1) return PA_ERR_INVALID_ARG;
   if (D <= 0 || D % 16) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (rows_overlap(key, D) || rows_overlap(value, D)) return PA_ERR_INVALID_ARG;
   if (T == 0 || Hkv == 0) return PA_OK;
   if (!key->data || !value->data || !slot_mapping->data) return PA_ERR_INVALID_ARG;
   const int ob = elem_bytes(out_dt), cb = elem_bytes(cache_dt);
@@ -745,7 +746,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     if ((r = check_desc(weights, 3))) return r;
     if (weights->dtype != PA_F32) return PA_ERR_UNSUPPORTED_DTYPE;
     if (weights->shape[0] != S64 || weights->shape[1] != Hkv || weights->shape[2] < block_table->shape[1] * kBlock ||
-        weights->stride[2] != 1)
+        weights->stride[2] != 1 || rows_overlap(weights, block_table->shape[1] * kBlock))
       return PA_ERR_INVALID_ARG;
     if (o.partition_size < -1 && o.partition_size != PA_PARTITION_BALANCED)
       return PA_ERR_UNSUPPORTED_SHAPE;  // cluster splits

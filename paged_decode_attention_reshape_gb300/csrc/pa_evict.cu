@@ -307,6 +307,7 @@ PA_API int pa_evict(pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *blo
   if (block_table->stride[1] != 1 || seq_lens->stride[0] != 1 || weights->stride[2] != 1 || kept->stride[2] != 1 ||
       new_seq_lens->stride[0] != 1 || new_weights->stride[2] != 1)
     return PA_ERR_INVALID_ARG;
+  if (rows_overlap(kept, budget) || rows_overlap(new_weights, W)) return PA_ERR_INVALID_ARG;
   const int eb = elem_bytes(cdt);
   if (!fp4 && (D <= 0 || (static_cast<int64_t>(D) * eb) % 16 || static_cast<int64_t>(D) * eb > 16 * 256))
     return PA_ERR_UNSUPPORTED_SHAPE;

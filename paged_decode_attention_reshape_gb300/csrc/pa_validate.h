@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "pa_internal.h"
 
 namespace pa {
@@ -25,6 +27,18 @@ inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3
 // Whether a tensor's elements lie on multiples of their size.
 inline bool on_elements(const pa_tensor *t) {
   return reinterpret_cast<uintptr_t>(t->data) % static_cast<uintptr_t>(elem_bytes(t->dtype)) == 0;
+}
+
+// Whether rows of `len` elements of an output [n0, n1, ...] share memory (a broadcast one's do): written
+// side by side, and read before they are added to, they would hold whichever came last.
+inline bool rows_overlap(const pa_tensor *t, int64_t len) {
+  int64_t n = t->shape[0], a = t->stride[0], m = t->shape[1], b = t->stride[1];  // a <= b
+  if (a > b) {
+    std::swap(n, m);
+    std::swap(a, b);
+  }
+  if (n < 1 || m < 1 || len < 1) return false;
+  return (n > 1 && a < len) || (m > 1 && b < (n > 1 ? (n - 1) * a : 0) + len);
 }
 
 // Rows [T, H, D] whose every 32-byte piece is 32-byte aligned (element size eb).
