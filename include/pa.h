@@ -9,6 +9,8 @@
  *                          Attention", Part 2; "How vLLM CUDA Kernels Write and
  *                          Read the Paged KV Cache", "Writing K and V into the cache")
  *   pa_gather_cache        the rows of given slots read back as values
+ *   pa_rotary              query and key rows rotated by their positions, heads normalised first
+ *   pa_rotary_and_cache    the same, with the rotated keys and the values written into the cache
  *   pa_decode / _ex        single-query paged decode attention with GQA, online
  *                          softmax and split-KV partitions merged by a
  *                          log-sum-exp reduce ("Inside vLLM CUDA Kernels", Part 3;
@@ -48,7 +50,7 @@
  *    The element's value is code * scale * k_scale (v_scale).
  *  - Every pointer is a multiple of its element's size (arrays, scales, error words), data
  *    pointers of rows and caches of 16 bytes: PA_ERR_ALIGNMENT otherwise.
- *  - Rows of pa_gather_cache's, pa_decode_accumulate's and pa_evict's outputs may not share memory
+ *  - Rows of pa_gather_cache's, pa_rotary's, pa_decode_accumulate's and pa_evict's outputs may not share memory
  *    (as a broadcast tensor's do): PA_ERR_INVALID_ARG.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *    default stream) and never synchronise, except pa_check_device_error and
@@ -206,6 +208,81 @@ int pa_reshape_and_cache_opt(const pa_tensor *key, const pa_tensor *value, pa_te
  */
 int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, const pa_tensor *v_cache,
                     const pa_tensor *slot_mapping, const pa_write_options *opt, pa_stream_t stream);
+
+/*
+ * Rotary positions.  Pair i < R / 2 of a row (elements i and i + R / 2, or interleaved 2i and 2i + 1; R,
+ * the rotated part, at most the head size) turns by the angle position * theta_i:
+ *     a' = m (a cos - b sin),  b' = m (b cos + a sin);   elements from R on stay.
+ * The frequencies are a device table of int64 [R / 2]: theta_i / (2 pi), turns per position, in units of
+ * 2^-64 (whole turns dropped).  The library multiplies positions into it in 64-bit integers, so an angle
+ * is exact to a turn's 2^-64 per position, however far the position.  Positions may be negative (the
+ * rotation back); a call with the differences of two position lists moves rotated rows from one to the
+ * other.
+ */
+typedef enum {
+    PA_ROTARY_PLAIN = 0,  /* theta_i = base^(-2 i / R) */
+    PA_ROTARY_LINEAR = 1, /* theta_i / factor: positions interpolated */
+    PA_ROTARY_BASE = 2,   /* base * factor^(R / (R - 2)) in place of base (the slowest pair slows by
+                             factor, the fastest stays); R > 2 */
+    PA_ROTARY_PARTS = 3   /* by what a pair turns over original_len tokens, n = original_len theta_i / (2 pi):
+                             theta_i from n >= high on, theta_i / factor up to n <= low, between them
+                             mixed linearly in n */
+} pa_rotary_scaling;
+
+/* Host only: fills frequencies (host int64 [rotary_dim / 2]), ready for a host-to-device copy.  factor for
+ * every scaling but PLAIN; original_len, low, high for PARTS (1 and 32 are usual, with the options'
+ * magnitude 0.1 ln(factor) + 1).  Tables of other rules are filled by the caller.
+ * PA_ERR_INVALID_ARG: an odd rotary_dim, values that are not positive and finite, low >= high. */
+int pa_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, double original_len, double low,
+                          double high, int64_t *frequencies);
+
+/* Options of pa_rotary and pa_rotary_and_cache.  Zero-initialise, then set what is needed. */
+typedef struct {
+    int interleaved;       /* 0: pairs (i, i + R / 2); else (2i, 2i + 1) */
+    float magnitude;       /* m above; 0 = 1.0 */
+    float eps;             /* of the norms, >= 0 */
+    const float *k_scale;  /* pa_rotary_and_cache: as pa_write_options */
+    const float *v_scale;
+    int64_t scale_stride;
+    int *device_error;
+} pa_rotary_options;
+
+/*
+ * pa_rotary -- rows of queries and keys rotated by their positions, each head normalised first where a
+ * weight is given.
+ *
+ *   q, q_out      [T, Hq, D] and
+ *   key, k_out    [T, Hk, D], PA_F32 / PA_BF16 / PA_F16 (one type for all), D = 64, 128 or 256; innermost
+ *                 stride 1.  Either pair may be NULL.  An output may be its input's memory with the
+ *                 same strides (in place), and may share no other memory with any input.
+ *   positions     PA_I64 or PA_I32 [T].
+ *   frequencies   PA_I64 [R / 2], R <= D a multiple of 16 (see above); NULL or empty: no rotation, and
+ *                 positions (may be NULL) is not read.
+ *   q_weight,     [D], PA_F32 or the rows' type, or NULL (no norm).  A normalised row is
+ *   k_weight      x (mean(x^2) + eps)^(-1/2) weight, over the whole head, before the rotation.
+ *   opt           NULL = defaults; scales and device_error are not used.
+ * Sums and products in fp32, each element rounded to the rows' type once.  Alignment of rows as
+ * pa_reshape_and_cache.  T == 0 is a no-op.  At most 2^35 rows.
+ */
+int pa_rotary(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa_tensor *key, const pa_tensor *positions,
+              const pa_tensor *frequencies, const pa_tensor *q_weight, const pa_tensor *k_weight,
+              const pa_rotary_options *opt, pa_stream_t stream);
+
+/*
+ * pa_rotary_and_cache -- pa_rotary of a step's queries and keys and pa_reshape_and_cache_opt of the
+ * rotated keys and the values, in one pass.
+ *
+ *   q, q_out      as pa_rotary (NULL: no queries).  Every row of q_out is written, whatever its slot.
+ *   key, value    [T, Hkv, D] of q's type.  Not written.
+ *   k_cache, v_cache, slot_mapping, kv_dtype: as pa_reshape_and_cache, scales, scale_stride and
+ *                 device_error of opt as pa_reshape_and_cache_opt.
+ * The results equal those of the two calls made one after the other, bit for bit: a key is rounded to
+ * its own type, then copied or quantised.
+ */
+int pa_rotary_and_cache(pa_tensor *q_out, const pa_tensor *q, const pa_tensor *key, const pa_tensor *value,
+                        pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *positions,
+                        const pa_tensor *slot_mapping, const pa_tensor *frequencies, const pa_tensor *q_weight,
+                        const pa_tensor *k_weight, int kv_dtype, const pa_rotary_options *opt, pa_stream_t stream);
 
 /*
  * pa_decode -- single-query paged decode attention (one query token per sequence).
@@ -606,8 +683,8 @@ const char *pa_status_string(int status);
  * synchronises on the recorded events, returns the summed device time (ms) and
  * the launch count for one kernel kind since the last read, and clears them.
  *   kind: 0 = cache write, 1 = decode (attention with the fused split-KV merge; the second
- *   kernel of pa_decode_accumulate counts here too).  pa_gather_cache, pa_evict and
- *   pa_copy_blocks are not bracketed.
+ *   kernel of pa_decode_accumulate counts here too); pa_rotary_and_cache counts as a cache
+ *   write.  pa_rotary, pa_gather_cache, pa_evict and pa_copy_blocks are not bracketed.
  */
 #define PA_KERNEL_WRITE 0
 #define PA_KERNEL_DECODE 1

@@ -26,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libpa_gb300.so")
 
 PA_F32, PA_BF16, PA_F16, PA_FP8_E4M3, PA_I32, PA_I64, PA_FP4_E2M1 = range(7)
 PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_FP4_E2M1 = 0, 1, 2
+PA_ROTARY_PLAIN, PA_ROTARY_LINEAR, PA_ROTARY_BASE, PA_ROTARY_PARTS = range(4)
 PA_KERNEL_WRITE, PA_KERNEL_DECODE = 0, 1
 PA_DEVERR_SLOT_RANGE, PA_DEVERR_BLOCK_RANGE, PA_DEVERR_SEQLEN_RANGE, PA_DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
 STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", -3: "PA_ERR_ALIGNMENT",
@@ -34,6 +35,7 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", 
 
 EXPORTS = ("pa_reshape_and_cache", "pa_reshape_and_cache_opt", "pa_decode", "pa_decode_ex", "pa_decode_opt",
            "pa_gather_cache", "pa_decode_accumulate", "pa_decode_accumulate_workspace_size",
+           "pa_rotary_frequencies", "pa_rotary", "pa_rotary_and_cache",
            "pa_evict", "pa_bm_truncate",
            "pa_attention_varlen", "pa_decode_step", "pa_decode_noalloc", "pa_decode_plan", "pa_decode_workspace_size", "pa_check_device_error",
            "pa_status_string", "pa_profile_enable", "pa_profile_read", "pa_bm_create", "pa_bm_destroy",
@@ -63,6 +65,12 @@ class PaDecodeOptions(ctypes.Structure):
                 ("alibi_slopes", ctypes.c_void_p), ("partition_size", ctypes.c_int),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("device_error", ctypes.c_void_p), ("first_wait_limit", ctypes.c_int)]
+
+
+class PaRotaryOptions(ctypes.Structure):
+    _fields_ = [("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float), ("eps", ctypes.c_float),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("device_error", ctypes.c_void_p)]
 
 
 class PAError(RuntimeError):
@@ -98,6 +106,13 @@ def lib() -> ctypes.CDLL:
             L.pa_reshape_and_cache_opt.argtypes = [T, T, T, T, T, i32, P, P]
             L.pa_gather_cache.restype = i32
             L.pa_gather_cache.argtypes = [T, T, T, T, T, P, P]
+            f64 = ctypes.c_double
+            L.pa_rotary_frequencies.restype = i32
+            L.pa_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+            L.pa_rotary.restype = i32
+            L.pa_rotary.argtypes = [T] * 8 + [P, P]
+            L.pa_rotary_and_cache.restype = i32
+            L.pa_rotary_and_cache.argtypes = [T] * 11 + [i32, P, P]
             L.pa_decode_opt.restype = i32
             L.pa_decode_opt.argtypes = [T, T, T, T, T, T, f32, i32, P, P]
             L.pa_decode_accumulate.restype = i32
@@ -184,6 +199,7 @@ _POINTER = struct.Struct("@P")
 _SHAPE = struct.Struct("@ii10q")
 _WRITE_OPTIONS = struct.Struct("@PPqP")
 _DECODE_OPTIONS = struct.Struct("@PPqPiPNPi0P")
+_ROTARY_OPTIONS = struct.Struct("@iffPPqP")
 _PAD = ((0,) * 5, (0,) * 4, (0,) * 3, (0,) * 2, (0,), ())  # extents behind the rank
 
 
@@ -279,6 +295,45 @@ def pa_gather_cache(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_
     args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
     rc = lib().pa_gather_cache(*args, o, _stream(stream))
     _check(rc, "pa_gather_cache")
+
+
+def pa_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = PA_ROTARY_PLAIN, factor: float = 1.0,
+                          original_len: float = 0.0, low: float = 1.0, high: float = 32.0) -> torch.Tensor:
+    """int64 [rotary_dim / 2] on the host: turns per position in units of 2^-64, for pa_rotary (.to the device)."""
+    table = torch.zeros(max(int(rotary_dim), 0) // 2, dtype=torch.int64)
+    _check(lib().pa_rotary_frequencies(int(rotary_dim), float(base), int(scaling), float(factor), float(original_len),
+                                       float(low), float(high), table.data_ptr()), "pa_rotary_frequencies")
+    return table
+
+
+def _desc_or_none(t):
+    return None if t is None else _desc(t)
+
+
+def pa_rotary(q_out, q, k_out, key, positions, frequencies, q_weight=None, k_weight=None, eps: float = 1e-6,
+              interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Rows of queries q [T, Hq, D] and keys key [T, Hk, D] rotated by positions [T] (int64 or int32) into
+    q_out and k_out (which may be q and key themselves; either pair may be None).  frequencies: int64 [R / 2]
+    (pa_rotary_frequencies) or None.  With q_weight / k_weight [D] each head is normalised first."""
+    o = _ROTARY_OPTIONS.pack(1 if interleaved else 0, magnitude, eps, 0, 0, 0, 0)
+    args = tuple(map(_desc_or_none, (q_out, q, k_out, key, positions, frequencies, q_weight, k_weight)))
+    rc = lib().pa_rotary(*args, o, _stream(stream))
+    _check(rc, "pa_rotary")
+
+
+def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, frequencies,
+                        kv_dtype: int = PA_KV_AUTO, q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, magnitude: float = 1.0, k_scale=None, v_scale=None,
+                        scale_stride: int = 0, device_error=None, stream=None) -> None:
+    """pa_rotary of q (into q_out) and of key, and the rotated keys and the values written into the cache at
+    slot_mapping, in one pass; scales and kv_dtype as pa_reshape_and_cache_opt."""
+    o = _ROTARY_OPTIONS.pack(1 if interleaved else 0, magnitude, eps, _addr(k_scale), _addr(v_scale),
+                             int(scale_stride), _addr(device_error))
+    args = (_desc_or_none(q_out), _desc_or_none(q), _desc(key), _desc(value), _cache(k_cache), _cache(v_cache))
+    rc = lib().pa_rotary_and_cache(*args, _desc_or_none(positions), _desc(slot_mapping), _desc_or_none(frequencies),
+                                   _desc_or_none(q_weight), _desc_or_none(k_weight), int(kv_dtype), o,
+                                   _stream(stream))
+    _check(rc, "pa_rotary_and_cache")
 
 
 def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num_kv_heads: int,

@@ -616,6 +616,221 @@ PA_API int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_
   return launch_gather(p, cache_dt, out_dt, sm, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- rotary positions
+
+PA_API int pa_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, double original_len,
+                                 double low, double high, int64_t *frequencies) {
+  if (rotary_dim < 0 || rotary_dim % 2 || (rotary_dim > 0 && !frequencies)) return PA_ERR_INVALID_ARG;
+  if (!(base > 0.0) || std::isinf(base) || scaling < PA_ROTARY_PLAIN || scaling > PA_ROTARY_PARTS) return PA_ERR_INVALID_ARG;
+  if (scaling != PA_ROTARY_PLAIN && (!(factor > 0.0) || std::isinf(factor))) return PA_ERR_INVALID_ARG;
+  if (scaling == PA_ROTARY_BASE && rotary_dim == 2) return PA_ERR_INVALID_ARG;
+  if (scaling == PA_ROTARY_PARTS && (!(original_len > 0.0) || std::isinf(original_len) || !(low >= 0.0) || !(high > low) ||
+                                     std::isinf(high)))
+    return PA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  const double b = scaling == PA_ROTARY_BASE ? base * std::pow(factor, rotary_dim / (rotary_dim - 2.0)) : base;
+  if (!(b > 0.0) || std::isinf(b)) return PA_ERR_INVALID_ARG;
+  auto theta = [&](int i) {
+    const double x = std::pow(b, -2.0 * i / rotary_dim);
+    if (scaling == PA_ROTARY_LINEAR) return x / factor;
+    if (scaling != PA_ROTARY_PARTS) return x;
+    const double turns = original_len * x / two_pi;  // over the original context
+    const double keep = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+    return keep * x + (1.0 - keep) * (x / factor);
+  };
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(theta(i))) return PA_ERR_INVALID_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = theta(i) / two_pi, part = f - std::floor(f);  // whole turns per position turn nothing
+    const double scaled = std::nearbyint(std::ldexp(part, 64));
+    const uint64_t bits = scaled >= 0x1p64 ? 0 : static_cast<uint64_t>(scaled);
+    frequencies[i] = static_cast<int64_t>(bits);
+  }
+  return PA_OK;
+}
+
+namespace {
+
+// The rows of one kind, [T, H, D], and where they go (nullable): the checks that need no other tensor.
+int check_rows(const pa_tensor *x, const pa_tensor *out) {
+  int r;
+  if ((r = check_desc(x, 3)) || (out && (r = check_desc(out, 3)))) return r;
+  if (x->dtype != PA_F32 && x->dtype != PA_BF16 && x->dtype != PA_F16) return PA_ERR_UNSUPPORTED_DTYPE;
+  if (x->stride[2] != 1) return PA_ERR_INVALID_ARG;
+  if (x->shape[1] > 65535) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (!out) return PA_OK;
+  if (out->dtype != x->dtype) return PA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (out->shape[i] != x->shape[i]) return PA_ERR_INVALID_ARG;
+  if (out->stride[2] != 1 || rows_overlap(out, out->shape[2])) return PA_ERR_INVALID_ARG;
+  // in place: the same rows at the same places
+  if (out->data && out->data == x->data && (out->stride[0] != x->stride[0] || out->stride[1] != x->stride[1]))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+int check_row_pointers(const pa_tensor *t) {
+  const int eb = elem_bytes(t->dtype);
+  if (t->shape[0] == 0 || t->shape[1] == 0) return PA_OK;
+  if (!t->data) return PA_ERR_INVALID_ARG;
+  if (!aligned16(t->data) || (t->stride[0] * eb) % 16 || (t->stride[1] * eb) % 16) return PA_ERR_ALIGNMENT;
+  return PA_OK;
+}
+
+int check_weight(const pa_tensor *w, int64_t D, int dtype) {
+  int r;
+  if (!w) return PA_OK;
+  if ((r = check_desc(w, 1))) return r;
+  if (w->dtype != PA_F32 && w->dtype != dtype) return PA_ERR_UNSUPPORTED_DTYPE;
+  if (w->shape[0] != D || w->stride[0] != 1 || !w->data) return PA_ERR_INVALID_ARG;
+  return on_elements(w) ? PA_OK : PA_ERR_ALIGNMENT;
+}
+
+// pa_rotary (no caches) and pa_rotary_and_cache (no k_out).
+int rotary_impl(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa_tensor *key, const pa_tensor *value,
+                pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *positions, const pa_tensor *slot_mapping,
+                const pa_tensor *frequencies, const pa_tensor *q_weight, const pa_tensor *k_weight, int kv_dtype,
+                const pa_rotary_options *opt, pa_stream_t stream, bool cached) {
+  const pa_rotary_options o = opt ? *opt : pa_rotary_options{};
+  if (o.scale_stride < 0 || !(o.eps >= 0.f) || std::isinf(o.eps)) return PA_ERR_INVALID_ARG;
+  int r;
+  if (!q != !q_out || (!cached && !key != !k_out) || (cached && (!key || !value || !slot_mapping)) || (!q && !key))
+    return PA_ERR_INVALID_ARG;
+  if ((q && (r = check_rows(q, q_out))) || (key && (r = check_rows(key, k_out))) || (value && (r = check_rows(value, nullptr))))
+    return r;
+  const pa_tensor *first = q ? q : key;
+  const int dt = first->dtype;
+  const int64_t T = first->shape[0], D = first->shape[2];
+  for (const pa_tensor *t : {key, value}) {
+    if (!t) continue;
+    if (t->dtype != dt || t->shape[0] != T || t->shape[2] != D) return PA_ERR_INVALID_ARG;
+  }
+  if (D != 64 && D != 128 && D != 256) return PA_ERR_UNSUPPORTED_SHAPE;
+  int64_t pairs = 0;
+  if (frequencies) {
+    if ((r = check_desc(frequencies, 1))) return r;
+    if (frequencies->dtype != PA_I64) return PA_ERR_UNSUPPORTED_DTYPE;
+    pairs = frequencies->shape[0];
+    if (pairs > D / 2) return PA_ERR_INVALID_ARG;
+    if (pairs % 8) return PA_ERR_UNSUPPORTED_SHAPE;  // (lanes take eight pairs)
+    if (pairs > 0 && (frequencies->stride[0] != 1 || !frequencies->data)) return PA_ERR_INVALID_ARG;
+    if (pairs > 0 && !on_elements(frequencies)) return PA_ERR_ALIGNMENT;
+  }
+  if (pairs > 0) {
+    if ((r = check_desc(positions, 1))) return r;
+    if (positions->dtype != PA_I64 && positions->dtype != PA_I32) return PA_ERR_UNSUPPORTED_DTYPE;
+    if (positions->shape[0] != T || positions->stride[0] != 1) return PA_ERR_INVALID_ARG;
+  }
+  if ((q_weight && !q) || (k_weight && !key)) return PA_ERR_INVALID_ARG;
+  if ((r = check_weight(q_weight, D, dt)) || (r = check_weight(k_weight, D, dt))) return r;
+  int NB = 0, Hkv = 0, Dc = 0;
+  if (cached) {
+    if ((r = check_desc(slot_mapping, 1)) || (r = validate_cache_pair(k_cache, v_cache, &NB, &Hkv, &Dc))) return r;
+    if (slot_mapping->dtype != PA_I64) return PA_ERR_UNSUPPORTED_DTYPE;
+    const int want = kv_dtype == PA_KV_AUTO ? dt : kv_dtype == PA_KV_FP8_E4M3 ? PA_FP8_E4M3 : PA_FP4_E2M1;
+    if (kv_dtype != PA_KV_AUTO && kv_dtype != PA_KV_FP8_E4M3 && kv_dtype != PA_KV_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (k_cache->dtype != want) return PA_ERR_UNSUPPORTED_DTYPE;
+    if (Dc != D || key->shape[1] != Hkv || value->shape[1] != Hkv) return PA_ERR_INVALID_ARG;
+    if (slot_mapping->shape[0] != T || slot_mapping->stride[0] != 1) return PA_ERR_INVALID_ARG;
+  }
+  const int64_t Hq = q ? q->shape[1] : 0, Hk = key ? key->shape[1] : 0, Hv = value ? value->shape[1] : 0;
+  if (T == 0 || Hq + Hk + Hv == 0) return PA_OK;
+  if (T > INT64_MAX / (Hq + Hk + Hv) || T * (Hq + Hk + Hv) > static_cast<int64_t>(INT32_MAX) * 16)
+    return PA_ERR_UNSUPPORTED_SHAPE;  // the grid
+  for (const pa_tensor *t : {q, static_cast<const pa_tensor *>(q_out), key, static_cast<const pa_tensor *>(k_out), value})
+    if (t && (r = check_row_pointers(t))) return r;
+  if (pairs > 0 && !positions->data) return PA_ERR_INVALID_ARG;
+  if (pairs > 0 && !on_elements(positions)) return PA_ERR_ALIGNMENT;
+  if (cached && !slot_mapping->data) return PA_ERR_INVALID_ARG;
+  if (cached && !on_elements(slot_mapping)) return PA_ERR_ALIGNMENT;
+  if (!aligned4(o.k_scale) || !aligned4(o.v_scale) || !aligned4(o.device_error)) return PA_ERR_ALIGNMENT;
+
+  const int eb = elem_bytes(dt);
+  RotaryParams p{};
+  p.T = T;
+  p.D = static_cast<int>(D);
+  p.R = static_cast<int>(2 * pairs);
+  p.Hq = static_cast<int>(Hq);
+  p.Hk = static_cast<int>(Hk);
+  p.Hv = static_cast<int>(Hv);
+  p.wide = true;
+  auto rows = [&](const pa_tensor *t, int64_t &ts, int64_t &hs) {
+    if (!t) return static_cast<char *>(nullptr);
+    ts = t->stride[0] * eb;
+    hs = t->stride[1] * eb;
+    p.wide = p.wide && rows_aligned32(t, eb);
+    return static_cast<char *>(t->data);
+  };
+  p.q = rows(q, p.q_ts, p.q_hs);
+  p.q_out = rows(q_out, p.qo_ts, p.qo_hs);
+  p.key = rows(key, p.key_ts, p.key_hs);
+  p.k_out = rows(k_out, p.ko_ts, p.ko_hs);
+  p.value = rows(value, p.val_ts, p.val_hs);
+  if (pairs > 0) {
+    p.positions = positions->data;
+    p.pos64 = positions->dtype == PA_I64;
+    p.frequencies = static_cast<const uint64_t *>(frequencies->data);
+  }
+  if (q_weight) {
+    p.q_weight = q_weight->data;
+    p.q_weight_dtype = q_weight->dtype;
+  }
+  if (k_weight) {
+    p.k_weight = k_weight->data;
+    p.k_weight_dtype = k_weight->dtype;
+  }
+  p.magnitude = o.magnitude == 0.f ? 1.f : o.magnitude;
+  p.eps = o.eps;
+  p.interleaved = o.interleaved != 0;
+  p.err = o.device_error;
+  if (cached) {
+    const int cb = elem_bytes(k_cache->dtype);
+    const bool paged4 = k_cache->dtype == PA_FP4_E2M1;
+    p.slots = static_cast<const int64_t *>(slot_mapping->data);
+    p.k_cache = static_cast<char *>(k_cache->data);
+    p.v_cache = static_cast<char *>(v_cache->data);
+    p.kc_s0 = k_cache->stride[0] * cb;
+    p.kc_s1 = k_cache->stride[1] * cb;
+    p.kc_s2 = paged4 ? 0 : k_cache->stride[2] * cb;
+    p.vc_s0 = v_cache->stride[0] * cb;
+    p.vc_s1 = v_cache->stride[1] * cb;
+    p.vc_s2 = paged4 ? 0 : v_cache->stride[2] * cb;
+    p.num_slots = static_cast<int64_t>(NB) * kBlock;
+    if (kv_dtype == PA_KV_AUTO) {
+      for (const pa_tensor *c : {k_cache, v_cache})
+        p.wide = p.wide && rows_aligned32(c, cb) && (c->stride[2] * cb) % 32 == 0;
+    } else {
+      p.k_scale = o.k_scale;
+      p.v_scale = o.v_scale;
+      p.scale_stride = o.scale_stride;
+    }
+  }
+  const int sm = device_sm_count();
+  if (sm <= 0) return PA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!cached) return launch_rotary(p, dt, dt, sm, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  ProfScope ps(PA_KERNEL_WRITE, st);
+  return launch_rotary(p, dt, k_cache->dtype, sm, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+PA_API int pa_rotary(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa_tensor *key,
+                     const pa_tensor *positions, const pa_tensor *frequencies, const pa_tensor *q_weight,
+                     const pa_tensor *k_weight, const pa_rotary_options *opt, pa_stream_t stream) {
+  return rotary_impl(q_out, q, k_out, key, nullptr, nullptr, nullptr, positions, nullptr, frequencies, q_weight,
+                     k_weight, PA_KV_AUTO, opt, stream, false);
+}
+
+PA_API int pa_rotary_and_cache(pa_tensor *q_out, const pa_tensor *q, const pa_tensor *key, const pa_tensor *value,
+                               pa_tensor *k_cache, pa_tensor *v_cache, const pa_tensor *positions,
+                               const pa_tensor *slot_mapping, const pa_tensor *frequencies, const pa_tensor *q_weight,
+                               const pa_tensor *k_weight, int kv_dtype, const pa_rotary_options *opt,
+                               pa_stream_t stream) {
+  return rotary_impl(q_out, q, nullptr, key, value, k_cache, v_cache, positions, slot_mapping, frequencies, q_weight,
+                     k_weight, kv_dtype, opt, stream, true);
+}
+
 PA_API int pa_decode_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_blocks_per_seq,
                           int kv_dtype_code, int sm_count, int partition_size, int *partition_out,
                           int *num_partitions_out) {

@@ -77,6 +77,35 @@ struct GatherParams {
   bool i32;                        // T, block count and every stride below 2^31
 };
 
+// Rotation (and norm) of query and key rows (pa_rotary.cu); strides in bytes (s2, the token stride, 0
+// for a 4-bit cache).
+struct RotaryParams {
+  const char *q, *key, *value;
+  char *q_out, *k_out;             // k_out: without a cache
+  char *k_cache, *v_cache;         // nullable: keys go to k_out, no values
+  const void *positions;           // int64 (pos64) or int32
+  const int64_t *slots;
+  const uint64_t *frequencies;     // [R / 2], turns per position in 2^-64
+  const void *q_weight, *k_weight; // [D], nullable (no norm)
+  int q_weight_dtype, k_weight_dtype;
+  int64_t T;
+  int Hq, Hk, Hv;                  // heads of queries, keys and values (0: none)
+  int D, R;                        // head size, rotated part (a multiple of 16)
+  int64_t q_ts, q_hs, qo_ts, qo_hs, key_ts, key_hs, ko_ts, ko_hs, val_ts, val_hs;
+  int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
+  int64_t num_slots;
+  const float *k_scale, *v_scale;  // nullable (1.0)
+  int64_t scale_stride;
+  int *err;
+  float magnitude, eps;
+  bool pos64, interleaved;
+  bool wide;                       // every 32-byte piece of the rows (and of a cache of their type) is aligned
+  int rows_per_cta;                // set by the launch, as is the reciprocal of the rows per token
+  uint32_t magic;
+};
+// Dynamic shared memory of the largest launch: 256 / (D / 16) x 4 rows of one head each.
+constexpr int kRotarySmem = 68 * 1024;
+
 struct DecodeParams {
   void *out;
   const void *q;
@@ -177,6 +206,9 @@ cudaError_t launch_write(const WriteParams &p, int in_dtype, int cache_dtype, in
 
 cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t st);
 cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, int sm_count, cudaStream_t st);
+
+// k_cache null: rows only, else the cache type says what becomes of keys and values.
+cudaError_t launch_rotary(const RotaryParams &p, int dtype, int cache_dtype, int sm_count, cudaStream_t st);
 
 constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND_FP4_F16Q; }
 // Tensor-core kernel shape per (kind, head size): warps per CTA and pipeline

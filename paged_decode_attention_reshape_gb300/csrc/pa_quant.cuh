@@ -1,5 +1,5 @@
-// pa_quant.cuh -- input rows as fp32 values and the quotients that quantisation takes, shared
-// by the cache writes (pa_write.cu, pa_fp4.cu).
+// pa_quant.cuh -- input rows as fp32 values, the quotients that quantisation takes and the E4M3
+// conversion, shared by the cache writes (pa_write.cu, pa_fp4.cu, pa_rotary.cu).
 #pragma once
 
 #include "pa_device.cuh"
@@ -107,6 +107,68 @@ __device__ __forceinline__ float clamp_mag(float x) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(x)), "f"(0x1p80f));
   return r;
+}
+
+// E4M3 code pair of two quotients (cvt ... satfinite: round-to-nearest-even with
+// saturation); low byte = a.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+
+// One 16-byte pack of inputs -> E4M3 codes of x / scale (correctly rounded quotient).
+// 16-bit inputs: the codes of |x| / |s| are computed with |x| clamped to 2^80 (a NaN stays
+// NaN), which keeps the fused steps exact for every input -- nothing overflows, and a |x|
+// small enough for the steps to lose exactness gives a quotient far below the smallest E4M3
+// value -- and the sign of x / s is put back on each code (round to nearest even and
+// saturation are symmetric in the sign).  Zero, infinite and NaN inputs then need no branch.
+template <int DT>
+__device__ __forceinline__ void store_fp8(char *dst, const uint4 &v, const Divisor &dv) {
+  constexpr int E = 16 / In<DT>::bytes;
+  float x[E], q[E];
+  unpack8<DT>(v, x);
+  if constexpr (E == 8) {
+    if (dv.fast) {
+      const Divisor da{fabsf(dv.s), fabsf(dv.y), true};
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const float2 r = da.div2_fast(clamp_mag(x[i]), clamp_mag(x[i + 1]));
+        q[i] = r.x;
+        q[i + 1] = r.y;
+      }
+      // sign bits of elements 0..3 and 4..7 (bit 15 of each 16-bit input) into bit 7 of
+      // each code byte, flipped for a negative scale
+      const uint32_t neg = dv.s < 0.f ? 0x80808080u : 0u;
+      uint2 o;
+      o.x = e4m3_pair(q[0], q[1]) | (e4m3_pair(q[2], q[3]) << 16);
+      o.y = e4m3_pair(q[4], q[5]) | (e4m3_pair(q[6], q[7]) << 16);
+      o.x |= (__byte_perm(v.x, v.y, 0x7531) ^ neg) & 0x80808080u;
+      o.y |= (__byte_perm(v.z, v.w, 0x7531) ^ neg) & 0x80808080u;
+      *reinterpret_cast<uint2 *>(dst) = o;
+      return;
+    }
+  }
+  bool fast = dv.fast;
+#pragma unroll
+  for (int i = 0; i < E; ++i) fast &= Divisor::in_range(x[i]);
+  if (fast) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const float2 r = dv.div2_fast(x[i], x[i + 1]);
+      q[i] = r.x;
+      q[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) q[i] = dv.div(x[i]);
+  }
+  if constexpr (E == 8) {
+    uint2 o;
+    o.x = e4m3_pair(q[0], q[1]) | (e4m3_pair(q[2], q[3]) << 16);
+    o.y = e4m3_pair(q[4], q[5]) | (e4m3_pair(q[6], q[7]) << 16);
+    *reinterpret_cast<uint2 *>(dst) = o;
+  } else {
+    *reinterpret_cast<uint32_t *>(dst) = e4m3_pair(q[0], q[1]) | (e4m3_pair(q[2], q[3]) << 16);
+  }
 }
 
 }  // namespace pa
