@@ -19,6 +19,8 @@
  *   pa_decode_step         the cache write and the decode of one step in one call
  *   pa_decode_accumulate   the decode that also adds up every token's attention weight
  *   pa_evict               a sequence shortened to its recent and heaviest tokens, in place
+ *   pa_decode_window       the decode over the last tokens of a window and a few first ones
+ *   pa_attention_window    the same for several new query tokens per sequence
  *   pa_attention_varlen    several new query tokens per sequence, causal
  *                          ("Inside vLLM CUDA Kernels", Part 3, the varlen read path);
  *                          long chunks run on a tcgen05 query-tile kernel
@@ -506,6 +508,38 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
                         const pa_tensor *query_start_loc, const pa_tensor *block_table, const pa_tensor *seq_lens,
                         float scale, int num_kv_heads, int max_query_len, const pa_decode_options *opt,
                         pa_stream_t stream);
+
+/*
+ * pa_decode_window, pa_attention_window -- pa_decode_opt and pa_attention_varlen under a sliding window
+ * with a few first tokens that stay visible: a query at position P sees the tokens t <= P with
+ * t > P - window or t < sinks.
+ *
+ *   window           >= 1: the tokens a query sees up to and with its own, besides the first ones.
+ *   sinks            >= 0: first tokens that every query sees.
+ *   other arguments  as pa_decode_opt (pa_attention_varlen), ALiBi, scales and every split included.
+ * Only pages that hold a visible token are read: entries of the block table between the first tokens'
+ * pages and the window's (its start is max(0, P + 1 - window), of the sequence's first query) may hold any
+ * value, so their blocks can be given back.  Cost and workspace go by the window, not by the length.
+ * Tokens of a page that is read which no query of the sequence sees never reach the output, whatever
+ * they hold; a key or value that some query sees has to be finite for the other queries of its sequence
+ * in the same call (they are multiplied by a weight of zero).
+ * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen).
+ * Under a window a partition_size counts the visible tokens' pages, so it can be small.
+ */
+int pa_decode_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                     const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads, int window,
+                     int sinks, const pa_decode_options *opt, pa_stream_t stream);
+int pa_attention_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                        const pa_tensor *query_start_loc, const pa_tensor *block_table, const pa_tensor *seq_lens,
+                        float scale, int num_kv_heads, int max_query_len, int window, int sinks,
+                        const pa_decode_options *opt, pa_stream_t stream);
+
+/* Bytes of workspace that either call needs for this shape and partition_size on the current device (0 when
+ * it does not split, for invalid arguments, or when no device can be queried).  kv_dtype_code: pa_dtype of
+ * the cache; max_query_len: 1 for pa_decode_window.  Host-only. */
+size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                       int max_blocks_per_seq, int kv_dtype_code, int window, int sinks,
+                                       int max_query_len, int partition_size);
 
 /*
  * pa_decode_step -- one decode step in one call: the cache write of the step's new rows

@@ -36,6 +36,7 @@ STATUS = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED_DTYPE", 
 EXPORTS = ("pa_reshape_and_cache", "pa_reshape_and_cache_opt", "pa_decode", "pa_decode_ex", "pa_decode_opt",
            "pa_gather_cache", "pa_decode_accumulate", "pa_decode_accumulate_workspace_size",
            "pa_rotary_frequencies", "pa_rotary", "pa_rotary_and_cache",
+           "pa_decode_window", "pa_attention_window", "pa_decode_window_workspace_size",
            "pa_evict", "pa_bm_truncate",
            "pa_attention_varlen", "pa_decode_step", "pa_decode_noalloc", "pa_decode_plan", "pa_decode_workspace_size", "pa_check_device_error",
            "pa_status_string", "pa_profile_enable", "pa_profile_read", "pa_bm_create", "pa_bm_destroy",
@@ -119,6 +120,12 @@ def lib() -> ctypes.CDLL:
             L.pa_decode_accumulate.argtypes = [T, T, T, T, T, T, f32, i32, T, P, P]
             L.pa_decode_accumulate_workspace_size.restype = ctypes.c_size_t
             L.pa_decode_accumulate_workspace_size.argtypes = [i32] * 6
+            L.pa_decode_window.restype = i32
+            L.pa_decode_window.argtypes = [T, T, T, T, T, T, f32, i32, i32, i32, P, P]
+            L.pa_attention_window.restype = i32
+            L.pa_attention_window.argtypes = [T, T, T, T, T, T, T, f32, i32, i32, i32, i32, P, P]
+            L.pa_decode_window_workspace_size.restype = ctypes.c_size_t
+            L.pa_decode_window_workspace_size.argtypes = [i32] * 10
             L.pa_decode_step.restype = i32
             L.pa_decode_step.argtypes = [T, T, T, T, T, T, T, T, T, T, f32, i32, P, P]
             L.pa_attention_varlen.restype = i32
@@ -374,6 +381,42 @@ def pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_
     """Bytes of pa_decode_accumulate's workspace; zero-fill it once before first use (torch.zeros)."""
     return int(lib().pa_decode_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size,
                                                          max_blocks_per_seq, partition_size))
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num_kv_heads: int, window: int,
+                     sinks: int = 0, k_scale=None, v_scale=None, scale_stride: int = 0, alibi_slopes=None,
+                     partition_size: int = 0, workspace=None, device_error=None, stream=None,
+                     first_wait_limit: int = 0) -> None:
+    """pa_decode_opt over the last `window` tokens of each sequence and its first `sinks` ones.  Table entries
+    of pages in between are not read.  A caller's workspace needs pa_decode_window_workspace_size bytes."""
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    rc = lib().pa_decode_window(*args, float(scale), int(num_kv_heads), int(window), int(sinks), o, _stream(stream))
+    _check(rc, "pa_decode_window")
+
+
+def pa_attention_window(out, q, k_cache, v_cache, query_start_loc, block_table, seq_lens, scale: float,
+                        num_kv_heads: int, max_query_len: int, window: int, sinks: int = 0, k_scale=None, v_scale=None,
+                        scale_stride: int = 0, alibi_slopes=None, partition_size: int = 0, workspace=None,
+                        device_error=None, stream=None, first_wait_limit: int = 0) -> None:
+    """pa_attention_varlen where query i of sequence s, at position P, sees the last `window` tokens up to P
+    and the first `sinks` ones.  Workspace as pa_decode_window."""
+    o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
+                        first_wait_limit)
+    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(query_start_loc), _desc(block_table),
+            _desc(seq_lens))
+    rc = lib().pa_attention_window(*args, float(scale), int(num_kv_heads), int(max_query_len), int(window), int(sinks),
+                                   o, _stream(stream))
+    _check(rc, "pa_attention_window")
+
+
+def pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, kv_dtype_code,
+                                    window, sinks=0, max_query_len=1, partition_size=0) -> int:
+    """Bytes of workspace of pa_decode_window (max_query_len 1) or pa_attention_window; zero-fill it once
+    before first use (torch.zeros)."""
+    return int(lib().pa_decode_window_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq,
+                                                     kv_dtype_code, window, sinks, max_query_len, partition_size))
 
 
 def pa_evict(k_cache, v_cache, block_table, seq_lens, weights, budget: int, recent: int, kept, new_seq_lens,

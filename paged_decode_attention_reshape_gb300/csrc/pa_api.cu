@@ -285,6 +285,18 @@ Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool 
   return pl;
 }
 
+// Under a window: the most pages that a work item of the decode kernels reads (its numbers of Window),
+// for 8 columns of G heads a query and at most nq queries.  Windows and first tokens as given by the caller.
+int window_blocks(int maxNB, int64_t window, int64_t sinks, int G, int nq) {
+  const int64_t span = std::min(nq, 7 / G + 2);  // queries among 8 columns
+  const int64_t pages = (window + span - 1 + kBlock - 2) / kBlock + 1 + (sinks + kBlock - 1) / kBlock;
+  return static_cast<int>(std::min<int64_t>(maxNB, pages));
+}
+// The plan of a call under a window, of maxNB pages by window_blocks.
+Plan make_window_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, int request, bool varlen) {
+  return make_plan(S, Hq, Hkv, D, maxNB, kind, sm, device, request, varlen, false);
+}
+
 // Split-KV workspace: [arrival counters, one int per (sequence, kv head, head group)]
 // [partial (m, l): one float2 per row] [partial acc: D floats per row], each region
 // starting on a 256-byte boundary.  Rows: one per (sequence, head, partition) for
@@ -831,21 +843,26 @@ PA_API int pa_rotary_and_cache(pa_tensor *q_out, const pa_tensor *q, const pa_te
                      k_weight, kv_dtype, opt, stream, true);
 }
 
+// A decode kernel that reads a cache of this element type, -1 for none.
+static int kind_of_cache(int dtype) {
+  switch (dtype) {
+    case PA_FP8_E4M3: return KIND_FP8_BF16Q;
+    case PA_FP4_E2M1: return KIND_FP4_BF16Q;
+    case PA_BF16: return KIND_BF16;
+    case PA_F16: return KIND_F16;
+    case PA_F32: return KIND_F32;
+    default: return -1;
+  }
+}
+
 PA_API int pa_decode_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_blocks_per_seq,
                           int kv_dtype_code, int sm_count, int partition_size, int *partition_out,
                           int *num_partitions_out) {
   if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_size <= 0 ||
       max_blocks_per_seq < 0)
     return PA_ERR_INVALID_ARG;
-  int kind;
-  switch (kv_dtype_code) {
-    case PA_FP8_E4M3: kind = KIND_FP8_BF16Q; break;
-    case PA_FP4_E2M1: kind = KIND_FP4_BF16Q; break;
-    case PA_BF16: kind = KIND_BF16; break;
-    case PA_F16: kind = KIND_F16; break;
-    case PA_F32: kind = KIND_F32; break;
-    default: return PA_ERR_INVALID_ARG;
-  }
+  const int kind = kind_of_cache(kv_dtype_code);
+  if (kind < 0) return PA_ERR_INVALID_ARG;
   const bool device = sm_count <= 0;
   if (device) sm_count = device_sm_count();
   if (sm_count <= 0) return PA_ERR_CUDA;
@@ -888,6 +905,39 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
   return workspace_layout(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, P, 0).total;
 }
 
+PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                              int max_blocks_per_seq, int kv_dtype_code, int window, int sinks,
+                                              int max_query_len, int partition_size) {
+  const int kind = kind_of_cache(kv_dtype_code);
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_size <= 0 ||
+      max_blocks_per_seq < 0 || max_blocks_per_seq > INT32_MAX / kBlock || kind < 0 || window < 1 || sinks < 0 ||
+      max_query_len < 1 || static_cast<int64_t>(num_heads) * max_query_len > INT32_MAX)
+    return 0;
+  const int sm = device_sm_count();
+  if (sm <= 0) return 0;
+  const int Hqv = num_heads * max_query_len;
+  size_t need = 0;
+  for (const bool varlen : {false, true}) {  // (a call of pa_attention_window may have one query each, too)
+    if (!varlen && max_query_len > 1) continue;
+    if (varlen && partition_size == PA_PARTITION_BALANCED) continue;
+    int NB = max_blocks_per_seq;
+    Plan pl;
+    if (static_cast<int64_t>(window) + sinks >= static_cast<int64_t>(NB) * kBlock) {
+      for (const bool plain : {false, true}) {
+        pl = make_plan(num_seqs, Hqv, num_kv_heads, head_size, NB, kind, sm, true, partition_size, varlen, plain);
+        if (pl.status == PA_OK && pl.cluster == 0 && (pl.flat > 0 || (pl.P > 0 && pl.P < NB * kBlock)))
+          need = std::max(need, workspace_layout(num_seqs, Hqv, num_kv_heads, head_size, NB, pl.P, pl.flat).total);
+      }
+      continue;
+    }
+    NB = window_blocks(NB, window, sinks, num_heads / num_kv_heads, max_query_len);
+    pl = make_window_plan(num_seqs, Hqv, num_kv_heads, head_size, NB, kind, sm, true, partition_size, varlen);
+    if (pl.status == PA_OK && pl.cluster == 0 && (pl.flat > 0 || (pl.P > 0 && pl.P < NB * kBlock)))
+      need = std::max(need, workspace_layout(num_seqs, Hqv, num_kv_heads, head_size, NB, pl.P, pl.flat).total);
+  }
+  return need;
+}
+
 PA_API size_t pa_decode_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                                   int max_blocks_per_seq, int partition_size) {
   if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_size < 0 ||
@@ -908,7 +958,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
                 const pa_decode_options &o, bool internal_ws, pa_stream_t stream,
                 const pa_tensor *query_start_loc = nullptr, int max_query_len = 1,
                 const pa_tensor *new_rows_start = nullptr, bool early = false, bool dry = false,
-                size_t *ws_need = nullptr, size_t *ws_counters = nullptr, pa_tensor *weights = nullptr) {
+                size_t *ws_need = nullptr, size_t *ws_counters = nullptr, pa_tensor *weights = nullptr,
+                int64_t window = 0, int64_t sinks = 0) {
   const float *k_scale = o.k_scale, *v_scale = o.v_scale;
   const int partition_size = o.partition_size;
   void *workspace = o.workspace;
@@ -988,17 +1039,21 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   const int VH = (Hq / Hkv) * (varlen ? max_query_len : 1);
   const int Hqv = Hkv * VH;
   const int maxNB = static_cast<int>(block_table->shape[1]);
+  if (window + sinks >= static_cast<int64_t>(maxNB) * kBlock) window = sinks = 0;  // every token is seen
+  // pages that a work item reads at most
+  const int NBw = window > 0 ? window_blocks(maxNB, window, sinks, Hq / Hkv, varlen ? max_query_len : 1) : maxNB;
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
   // Chunks of query tokens run on the query-tile kernel (rows in the MMA M dimension, pages
   // shared by 64 rows, no split) unless a split was asked for.
   const bool chunk = varlen && (kind == KIND_BF16 || kind == KIND_F16) && (D == 64 || D == 128) &&
                      (partition_size == 0 || partition_size == -1) && VH >= chunk_min_columns(D);
-  const Plan pl = make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,
-                            !varlen && !o.alibi_slopes);
+  const Plan pl = window > 0 ? make_window_plan(S, Hqv, Hkv, D, NBw, kind, sm, true, chunk ? -1 : partition_size, varlen)
+                             : make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,
+                                         !varlen && !o.alibi_slopes);
   if (pl.status != PA_OK) return pl.status;
   const int P = pl.P;
-  const int max_parts = pl.cluster > 1 ? pl.cluster : P > 0 ? (maxNB * kBlock + P - 1) / P : 1;
+  const int max_parts = pl.cluster > 1 ? pl.cluster : P > 0 ? (NBw * kBlock + P - 1) / P : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   DecodeParams p{};
@@ -1028,6 +1083,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   p.v_scale = v_scale;
   p.scale_stride = o.scale_stride;
   p.alibi = o.alibi_slopes;
+  p.window = static_cast<int>(window);
+  p.sinks = static_cast<int>(sinks);
   p.pages_per_part = P > 0 ? P / kBlock : std::max(maxNB, 1);
   p.max_parts = max_parts;
   p.cluster = pl.cluster;
@@ -1070,7 +1127,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   }
   size_t to_clear = 0;
   if ((max_parts > 1 && pl.cluster <= 1) || pl.flat > 0 || weights) {
-    const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, maxNB, max_parts > 1 ? P : 0, pl.flat);
+    const WsLayout lay = workspace_layout(S, Hqv, Hkv, D, NBw, max_parts > 1 ? P : 0, pl.flat);
     const ScoreLayout sc = weights ? score_layout(S, Hq, Hkv, maxNB) : ScoreLayout{0, 0, 0};
     const size_t total = weights ? round256(lay.total) + sc.total : lay.total;
     size_t ml_off = lay.ml_off;
@@ -1121,17 +1178,19 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     p.vc_s0 = v_cache->stride[0];
     p.vc_s1 = v_cache->stride[1];
     ProfScope ps(PA_KERNEL_DECODE, st);
-    e = pl.warps ? launch_decode_fp4_warps(p, kind, sm * mma_min_ctas(kind, D), st) : launch_decode_mma_fp4(p, kind, st);
+    e = pl.warps        ? launch_decode_fp4_warps(p, kind, sm * mma_min_ctas(kind, D), st)
+        : p.window > 0 ? launch_decode_window_fp4(p, kind, st)
+                       : launch_decode_mma_fp4(p, kind, st);
   } else {
     ProfScope ps(PA_KERNEL_DECODE, st);
     if (chunk) {
       CUtensorMap tmQ{};
       p.q_tma = make_q_map(q, p.G, &tmQ) == PA_OK ? 1 : 0;
-      e = launch_chunk_umma(p, kind, tmK, tmV, tmQ, st);
+      e = p.window > 0 ? launch_chunk_window(p, kind, tmK, tmV, tmQ, st) : launch_chunk_umma(p, kind, tmK, tmV, tmQ, st);
     } else if (kind == KIND_BF16 || kind == KIND_F16) {
-      e = launch_decode_mma_16(p, kind, tmK, tmV, st);
+      e = p.window > 0 ? launch_decode_window_16(p, kind, tmK, tmV, st) : launch_decode_mma_16(p, kind, tmK, tmV, st);
     } else {
-      e = launch_decode_mma_fp8(p, kind, tmK, tmV, st);
+      e = p.window > 0 ? launch_decode_window_fp8(p, kind, tmK, tmV, st) : launch_decode_mma_fp8(p, kind, tmK, tmV, st);
     }
   }
   if (e == cudaSuccess && weights && maxNB > 0) {
@@ -1220,6 +1279,27 @@ PA_API int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tens
   const bool internal = !o.workspace && o.workspace_bytes == 0;
   return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
                      query_start_loc, max_query_len);
+}
+
+PA_API int pa_decode_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                            const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads,
+                            int window, int sinks, const pa_decode_options *opt, pa_stream_t stream) {
+  if (window < 1 || sinks < 0) return PA_ERR_INVALID_ARG;
+  const pa_decode_options o = opt ? *opt : pa_decode_options{};
+  const bool internal = !o.workspace && o.workspace_bytes == 0;
+  return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
+                     nullptr, 1, nullptr, false, false, nullptr, nullptr, nullptr, window, sinks);
+}
+
+PA_API int pa_attention_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
+                               const pa_tensor *query_start_loc, const pa_tensor *block_table,
+                               const pa_tensor *seq_lens, float scale, int num_kv_heads, int max_query_len, int window,
+                               int sinks, const pa_decode_options *opt, pa_stream_t stream) {
+  if (!query_start_loc || window < 1 || sinks < 0) return PA_ERR_INVALID_ARG;
+  const pa_decode_options o = opt ? *opt : pa_decode_options{};
+  const bool internal = !o.workspace && o.workspace_bytes == 0;
+  return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
+                     query_start_loc, max_query_len, nullptr, false, false, nullptr, nullptr, nullptr, window, sinks);
 }
 
 PA_API int pa_decode_step(pa_tensor *out, const pa_tensor *q, const pa_tensor *key, const pa_tensor *value,

@@ -37,6 +37,13 @@
 // of one issuer run in order, so S of group k + 2 may overwrite the P that P.V of group k
 // reads.  Tile 0 zeroes the V rows past the sequence in the last page before it hands over
 // its P and arrives on v_tail (used once), which the other tiles' last P.V waits for.
+//
+// Under a window (WIN, pa_attention_window: a query at position P sees t <= P with t > P - window or
+// t < sinks) the scan takes the pages of the first tokens, in groups of their own, and then those from
+// the first query's window on; where the two meet there is one run of pages and no gap.  Rows mask what
+// lies outside their own window in the groups at its edges; the V rows that no query of the CTA sees
+// (behind the first tokens, before the window) are zeroed like the tail, each group's on a barrier of
+// its own that is used once.
 #pragma once
 
 #include "pa_device.cuh"
@@ -210,8 +217,8 @@ struct UmmaCfg {
   static constexpr int RING = R * BOXB;               // one box region of a ring
   static constexpr int QOFF = 0, KOFF = T * QTILE, VOFF = KOFF + NBOX * RING, BAR_OFF = VOFF + NBOX * RING;
   // barriers: full[NS], empty[NS]; per tile s_full x2, p_full x2, o_done, drain (48 bytes);
-  // q_full, v_tail
-  static constexpr int TBAR = 2 * NS * 8, NBARS = 2 * NS + 6 * T + 2;
+  // q_full, v_tail, v_gap x2 (under a window)
+  static constexpr int TBAR = 2 * NS * 8, NBARS = 2 * NS + 6 * T + 4;
   static constexpr size_t SMEM = 1024 + BAR_OFF + NBARS * 8 + 16;
   static constexpr uint32_t TMEM_COLS = 256 * T;      // tile t: S/P buffers at 256 t + 0 / 64, O at 256 t + 128
   static constexpr uint32_t OCOL = 128;
@@ -230,7 +237,34 @@ __device__ __forceinline__ bool umma_wait(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 
-template <int KIND, int D, int T>
+// The groups of 4 pages that a CTA under a window scans.
+struct WindowGroups {
+  int first;       // first page of the window's run
+  int ns, sinks_groups;  // pages of the first tokens (0: they belong to the run), their groups
+  int gap0, gap1;  // groups with tokens of [sinks, start), which no query sees, to zero (-1: none)
+  __device__ __forceinline__ WindowGroups() : first(0), ns(0), sinks_groups(0), gap0(-1), gap1(-1) {}
+  __device__ __forceinline__ WindowGroups(const Window &w) {
+    ns = w.skip == 0 ? 0 : w.ns;
+    first = w.skip == 0 ? 0 : w.ns + w.skip;
+    sinks_groups = (ns + 3) / 4;
+    gap0 = gap1 = -1;
+    if (w.sinks < w.start) {
+      // the hidden tokens of the pages that are read: one run (no gap), or the end of the first tokens'
+      // last page and the start of the window's first
+      const int a = w.skip == 0 ? w.sinks / (4 * kBlock) : (w.sinks % kBlock ? (ns - 1) / 4 : -1);
+      const int b = w.skip == 0 ? (w.start - 1) / (4 * kBlock) : (w.start > first * kBlock ? sinks_groups : -1);
+      gap0 = a >= 0 && ns + (w.skip == 0) > 0 ? a : -1;
+      gap1 = b != gap0 ? b : -1;
+    }
+  }
+  __device__ __forceinline__ int base(int k) const { return k < sinks_groups ? 4 * k : first + 4 * (k - sinks_groups); }
+  // pages of group k, npages the end of the run
+  __device__ __forceinline__ int pages(int k, int npages) const {
+    return min(4, (k < sinks_groups ? ns : npages) - base(k));
+  }
+};
+
+template <int KIND, int D, int T, bool WIN>
 __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D, T>::MIN_CTAS)
     chunk_umma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
@@ -248,6 +282,7 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
   auto odone = [&](int t) { return tbar0 + 48u * t + 32u; };
   auto drain = [&](int t) { return tbar0 + 48u * t + 40u; };
   const uint32_t qfull = tbar0 + 48u * T, vtailb = qfull + 8u;
+  auto vgap = [&](int i) { return vtailb + 8u + 8u * i; };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + C::BAR_OFF + C::NBARS * 8);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *bad_block = reinterpret_cast<volatile int *>(tmem_slot + 2);
@@ -277,7 +312,12 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
   const int pos0 = len - nq;                    // row r sees tokens 0 .. pos0 + r / G
   const int vis = pos0 + (r0 + nrows - 1) / G + 1;
   const int npages = (vis + kBlock - 1) / kBlock;
-  const int ngr = (npages + C::GP - 1) / C::GP;
+  const Window win = WIN ? make_window(p.window, p.sinks, pos0 + r0 / G) : Window{};
+  const WindowGroups wg = WIN ? WindowGroups(win) : WindowGroups();
+  const int ngr = WIN ? wg.sinks_groups + (npages - wg.first + C::GP - 1) / C::GP : (npages + C::GP - 1) / C::GP;
+  // first page and number of pages of group k
+  auto group_base = [&](int k) { return WIN ? wg.base(k) : k * C::GP; };
+  auto group_pages = [&](int k) { return WIN ? wg.pages(k, npages) : min(C::GP, npages - k * C::GP); };
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full0 + 8 * i, 1);
@@ -293,6 +333,10 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     }
     mbar_init(qfull, 1);
     mbar_init(vtailb, 128);
+    if (WIN) {
+      mbar_init(vgap(0), 128);
+      mbar_init(vgap(1), 128);
+    }
     *abort = 0;
     *bad_block = 0;
     fence_barrier_init();
@@ -346,7 +390,7 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     const uint64_t pol = policy_evict_normal();  // the other row tiles of (s, g) read the same pages
     const int c1 = p.nhd ? g : 0, c2 = p.nhd ? 0 : g;
     // block-table entries are read one group ahead, off the path from a free slot to its copies
-    int pid_next = lane < min(C::GP, npages) ? __ldg(bt + lane) : 0;
+    int pid_next = lane < group_pages(0) ? __ldg(bt + group_base(0) + lane) : 0;
     if (p.q_tma && lane == 0) {
       // Q first: the row tiles' boxes (query tokens x G heads x 64 dims each); rows past nrows
       // hold other tokens or zeros, and only feed rows that are never stored
@@ -360,9 +404,9 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     for (int k = 0; k < ngr; ++k) {
       const int gs = k % C::NS;
       if (k >= C::NS && !__all_sync(0xffffffffu, umma_wait(empty0 + 8 * gs, ((k / C::NS) - 1) & 1, abort))) break;
-      const int npg = min(C::GP, npages - k * C::GP);
+      const int npg = group_pages(k);
       int pid = pid_next;
-      if (k + 1 < ngr) pid_next = lane < min(C::GP, npages - (k + 1) * C::GP) ? __ldg(bt + (k + 1) * C::GP + lane) : 0;
+      if (k + 1 < ngr) pid_next = lane < group_pages(k + 1) ? __ldg(bt + group_base(k + 1) + lane) : 0;
       if (lane < npg && (pid < 0 || pid >= p.num_blocks)) {
         *bad_block = 1;
         if (p.err) atomicOr(p.err, kErrBlock);
@@ -419,12 +463,17 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
         }
         if (k >= 1) {
           const int kp = k - 1, gsp = kp % C::NS, bp = kp & 1;
-          const int npg = min(C::GP, npages - kp * C::GP);
+          const int npg = group_pages(kp);
           if (!__all_sync(0xffffffffu, umma_wait(pfull(t, bp), (kp >> 1) & 1, abort))) break;
           // the last page's V tail is zeroed by tile 0 before it hands over its P; the other
           // tiles' last P.V waits for that on v_tail, a barrier used once (a parity wait on
           // tile 0's p_full could pass a phase early if tile 0 ran several groups behind)
           if (t > 0 && kp == ngr - 1 && vtail && !__all_sync(0xffffffffu, umma_wait(vtailb, 0, abort))) break;
+          if constexpr (WIN) {
+            if (t > 0 && (kp == wg.gap0 || kp == wg.gap1) &&
+                !__all_sync(0xffffffffu, umma_wait(vgap(kp == wg.gap0 ? 0 : 1), 0, abort)))
+              break;
+          }
           umma::fence_after();
           if (elect_one()) {
             for (int i = 0; i < npg; ++i) {
@@ -464,8 +513,10 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
       }
       // ---- logits in log2 units, masked past the row's position; a group the whole warp
       // sees in full (or rows without a query) skips the mask
-      const int t0 = k * C::GP * kBlock;
-      const bool whole = __all_sync(0xffffffffu, t0 + 63 <= pos || !valid);
+      const int t0 = group_base(k) * kBlock;
+      bool mine = t0 + 63 <= pos;
+      if constexpr (WIN) mine = mine && group_pages(k) == C::GP && (t0 > pos - p.window || t0 + 64 <= p.sinks);
+      const bool whole = __all_sync(0xffffffffu, mine || !valid);
       const float base = ab * static_cast<float>(t0 - pos);  // ALiBi bias of token t0
       // raw: the scores stay unscaled (scale > 0 keeps their order) and the scale is folded
       // into the exponent below; otherwise x holds the biased / masked log2 logits
@@ -476,10 +527,12 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
           for (int i = 0; i < 64; ++i) x[i] = fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base));
         }
       } else {
-        const int lim = pos - t0;  // tokens i <= lim are visible
+        const int lim = WIN ? min(pos - t0, group_pages(k) * kBlock - 1) : pos - t0;  // tokens i <= lim are visible
+        const int lo = WIN ? pos - p.window - t0 : -1, hi = WIN ? p.sinks - t0 : 0;  // and, of those, i > lo and i < hi
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          x[i] = i <= lim ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base)) : -INFINITY;
+          x[i] = i <= lim && (!WIN || i > lo || i < hi) ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base))
+                                                        : -INFINITY;
       }
       // row max of the group: a tree of three-input max instructions
       float lm;
@@ -549,13 +602,27 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
         l += (a.x + a.y) + (c.x + c.y);
       }
       umma::wait_st();
+      if constexpr (WIN) {
+        if (tile == 0 && (k == wg.gap0 || k == wg.gap1)) {  // tokens of the group that no query sees
+          const int end = t0 + group_pages(k) * kBlock;
+          const int first = max(win.sinks, t0), n = min(win.start, end) - first;
+          for (int c = tid; c < n * 8 * C::NBOX; c += 128) {
+            const int bx = c / (n * 8), i = first - t0 + (c / 8) % n, ch = c % 8;
+            const int slot = (k % C::NS) * C::GP + i / kBlock;
+            *reinterpret_cast<uint4 *>(sgen + C::VOFF + bx * C::RING + slot * C::BOXB + (i % kBlock) * 128 + ch * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(vgap(k == wg.gap0 ? 0 : 1));
+        }
+      }
       if (k == ngr - 1 && tile == 0) {
         // V rows of tokens >= len in the last page may hold anything (NaN included) and
         // P . V would carry it into O even with P = 0 there: tile 0 zeroes them before it
         // hands over its P (the P . V of every tile is issued after that)
         const int lastp = npages - 1, nv = min(kBlock, len - lastp * kBlock);
         if (nv < kBlock) {
-          const int slot = (k % C::NS) * C::GP + (lastp - k * C::GP);
+          const int slot = (k % C::NS) * C::GP + (lastp - group_base(k));
           const int chunks = (kBlock - nv) * 8 * C::NBOX;  // 16-byte chunks
           for (int c = tid; c < chunks; c += 128) {
             const int bx = c / ((kBlock - nv) * 8), rr = (c / 8) % (kBlock - nv) + nv, ch = c % 8;
@@ -648,12 +715,12 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
   }
 }
 
-template <int KIND, int D, int T>
+template <int KIND, int D, int T, bool WIN>
 struct UmmaLaunch {
   using C = UmmaCfg<KIND, D, T>;
   static cudaError_t launch(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                             const CUtensorMap &tmQ, cudaStream_t st) {
-    auto kern = chunk_umma_kernel<KIND, D, T>;
+    auto kern = chunk_umma_kernel<KIND, D, T, WIN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
@@ -664,5 +731,22 @@ struct UmmaLaunch {
     return e != cudaSuccess ? e : cudaGetLastError();
   }
 };
+
+template <bool WIN>
+cudaError_t launch_chunk(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                         const CUtensorMap &tmQ, cudaStream_t st) {
+  // head size 128 with more than one tile of query rows per KV head: two 128-row tiles per
+  // CTA share each page (measured faster there; at head size 64 one tile per CTA is faster)
+  const bool two = p.D == 128 && p.nq_max * p.G > kChunkTwoTileColumns;
+  if (kind == KIND_BF16 && p.D == 64) return UmmaLaunch<KIND_BF16, 64, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
+  if (kind == KIND_BF16 && p.D == 128)
+    return two ? UmmaLaunch<KIND_BF16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)
+               : UmmaLaunch<KIND_BF16, 128, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
+  if (kind == KIND_F16 && p.D == 64) return UmmaLaunch<KIND_F16, 64, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
+  if (kind == KIND_F16 && p.D == 128)
+    return two ? UmmaLaunch<KIND_F16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)
+               : UmmaLaunch<KIND_F16, 128, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
+  return cudaErrorInvalidValue;
+}
 
 }  // namespace pa

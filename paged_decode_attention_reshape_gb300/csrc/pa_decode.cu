@@ -13,8 +13,8 @@ namespace pa {
 // (coalesced 128-byte loads), one butterfly reduction per (token, head) gives
 // the score, and the per-head online-softmax state is kept in registers.
 
-// ACC: scores and softmax sums kept for pa_decode_accumulate.
-template <int D, int W, bool ACC>
+// ACC: scores and softmax sums kept for pa_decode_accumulate.  WIN: under a window (Window).
+template <int D, int W, bool ACC, bool WIN>
 __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p) {
   constexpr int PER = D / 32;
   __shared__ float sm[W][8][D + 2];
@@ -45,7 +45,9 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
   if (ng <= 0) return;
   const Cols cm{row0, p.G, g, v0};
   const int pos0 = len - nq;  // column hh sees the tokens up to pos0 + (v0 + hh) / G
-  const int npages = (pos0 + (v0 + ng - 1) / p.G + 1 + kBlock - 1) / kBlock;
+  const int vis = pos0 + (v0 + ng - 1) / p.G + 1;
+  const Window win = WIN && vis > 0 ? make_window(p.window, p.sinks, pos0 + v0 / p.G) : Window{};
+  const int npages = (vis + kBlock - 1) / kBlock - win.skip;
   const bool clustered = p.cluster > 1;  // rank `part` of a cluster splitting the unit equally
   const int pb = clustered ? static_cast<int>(static_cast<int64_t>(part) * npages / p.cluster) : part * p.pages_per_part;
   const int pe = clustered ? static_cast<int>(static_cast<int64_t>(part + 1) * npages / p.cluster)
@@ -74,7 +76,8 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
   }
   bool bad = false;
   const int32_t *bt = p.block_table + static_cast<int64_t>(s) * p.bt_ss;
-  for (int page = pb + warp; page < pe; page += W) {
+  for (int v = pb + warp; v < pe; v += W) {
+    const int page = WIN ? win.page(v) : v;
     const int pid = __ldg(bt + page);
     if (pid < 0 || pid >= p.num_blocks) {
       bad = true;
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
       const int tt = page * kBlock + t;  // the token's position
 #pragma unroll
       for (int hh = 0; hh < 8; ++hh) {
-        if (tt <= pos[hh]) {  // visible to this column (never for hh >= ng)
+        if (tt <= pos[hh] && (!WIN || tt > pos[hh] - p.window || tt < p.sinks)) {  // visible to this column (never for hh >= ng)
           float z = 0.f;
 #pragma unroll
           for (int i = 0; i < PER; ++i) z = fmaf(q[hh][i], kr[i], z);
@@ -184,14 +187,14 @@ __global__ void __launch_bounds__(W * 32) decode_f32_kernel(const DecodeParams p
 }
 
 namespace {
-template <bool ACC>
+template <bool ACC, bool WIN>
 cudaError_t launch_f32(const DecodeParams &p, cudaStream_t st) {
   const dim3 grid(p.max_parts, p.Hkv * p.HG, p.S);
   cudaError_t e;
   switch (p.D) {
-    case 64: e = launch_pdl(decode_f32_kernel<64, 4, ACC>, grid, dim3(128), 0, st, p.cluster, p); break;
-    case 128: e = launch_pdl(decode_f32_kernel<128, 4, ACC>, grid, dim3(128), 0, st, p.cluster, p); break;
-    case 256: e = launch_pdl(decode_f32_kernel<256, 2, ACC>, grid, dim3(64), 0, st, p.cluster, p); break;
+    case 64: e = launch_pdl(decode_f32_kernel<64, 4, ACC, WIN>, grid, dim3(128), 0, st, p.cluster, p); break;
+    case 128: e = launch_pdl(decode_f32_kernel<128, 4, ACC, WIN>, grid, dim3(128), 0, st, p.cluster, p); break;
+    case 256: e = launch_pdl(decode_f32_kernel<256, 2, ACC, WIN>, grid, dim3(64), 0, st, p.cluster, p); break;
     default: return cudaErrorInvalidValue;
   }
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -199,7 +202,8 @@ cudaError_t launch_f32(const DecodeParams &p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st) {
-  return p.scores ? launch_f32<true>(p, st) : launch_f32<false>(p, st);
+  if (p.window > 0) return launch_f32<false, true>(p, st);
+  return p.scores ? launch_f32<true, false>(p, st) : launch_f32<false, false>(p, st);
 }
 
 // ------------------------------------------------- accumulated attention weights

@@ -28,7 +28,8 @@
 //      cancel the error is all there is.
 //
 // Tokens behind the end exist only in a range's last stage, which takes a branch of its own:
-// scores -inf, p = 0 and V scales 0 (codes are always finite), so nothing stale is summed.
+// scores -inf, p = 0 and V scales 0 (codes are always finite), so nothing stale is summed.  Under a
+// window (WIN) the stages that hold its start or the first tokens' end take that branch too.
 #pragma once
 
 namespace pa {
@@ -83,6 +84,26 @@ __device__ __forceinline__ float *fp4_score_lane(const DecodeParams &p, int s, i
          2 * (lane & 3);
 }
 
+// Under a window: a stage's pages, their first tokens and the tokens of each that some column sees.
+template <int NP, bool WIN>
+struct Fp4Pages {
+  int tok[NP];
+  uint32_t seen[NP];
+  bool all;
+  // pages v .. of `win`, those from pe on another range's or nobody's
+  __device__ __forceinline__ Fp4Pages(const Window &win, int v, int pe, int len) : all(true) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int page = win.page(v + j);
+      tok[j] = page * kBlock;
+      seen[j] = v + j < pe ? win.seen(page, len) : 0u;
+      all &= seen[j] == 0xffffu;
+    }
+  }
+};
+template <int NP>
+struct Fp4Pages<NP, false> {};
+
 // One warp's attention over the stages of a range: query fragments, softmax state, accumulator, and
 // the places its lane reads in a stage.
 template <typename C, int D, bool PLAIN>
@@ -134,8 +155,15 @@ struct Fp4State {
   // One stage at offset sto: tokens from tok0 on, `left` of them the range's.  TAIL when the range
   // ends inside it (its last stage at most): compiled apart, so that the others carry no trace of
   // the end.  ACC: scores to score_lane, this lane's place in the unit's first page of scores.
-  template <bool TAIL, bool ACC>
-  __device__ __forceinline__ void stage(const DecodeParams &p, uint32_t sto, int tok0, int left, float *score_lane) {
+  // WIN: the stage's pages are `pages`, TAIL when some token of theirs is hidden from every column.
+  template <bool TAIL, bool ACC, bool WIN = false>
+  __device__ __forceinline__ void stage(const DecodeParams &p, uint32_t sto, int tok0, int left, float *score_lane,
+                                        const Fp4Pages<NP, WIN> &pages = Fp4Pages<NP, WIN>{}) {
+    // WIN: whether token t of page j is hidden from every column
+    auto hidden = [&](int j, int t) {
+      if constexpr (WIN) return ((pages.seen[j] >> t) & 1u) == 0u;
+      else return false;
+    };
     // ---- scores: fragment rows ra, ra + 8 = tokens, columns 2qc, 2qc + 1
     float x[NP][4];
 #pragma unroll
@@ -171,18 +199,29 @@ struct Fp4State {
       if constexpr (TAIL) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          if (j * kBlock + ra >= left) x[j][0] = x[j][1] = -INFINITY;
-          if (j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = -INFINITY;
+          if (WIN ? hidden(j, ra) : j * kBlock + ra >= left) x[j][0] = x[j][1] = -INFINITY;
+          if (WIN ? hidden(j, ra + 8) : j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = -INFINITY;
         }
       }
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const int ta = tok0 + j * kBlock + ra, tb = ta + 8;
+        int ta = tok0 + j * kBlock + ra, tb = ta + 8;
+        if constexpr (WIN) {
+          ta = pages.tok[j] + ra;
+          tb = ta + 8;
+        }
         x[j][0] = ta <= seeA ? fmaf(ab0, static_cast<float>(ta - posA), x[j][0] * sc0) : -INFINITY;
         x[j][1] = ta <= seeB ? fmaf(ab1, static_cast<float>(ta - posB), x[j][1] * sc1) : -INFINITY;
         x[j][2] = tb <= seeA ? fmaf(ab0, static_cast<float>(tb - posA), x[j][2] * sc0) : -INFINITY;
         x[j][3] = tb <= seeB ? fmaf(ab1, static_cast<float>(tb - posB), x[j][3] * sc1) : -INFINITY;
+        if constexpr (WIN) {
+          auto outside = [&](int t, int pos) { return t <= pos - p.window && t >= p.sinks; };
+          if (outside(ta, posA) || (TAIL && hidden(j, ra))) x[j][0] = -INFINITY;
+          if (outside(ta, posB) || (TAIL && hidden(j, ra))) x[j][1] = -INFINITY;
+          if (outside(tb, posA) || (TAIL && hidden(j, ra + 8))) x[j][2] = -INFINITY;
+          if (outside(tb, posB) || (TAIL && hidden(j, ra + 8))) x[j][3] = -INFINITY;
+        }
       }
     }
     if constexpr (ACC) {
@@ -245,8 +284,8 @@ struct Fp4State {
     if constexpr (PLAIN && TAIL) {  // (a zero scale times the -inf above is no number)
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        if (j * kBlock + ra >= left) x[j][0] = x[j][1] = 0.f;
-        if (j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = 0.f;
+        if (WIN ? hidden(j, ra) : j * kBlock + ra >= left) x[j][0] = x[j][1] = 0.f;
+        if (WIN ? hidden(j, ra + 8) : j * kBlock + ra + 8 >= left) x[j][2] = x[j][3] = 0.f;
       }
     }
 
@@ -270,10 +309,15 @@ struct Fp4State {
         Runs::codes(va + von8, b, w[2]);
         Runs::codes(va + von8 + vodd, b, w[3]);
         uint32_t z01 = Runs::scale_pair(vq, 0, b), z23 = Runs::scale_pair(vq, 1, b);
-        if constexpr (TAIL) {  // zero scales for the tokens behind the end
-          const int lv = left - j * kBlock - 2 * qc;  // of tokens 2qc, + 1, + 8, + 9
-          z01 &= (lv > 0 ? 0x00ffu : 0u) | (lv > 1 ? 0xff00u : 0u);
-          z23 &= (lv > 8 ? 0x00ffu : 0u) | (lv > 9 ? 0xff00u : 0u);
+        if constexpr (TAIL) {  // zero scales for the hidden tokens
+          if constexpr (WIN) {
+            z01 &= (hidden(j, 2 * qc) ? 0u : 0x00ffu) | (hidden(j, 2 * qc + 1) ? 0u : 0xff00u);
+            z23 &= (hidden(j, 2 * qc + 8) ? 0u : 0x00ffu) | (hidden(j, 2 * qc + 9) ? 0u : 0xff00u);
+          } else {
+            const int lv = left - j * kBlock - 2 * qc;  // of tokens 2qc, + 1, + 8, + 9
+            z01 &= (lv > 0 ? 0x00ffu : 0u) | (lv > 1 ? 0xff00u : 0u);
+            z23 &= (lv > 8 ? 0x00ffu : 0u) | (lv > 9 ? 0xff00u : 0u);
+          }
         }
         const uint32_t s01 = e4m3x2_to_f16x2(z01), s23 = e4m3x2_to_f16x2(z23);
 #pragma unroll
@@ -303,15 +347,23 @@ struct Fp4State {
     if (left >= NP * kBlock) stage<false, ACC>(p, sto, tok0, left, score_lane);
     else stage<true, ACC>(p, sto, tok0, left, score_lane);
   }
+  // The same under a window: the stage's pages from number v on, of a range that ends before number pe.
+  __device__ __forceinline__ void window_stage(const DecodeParams &p, uint32_t sto, const Window &win, int v, int pe,
+                                               int len) {
+    const Fp4Pages<NP, true> pages(win, v, pe, len);
+    if (pages.all) stage<false, false, true>(p, sto, 0, 0, nullptr, pages);
+    else stage<true, false, true>(p, sto, 0, 0, nullptr, pages);
+  }
 };
 
 // Runs pages [pb, pe) of sequence s; arguments and result as run_pages_tma (there is no wait here
 // that could give up).
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC, bool WIN>
 __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint32_t sbase, uint8_t *const sgen,
                                               int &used, const int s, const int len, const Cols &cm,
                                               const int pos0, const int ng, const int pb, const int pe, int entry,
-                                              const bool entry_ready, const uint64_t pol, const int wait_page) {
+                                              const bool entry_ready, const uint64_t pol, const int wait_page,
+                                              const Window &win) {
   using C = MmaCfg<KIND, D, W, STAGES>;
   constexpr int NP = C::NP;
   constexpr int PER = 32 / NP;  // stages whose table entries the warp's lanes hold at a time
@@ -345,7 +397,8 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
     if (at == 0) {
       if (k > 0 || !entry_ready) {
         const int i = C::entry(warp, lane) + k * NP * W;
-        entry = i < n ? __ldg(bt + i) : 0;
+        if constexpr (WIN) entry = i < n ? __ldg(bt + (win.page(pb + i) - pb)) : 0;
+        else entry = i < n ? __ldg(bt + i) : 0;
       }
       check_entries(k);
     }
@@ -360,7 +413,7 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
     else copy_commit();
   }
 
-  const int end = min(len, pe * kBlock);
+  const int end = WIN ? len : min(len, pe * kBlock);
   Fp4State<C, D, PLAIN> state;
   state.place(stage0);
   state.begin(p, cm, ng, pos0, end);
@@ -370,8 +423,12 @@ __device__ __forceinline__ bool run_pages_fp4(const DecodeParams &p, const uint3
   for (int k = 0; k < nmine; ++k) {
     copy_wait<STAGES - 1>();  // this lane's copies of the stage, then the whole warp's
     __syncwarp();
-    const int tok0 = (pb + NP * (warp + k * W)) * kBlock;
-    state.template any_stage<ACC>(p, (u0 + k) % STAGES * C::STAGEB, tok0, end - tok0, score_lane);
+    if constexpr (WIN) {
+      state.window_stage(p, (u0 + k) % STAGES * C::STAGEB, win, pb + NP * (warp + k * W), pe, len);
+    } else {
+      const int tok0 = (pb + NP * (warp + k * W)) * kBlock;
+      state.template any_stage<ACC>(p, (u0 + k) % STAGES * C::STAGEB, tok0, end - tok0, score_lane);
+    }
     __syncwarp();  // every lane has read the stage
     if (k + STAGES < nmine) issue(k + STAGES);
     else copy_commit();

@@ -55,11 +55,16 @@
 //
 // The kernel is launched as a programmatic dependent of the previous grid on the
 // stream: it waits for that grid before its first global read, so its launch
-// overlaps the previous kernel's tail.  Five variants per shape: the general one
+// overlaps the previous kernel's tail.  Seven variants per shape: the general one
 // (several query tokens, ALiBi), PLAIN (one query token, no ALiBi: one compare per score
 // for the page tail), and PLAIN + EARLY for pa_decode_step's multi-row steps, which reads
-// everything but the pages with new positions before that wait; and the first two storing
-// their scores (pa_decode_accumulate).
+// everything but the pages with new positions before that wait; the first two storing
+// their scores (pa_decode_accumulate); and the first two under a window (WIN, pa_decode_window).
+//
+// Under a window a work item's pages are numbered without the gap between the first tokens' pages and
+// the window's (Window in pa_internal.h): splits, warps and stages count those numbers, and only the
+// table index and the tokens' positions are looked up through them.  Only pages at the window's
+// start, the first tokens' end and the sequence's end hold tokens to hide; the others take one test.
 #pragma once
 
 #include "pa_device.cuh"
@@ -246,17 +251,23 @@ __device__ __forceinline__ void store_warp_state(uint8_t *sgen, float m0, float 
 // caller).  Returns true after a bad block id or a timed-out wait; `stalled` is set
 // on a timeout, after which the CTA must not issue into its stages again.
 // ACC: every score goes to p.scores too (log2 units; -inf where a column does not see the token).
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+// WIN: pb and pe are numbers of `win`.
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC, bool WIN>
 __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
                                           const uint32_t sbase, uint8_t *const sgen, int &used, bool &stalled,
                                           const int s, const int len, const Cols &cm, const int pos0,
                                           const int ng, const int pb, const int pe, int pid_reg,
-                                          const bool pid_ready, const uint64_t pol, const int wait_page) {
+                                          const bool pid_ready, const uint64_t pol, const int wait_page,
+                                          const Window &win) {
   using C = MmaCfg<KIND, D, W, STAGES>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = cm.g;
   const int32_t *bt = p.block_table + static_cast<int64_t>(s) * p.bt_ss;
   const int nmine = (pe - pb > warp) ? (pe - pb - warp + W - 1) / W : 0;
+  auto page_of = [&](int v) {
+    if constexpr (WIN) return win.page(v);
+    else return v;
+  };
   const uint32_t stage0 = sbase + static_cast<uint32_t>(warp * STAGES * C::STAGEB);
   const uint32_t bar0 = sbase + static_cast<uint32_t>(W * STAGES * C::STAGEB + warp * STAGES * 8);
   const int u0 = used;
@@ -272,7 +283,8 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
     }
     if ((kk & 31) == 0 && (kk > 0 || !pid_ready)) {
       const int k2 = kk + lane;
-      pid_reg = (k2 < nmine) ? __ldg(bt + pb + warp + k2 * W) : 0;
+      if constexpr (WIN) pid_reg = (k2 < nmine) ? __ldg(bt + win.page(pb + warp + k2 * W)) : 0;
+      else pid_reg = (k2 < nmine) ? __ldg(bt + pb + warp + k2 * W) : 0;
     }
     int pid = __shfl_sync(0xffffffffu, pid_reg, kk & 31);
     if (pid < 0 || pid >= p.num_blocks) {
@@ -347,8 +359,10 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
     }
     const uint32_t kb = stage0 + st * C::STAGEB;
     const uint32_t vb = kb + C::PAGEB;
-    const int page = pb + warp + k * W;
+    const int page = page_of(pb + warp + k * W);
     const int nv = min(kBlock, len - page * kBlock);  // valid tokens in this page
+    uint32_t seen = 0u;  // WIN: its tokens that some column sees
+    if constexpr (WIN) seen = win.seen(page, len);
 
     // ---- scores: two accumulation chains over the k-steps
     float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -390,7 +404,8 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
     // ---- online softmax (fragment: rows ra, ra+8 = tokens; columns 2qc, 2qc+1 = heads)
     float s0, s1, s2, s3;
     if constexpr (PLAIN) {  // one query token, no ALiBi: every column sees the tokens < len
-      const bool va = ra < nv, vb8 = ra + 8 < nv;
+      bool va = ra < nv, vb8 = ra + 8 < nv;
+      if constexpr (WIN) va = (seen >> ra) & 1u, vb8 = (seen >> (ra + 8)) & 1u;
       s0 = va ? (c0[0] + c1[0]) * sc0 : -INFINITY;
       s1 = va ? (c0[1] + c1[1]) * sc1 : -INFINITY;
       s2 = vb8 ? (c0[2] + c1[2]) * sc0 : -INFINITY;
@@ -401,6 +416,13 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
       s1 = ta <= posB ? fmaf(ab1, static_cast<float>(ta - posB), (c0[1] + c1[1]) * sc1) : -INFINITY;
       s2 = tb <= posA ? fmaf(ab0, static_cast<float>(tb - posA), (c0[2] + c1[2]) * sc0) : -INFINITY;
       s3 = tb <= posB ? fmaf(ab1, static_cast<float>(tb - posB), (c0[3] + c1[3]) * sc1) : -INFINITY;
+      if constexpr (WIN) {
+        auto outside = [&](int t, int pos) { return t <= pos - p.window && t >= p.sinks; };
+        if (outside(ta, posA)) s0 = -INFINITY;
+        if (outside(ta, posB)) s1 = -INFINITY;
+        if (outside(tb, posA)) s2 = -INFINITY;
+        if (outside(tb, posB)) s3 = -INFINITY;
+      }
     }
     if constexpr (ACC) {
       if (2 * qc < p.score_cols) {
@@ -462,10 +484,15 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
       bl1 = movmatrix_trans(pack_f16(p2 - fb.x, p3 - fb.y));
     }
 
-    // ---- O^T += V^T . P^T (tail rows of the last page zeroed first)
+    // ---- O^T += V^T . P^T (rows that no column sees, behind the end or outside the window, zeroed first)
     if constexpr (!C::FP8) {
-      const uint32_t mA = (2 * qc < nv ? 0x0000FFFFu : 0u) | (2 * qc + 1 < nv ? 0xFFFF0000u : 0u);
-      const uint32_t mB = (2 * qc + 8 < nv ? 0x0000FFFFu : 0u) | (2 * qc + 9 < nv ? 0xFFFF0000u : 0u);
+      uint32_t mA = (2 * qc < nv ? 0x0000FFFFu : 0u) | (2 * qc + 1 < nv ? 0xFFFF0000u : 0u);
+      uint32_t mB = (2 * qc + 8 < nv ? 0x0000FFFFu : 0u) | (2 * qc + 9 < nv ? 0xFFFF0000u : 0u);
+      if constexpr (WIN) {
+        const uint32_t s4 = seen >> (2 * qc);
+        mA = (s4 & 1u ? 0x0000FFFFu : 0u) | (s4 & 2u ? 0xFFFF0000u : 0u);
+        mB = (s4 & 0x100u ? 0x0000FFFFu : 0u) | (s4 & 0x200u ? 0xFFFF0000u : 0u);
+      }
       const int vtok = (lane & 7) | ((lane >> 4) << 3);
       const int vhalf = (lane >> 3) & 1;
 #pragma unroll
@@ -473,7 +500,7 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
         const int cidx = 2 * t + vhalf;  // 16-byte chunk of the row
         uint32_t a[4];
         ldmatrix_x4_trans(a, vb + (cidx >> 3) * 2048 + vtok * 128 + (((cidx & 7) ^ (vtok & 7)) << 4));
-        if (nv < kBlock) {
+        if (WIN ? seen != 0xffffu : nv < kBlock) {
           a[0] &= mA;
           a[1] &= mA;
           a[2] &= mB;
@@ -496,12 +523,12 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
         uint4 w1 = lds128(pgb + t1 * 128 + ((ra ^ (t1 & 7)) << 4));
         uint4 w2 = lds128(pgb + t2 * 128 + ((ra ^ (t2 & 7)) << 4));
         uint4 w3 = lds128(pgb + t3 * 128 + ((ra ^ (t3 & 7)) << 4));
-        if (nv < kBlock) {
+        if (WIN ? seen != 0xffffu : nv < kBlock) {
           const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-          if (t0 >= nv) w0 = z;
-          if (t1 >= nv) w1 = z;
-          if (t2 >= nv) w2 = z;
-          if (t3 >= nv) w3 = z;
+          if (WIN ? !((seen >> t0) & 1u) : t0 >= nv) w0 = z;
+          if (WIN ? !((seen >> t1) & 1u) : t1 >= nv) w1 = z;
+          if (WIN ? !((seen >> t2) & 1u) : t2 >= nv) w2 = z;
+          if (WIN ? !((seen >> t3) & 1u) : t3 >= nv) w3 = z;
         }
         const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
         const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
@@ -538,18 +565,19 @@ __device__ __forceinline__ bool run_pages_tma(const DecodeParams &p, const CUten
 
 namespace pa {
 
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC, bool WIN>
 __device__ __forceinline__ bool run_pages(const DecodeParams &p, const CUtensorMap *tmK, const CUtensorMap *tmV,
                                           const uint32_t sbase, uint8_t *const sgen, int &used, bool &stalled,
                                           const int s, const int len, const Cols &cm, const int pos0, const int ng,
                                           const int pb, const int pe, const int pid_reg, const bool pid_ready,
-                                          const uint64_t pol, const int wait_page) {
+                                          const uint64_t pol, const int wait_page, const Window &win) {
   if constexpr (MmaCfg<KIND, D, W, STAGES>::FP4)
-    return run_pages_fp4<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, sbase, sgen, used, s, len, cm, pos0, ng, pb,
-                                                               pe, pid_reg, pid_ready, pol, wait_page);
+    return run_pages_fp4<KIND, D, W, STAGES, PLAIN, EARLY, ACC, WIN>(p, sbase, sgen, used, s, len, cm, pos0, ng, pb,
+                                                                     pe, pid_reg, pid_ready, pol, wait_page, win);
   else
-    return run_pages_tma<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, tmK, tmV, sbase, sgen, used, stalled, s, len, cm,
-                                                               pos0, ng, pb, pe, pid_reg, pid_ready, pol, wait_page);
+    return run_pages_tma<KIND, D, W, STAGES, PLAIN, EARLY, ACC, WIN>(p, tmK, tmV, sbase, sgen, used, stalled, s, len,
+                                                                     cm, pos0, ng, pb, pe, pid_reg, pid_ready, pol,
+                                                                     wait_page, win);
 }
 
 // Merges the W warp states of the CTA (max / log-sum-exp rescaling) and, for every
@@ -642,8 +670,8 @@ __device__ __forceinline__ void zero_rows(const DecodeParams &p, const Cols &cm,
 // per-column causal limits and the bias.  EARLY (with PLAIN only): the early reads of
 // pa_decode_step (DecodeParams::early); a wait inside the page loop costs the other
 // variants about 1.4 us on a 30 us decode, so only this one carries it.
-// ACC: scores stored for pa_decode_accumulate.
-template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC>
+// ACC: scores stored for pa_decode_accumulate.  WIN: under a window.
+template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC, bool WIN>
 __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
@@ -677,7 +705,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     if (lane == 1 && p.qsl) prefetch_l2(p.qsl + (flat ? 0 : blockIdx.z));
     if (flat) {  // CTA c: the table rows (first head row only) and query heads of sequences c, c + CTAs, ...
       for (int z = part; z < p.S; z += p.flat) {
-        if (blockIdx.y == 0) {
+        if (!WIN && blockIdx.y == 0) {  // (under a window it takes the length to know the entries)
           const int32_t *row = p.block_table + static_cast<int64_t>(z) * p.bt_ss;
           for (int pg = lane * 32; pg < p.max_blocks; pg += 32 * 32) prefetch_l2(row + pg);
         }
@@ -690,7 +718,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
       // only) and its query heads (the first partition only); together the rows cover
       // every sequence, whichever row ends up working on it.
       const int z = blockIdx.z;
-      if (blockIdx.y == 0) {
+      if (!WIN && blockIdx.y == 0) {
         const int pg0 = p.cluster > 1 ? part * p.max_blocks / p.cluster : part * p.pages_per_part;
         const int pg1 = p.cluster > 1 ? (part + 1) * p.max_blocks / p.cluster : min(p.max_blocks, pg0 + p.pages_per_part);
         const int32_t *row = p.block_table + static_cast<int64_t>(z) * p.bt_ss;
@@ -736,6 +764,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
         const bool ok = L >= 0 && L <= p.max_blocks * kBlock;
         if (!ok && part == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, kErrSeqLen);
         n[j] = ok ? (L + kBlock - 1) / kBlock : 0;
+        if (WIN && ok && L > 0) n[j] -= make_window(p.window, p.sinks, L - 1).skip;
         sum += n[j];
       }
       int incl = sum;
@@ -790,8 +819,9 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
       const int zlen = __ldg(p.seq_lens + z);
       bool bad = true;
       if (!dead)
-        bad = run_pages<KIND, D, W, STAGES, PLAIN, false, ACC>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
-                                            x - ps, y - ps, 0, false, pol, kNoWaitPage);
+        bad = run_pages<KIND, D, W, STAGES, PLAIN, false, ACC, WIN>(p, &tmK, &tmV, sbase, sgen, used, stalled, z, zlen, cm, zlen - 1, ng,
+                                            x - ps, y - ps, 0, false, pol, kNoWaitPage,
+                                            WIN ? make_window(p.window, p.sinks, zlen - 1) : Window{});
       const bool any_bad = __syncthreads_or(bad);
       if (any_bad) dead = __syncthreads_or(stalled) || dead;
       if (x == ps && y == pn) {
@@ -829,7 +859,7 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   const bool split = p.max_parts > 1;
   int pid_reg = 0;  // lane i: physical block of my page i; with fixed-size partitions it is
                     // read speculatively (bounded by the table width) alongside seq_len
-  if (!clustered) {
+  if (!clustered && !WIN) {
     const int pg = part * p.pages_per_part + C::entry(warp, lane);
     if (pg < p.max_blocks) pid_reg = __ldg(bt + pg);
   }
@@ -855,16 +885,22 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
   const Cols cm{row0, p.G, g, v0};
   const int pos0 = len - nq;
   const int vis = pos0 + (v0 + ng - 1) / p.G + 1;  // tokens the CTA's last column sees
-  const int npages = (vis + kBlock - 1) / kBlock;
+  // (the window of the CTA's first column; a sequence without queries has left, one without tokens has no page)
+  const Window win = WIN && vis > 0 ? make_window(p.window, p.sinks, pos0 + v0 / p.G) : Window{};
+  const int npages = (vis + kBlock - 1) / kBlock - win.skip;
   int pb, pe;
   if (clustered) {
     pb = static_cast<int>(static_cast<int64_t>(part) * npages / p.cluster);
     pe = static_cast<int>(static_cast<int64_t>(part + 1) * npages / p.cluster);
     const int pg = pb + C::entry(warp, lane);
-    if (pg < pe) pid_reg = __ldg(bt + pg);
+    if (!WIN && pg < pe) pid_reg = __ldg(bt + pg);
   } else {
     pb = part * p.pages_per_part;
     pe = min(npages, pb + p.pages_per_part);
+  }
+  if constexpr (WIN) {
+    const int pg = pb + C::entry(warp, lane);
+    if (pg < pe) pid_reg = __ldg(bt + win.page(pg));
   }
   if (pb >= pe && !clustered) {  // (an empty cluster rank stays: it takes part in the merge)
     if (npages == 0 && part == 0) {  // empty sequence (any split)
@@ -880,8 +916,8 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
     wait_page = nnew <= 0 ? kNoWaitPage : max(0, len - nnew) / kBlock;
   }
 
-  const bool bad = run_pages<KIND, D, W, STAGES, PLAIN, EARLY, ACC>(p, &tmK, &tmV, sbase, sgen, used, stalled, s, len, cm, pos0, ng,
-                                                 pb, pe, pid_reg, true, pol, wait_page);
+  const bool bad = run_pages<KIND, D, W, STAGES, PLAIN, EARLY, ACC, WIN>(p, &tmK, &tmV, sbase, sgen, used, stalled, s, len, cm, pos0, ng,
+                                                 pb, pe, pid_reg, true, pol, wait_page, win);
   if (early) grid_dependency_wait();  // before any output or workspace write
   const bool any_bad = __syncthreads_or(bad);
 
@@ -936,24 +972,24 @@ struct MmaLaunch {
   using C = MmaCfg<KIND, D, W, ST>;
   static_assert(C::SMEM == mma_smem(KIND, D), "shape table out of sync");
 
-  template <bool PLAIN, bool EARLY, bool ACC>
+  template <bool PLAIN, bool EARLY, bool ACC, bool WIN>
   static cudaError_t attrs() {
     static std::atomic<uint64_t> done{0};
     return once_per_device(done, [] {
-      auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>;
+      auto kern = decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC, WIN>;
       cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
       if (e != cudaSuccess) return e;
       // same shared/L1 split as the cache write that usually precedes it (no reconfiguration)
       return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     });
   }
-  template <bool PLAIN, bool EARLY, bool ACC>
+  template <bool PLAIN, bool EARLY, bool ACC, bool WIN = false>
   static cudaError_t launch_variant(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                     cudaStream_t st) {
-    cudaError_t e = attrs<PLAIN, EARLY, ACC>();
+    cudaError_t e = attrs<PLAIN, EARLY, ACC, WIN>();
     if (e != cudaSuccess) return e;
     const dim3 grid = p.flat > 0 ? dim3(p.flat, p.Hkv * p.HG, 1) : dim3(p.max_parts, p.Hkv * p.HG, p.S);
-    e = launch_pdl(decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC>, grid, dim3(C::THREADS), C::SMEM, st, p.cluster,
+    e = launch_pdl(decode_mma_kernel<KIND, D, W, ST, PLAIN, EARLY, ACC, WIN>, grid, dim3(C::THREADS), C::SMEM, st, p.cluster,
                    p, tmK, tmV);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
@@ -964,10 +1000,14 @@ struct MmaLaunch {
     if (!plain) return launch_variant<false, false, false>(p, tmK, tmV, st);  // (ignores p.early: it waits first)
     return p.early ? launch_variant<true, true, false>(p, tmK, tmV, st) : launch_variant<true, false, false>(p, tmK, tmV, st);
   }
+  static cudaError_t launch_window(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    return !p.qsl && !p.alibi ? launch_variant<true, false, false, true>(p, tmK, tmV, st)
+                              : launch_variant<false, false, false, true>(p, tmK, tmV, st);
+  }
   static int occupancy() {  // 0 when it cannot be queried
     int n = 0;
-    if (attrs<false, false, false>() != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<KIND, D, W, ST, false, false, false>, C::THREADS,
+    if (attrs<false, false, false, false>() != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma_kernel<KIND, D, W, ST, false, false, false, false>, C::THREADS,
                                                       C::SMEM) !=
             cudaSuccess)
       return 0;

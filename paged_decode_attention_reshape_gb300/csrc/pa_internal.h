@@ -156,7 +156,38 @@ struct DecodeParams {
   float *scores, *lse;
   int score_cols;
   int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
+  // pa_decode_window / pa_attention_window (0: everything is seen): a query at position P sees the
+  // tokens t <= P with t > P - window or t < sinks.  Both at most max_blocks * 16.
+  int window, sinks;
 };
+
+// The pages that a work item under a window reads, numbered without the gap between the first tokens'
+// pages and the window's: every split cuts these numbers.  `start` is the first token inside the window of
+// the item's first query (of all its queries the earliest); tokens of [sinks, start) are seen by none.
+struct Window {
+  int ns;          // pages of the first tokens, as far as they are not the window's
+  int skip;        // pages in the gap
+  int start, sinks;
+  __host__ __device__ __forceinline__ int page(int v) const { return v < ns ? v : v + skip; }
+  // Bit t: token t of this page is below `len` and seen by some query.
+  __host__ __device__ __forceinline__ uint32_t seen(int page, int len) const {
+    const int base = page * kBlock;
+    const uint32_t gap = below(start - base) & ~below(sinks - base);
+    return below(len - base) & ~gap;
+  }
+  __host__ __device__ static __forceinline__ uint32_t below(int n) {  // bits 0 .. n - 1 of 16
+    return n >= kBlock ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1;
+  }
+};
+__host__ __device__ __forceinline__ Window make_window(int window, int sinks, int first_pos) {
+  Window w;
+  w.start = first_pos + 1 > window ? first_pos + 1 - window : 0;
+  w.sinks = sinks;
+  const int first = w.start / kBlock, pages = (sinks + kBlock - 1) / kBlock;
+  w.ns = pages < first ? pages : first;
+  w.skip = first - w.ns;
+  return w;
+}
 
 // The second kernel of pa_decode_accumulate.
 struct WeightsParams {
@@ -251,6 +282,12 @@ cudaError_t launch_decode_mma_16(const DecodeParams &p, int kind, const CUtensor
 cudaError_t launch_decode_mma_fp8(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   cudaStream_t st);  // KIND_FP8_*
 cudaError_t launch_decode_mma_fp4(const DecodeParams &p, int kind, cudaStream_t st);  // KIND_FP4_*
+// The same kernels under a window (p.window > 0).
+cudaError_t launch_decode_window_16(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                    cudaStream_t st);
+cudaError_t launch_decode_window_fp8(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                     cudaStream_t st);
+cudaError_t launch_decode_window_fp4(const DecodeParams &p, int kind, cudaStream_t st);
 cudaError_t launch_weights(const WeightsParams &p, int cols, cudaStream_t st);
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st);
 // Query-tile kernel for chunks of query tokens (pa_attention_varlen) on tcgen05 tensor
@@ -258,6 +295,8 @@ cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t st);
 // tmQ is read when p.q_tma is set (make_q_map).
 cudaError_t launch_chunk_umma(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                               const CUtensorMap &tmQ, cudaStream_t st);
+cudaError_t launch_chunk_window(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                const CUtensorMap &tmQ, cudaStream_t st);
 // Query columns per KV head (max_query_len x G) from which varlen attention uses it: below
 // that the column-group kernels are as fast or faster (256 sequences of 512-4096 tokens, 32/8
 // heads: at 32 columns 644 vs 737 us at head size 128, but 453 vs 325 us at head size 64).
