@@ -264,7 +264,7 @@ typedef struct {
  *   k_weight      x (mean(x^2) + eps)^(-1/2) weight, over the whole head, before the rotation.
  *   opt           NULL = defaults; scales and device_error are not used.
  * Sums and products in fp32, each element rounded to the rows' type once.  Alignment of rows as
- * pa_reshape_and_cache.  T == 0 is a no-op.  At most 2^35 rows.
+ * pa_reshape_and_cache.  T == 0 is a no-op; T < 2^31.
  */
 int pa_rotary(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa_tensor *key, const pa_tensor *positions,
               const pa_tensor *frequencies, const pa_tensor *q_weight, const pa_tensor *k_weight,

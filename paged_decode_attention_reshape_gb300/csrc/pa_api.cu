@@ -292,9 +292,33 @@ int window_blocks(int maxNB, int64_t window, int64_t sinks, int G, int nq) {
   const int64_t pages = (window + span - 1 + kBlock - 2) / kBlock + 1 + (sinks + kBlock - 1) / kBlock;
   return static_cast<int>(std::min<int64_t>(maxNB, pages));
 }
-// The plan of a call under a window, of maxNB pages by window_blocks.
-Plan make_window_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, int request, bool varlen) {
-  return make_plan(S, Hq, Hkv, D, maxNB, kind, sm, device, request, varlen, false);
+// The plan of a call under a window, of `pages` a unit by window_blocks (nearly what every longer sequence
+// reads, where a plan by the table's width has to guess).  Units that leave half of the resident CTA slots
+// empty are cut into 2, 4 or 8 parts a cluster, as long as the slots hold them all and a warp keeps two
+// pages; the cluster costs about 2 us, which fewer than eight pages a warp do not repay.  Units that
+// fill the slots once and a little more run as the balanced split where they are long.  Else whole units.
+// Measured on GB300, 8 KV heads of 128, bf16 (us; unsplit / 2 / 4 / 8 parts / fixed partitions of the best
+// size / balanced): 1 sequence, window 1024, 65 pages: 14.0 / 11.4 / 8.4 / 7.2 / 9.3 / 29.0; 1 x 128: 5.3 / 6.6 /
+// 5.6 / 5.8 / - / 10.5; 4 x 4112: 43.9 / 26.4 / 17.4 / 16.1 / 18.2 / 26.0; 8 x 1024: 14.4 / 12.5 / 11.3 / 19.2 / 12.8 /
+// 17.8; 16 x 256: 7.5 / 9.7 / 16.2 / 22.0 / 10.8 / 17.6; 32 x 1024: 24.3 / 36.3 / 36.3 / 51.6 / 31.2 / 29.8; 64 x 512,
+// 1.1 waves: 32.0 / 39.5 / - / - / 32.3 / 31.6; 64 x 2048: 96.3 / 95.0 / - / - / 89.1 / 87.3; 128 x 2048, E4M3, 1.7 waves:
+// 91.0 / 110 / - / - / 115 / 93.2.
+Plan make_window_plan(int S, int Hq, int Hkv, int D, int pages, int kind, int sm, bool device, int request, bool varlen) {
+  if (request != 0) return make_plan(S, Hq, Hkv, D, pages, kind, sm, device, request, varlen, false);
+  Plan pl{0, 0, 0, PA_OK, 0};
+  const int64_t units = static_cast<int64_t>(S) * Hkv * ((Hq / Hkv + 7) / 8);
+  const int64_t slots = static_cast<int64_t>(std::max(sm, 1)) * ctas_per_sm(kind, D, device);
+  const int warps = kind == KIND_F32 ? (D == 256 ? 2 : 4) : mma_warps(kind, D);
+  if (pages >= 8 * warps) {
+    for (const int C : {8, 4, 2}) {
+      if (units * C > slots || pages < 2 * C * warps) continue;
+      pl.cluster = C;
+      return pl;
+    }
+    if (units > slots && units * 3 < slots * 4 && pages >= 64 && !varlen && kind != KIND_F32)
+      return make_plan(S, Hq, Hkv, D, pages, kind, sm, device, S <= kFlatMaxSeqs ? PA_PARTITION_BALANCED : -1, varlen, false);
+  }
+  return pl;
 }
 
 // Split-KV workspace: [arrival counters, one int per (sequence, kv head, head group)]
@@ -746,9 +770,8 @@ int rotary_impl(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa
     if (slot_mapping->shape[0] != T || slot_mapping->stride[0] != 1) return PA_ERR_INVALID_ARG;
   }
   const int64_t Hq = q ? q->shape[1] : 0, Hk = key ? key->shape[1] : 0, Hv = value ? value->shape[1] : 0;
+  if (T > INT32_MAX) return PA_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || Hq + Hk + Hv == 0) return PA_OK;
-  if (T > INT64_MAX / (Hq + Hk + Hv) || T * (Hq + Hk + Hv) > static_cast<int64_t>(INT32_MAX) * 16)
-    return PA_ERR_UNSUPPORTED_SHAPE;  // the grid
   for (const pa_tensor *t : {q, static_cast<const pa_tensor *>(q_out), key, static_cast<const pa_tensor *>(k_out), value})
     if (t && (r = check_row_pointers(t))) return r;
   if (pairs > 0 && !positions->data) return PA_ERR_INVALID_ARG;
@@ -820,9 +843,16 @@ int rotary_impl(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!cached) return launch_rotary(p, dt, dt, sm, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const int cache_dtype = cached ? static_cast<int>(k_cache->dtype) : dt;
+  auto launch = [&] {
+    const cudaError_t e = dt == PA_F32    ? launch_rotary_f32(p, cache_dtype, sm, st)
+                          : dt == PA_BF16 ? launch_rotary_bf16(p, cache_dtype, sm, st)
+                                          : launch_rotary_f16(p, cache_dtype, sm, st);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  };
+  if (!cached) return launch();
   ProfScope ps(PA_KERNEL_WRITE, st);
-  return launch_rotary(p, dt, k_cache->dtype, sm, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch();
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // pa_fp4_quant.cuh -- a group of 16 elements to its E2M1 codes and E4M3 scale (the definition is in
-// pa_fp4.cu), shared by the 4-bit cache writes (pa_fp4.cu, pa_rotary.cu).
+// pa_fp4.cu), shared by the 4-bit cache writes (pa_fp4.cu, pa_rotary.cuh).
 #pragma once
 
 #include "pa_fp4.cuh"

@@ -77,7 +77,7 @@ struct GatherParams {
   bool i32;                        // T, block count and every stride below 2^31
 };
 
-// Rotation (and norm) of query and key rows (pa_rotary.cu); strides in bytes (s2, the token stride, 0
+// Rotation (and norm) of query and key rows (pa_rotary.cuh); strides in bytes (s2, the token stride, 0
 // for a 4-bit cache).
 struct RotaryParams {
   const char *q, *key, *value;
@@ -100,11 +100,11 @@ struct RotaryParams {
   float magnitude, eps;
   bool pos64, interleaved;
   bool wide;                       // every 32-byte piece of the rows (and of a cache of their type) is aligned
-  int rows_per_cta;                // set by the launch, as is the reciprocal of the rows per token
-  uint32_t magic;
+  // set by the launch: groups of rows that a warp takes at a time, queries', keys' and values'; rounds of a token
+  // per warp; what is left: `extra` tokens, each in `pieces` of `share` groups, or (pieces = 0) `share` groups
+  // for each warp and one more for the first `extra`
+  int groups_q, groups_k, groups_v, rounds, pieces, share, extra;
 };
-// Dynamic shared memory of the largest launch: 256 / (D / 16) x 4 rows of one head each.
-constexpr int kRotarySmem = 68 * 1024;
 
 struct DecodeParams {
   void *out;
@@ -239,7 +239,9 @@ cudaError_t launch_write_fp4(const Fp4WriteParams &p, int in_dtype, cudaStream_t
 cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype, int sm_count, cudaStream_t st);
 
 // k_cache null: rows only, else the cache type says what becomes of keys and values.
-cudaError_t launch_rotary(const RotaryParams &p, int dtype, int cache_dtype, int sm_count, cudaStream_t st);
+cudaError_t launch_rotary_f32(const RotaryParams &p, int cache_dtype, int sm_count, cudaStream_t st);
+cudaError_t launch_rotary_bf16(const RotaryParams &p, int cache_dtype, int sm_count, cudaStream_t st);
+cudaError_t launch_rotary_f16(const RotaryParams &p, int cache_dtype, int sm_count, cudaStream_t st);
 
 constexpr bool mma_fp4(int kind) { return kind == KIND_FP4_BF16Q || kind == KIND_FP4_F16Q; }
 // Tensor-core kernel shape per (kind, head size): warps per CTA and pipeline

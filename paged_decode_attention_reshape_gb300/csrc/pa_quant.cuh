@@ -1,5 +1,5 @@
 // pa_quant.cuh -- input rows as fp32 values, the quotients that quantisation takes and the E4M3
-// conversion, shared by the cache writes (pa_write.cu, pa_fp4.cu, pa_rotary.cu).
+// conversion, shared by the cache writes (pa_write.cu, pa_fp4.cu, pa_rotary.cuh).
 #pragma once
 
 #include "pa_device.cuh"
