@@ -90,7 +90,7 @@ def library_path() -> str:
 
 def lib() -> ctypes.CDLL:
     """Load libpa_gb300.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _describe
     if _lib is not None:
         return _lib
     with _lock:
@@ -174,6 +174,11 @@ def lib() -> ctypes.CDLL:
             L.pa_profile_enable.argtypes = [i32]
             L.pa_profile_read.restype = i32
             L.pa_profile_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]
+            try:
+                from ._marshal import describe
+                _describe = describe
+            except ImportError:  # (not built, or for another torch: the Python form says the same)
+                pass
             _lib = L
     return _lib
 
@@ -230,6 +235,12 @@ def _cache(t: torch.Tensor) -> bytes:
     return _desc(t, PA_FP4_E2M1 if t.dtype is torch.uint8 and t.dim() == 3 else None)
 
 
+def _describe(kinds: bytes, *tensors):
+    """The pa_tensor bytes of a call's tensors, None for None; kinds: b"t" or b"c" (_cache) for each.  lib()
+    puts the native form (csrc/pa_marshal.cpp: 0.06 us a tensor against 0.6) in its place where it is built."""
+    return tuple(None if t is None else _cache(t) if k == 99 else _desc(t) for k, t in zip(kinds, tensors))
+
+
 def _write_options(k_scale, v_scale, scale_stride, device_error) -> bytes:
     return _WRITE_OPTIONS.pack(_addr(k_scale), _addr(v_scale), int(scale_stride), _addr(device_error))
 
@@ -246,11 +257,16 @@ def _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size
 # call's host time), where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
+_cuda_ready = False  # torch.cuda.is_initialized() was true (it stays so)
 
 
 def _stream(stream) -> int:
+    global _cuda_ready
     if stream is None:
+        if _cuda_ready:
+            return _raw_stream(_current_device())
         if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            _cuda_ready = True
             return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -274,7 +290,7 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, kv_dtype: i
     """Scatter key/value [T, Hkv, D] rows into k_cache/v_cache [NB, Hkv, 16, D] at slot_mapping [T] (int64).
     kv_dtype PA_KV_FP8_E4M3 (PA_KV_FP4_E2M1: into 4-bit pages) quantises with the device fp32 scales
     k_scale/v_scale (1-element tensors)."""
-    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    args = _describe(b"ttcct", key, value, k_cache, v_cache, slot_mapping)
     rc = lib().pa_reshape_and_cache(*args, int(kv_dtype), _ptr(k_scale), _ptr(v_scale),
                                     _ptr(device_error), _stream(stream))
     _check(rc, "pa_reshape_and_cache")
@@ -287,7 +303,7 @@ def pa_reshape_and_cache_opt(key, value, k_cache, v_cache, slot_mapping, kv_dtyp
     (scale_stride 0: one scale for every head).  The cache may be a strided view (an NHD cache
     [NB, 16, Hkv, D] passed as .permute(0, 2, 1, 3))."""
     o = _write_options(k_scale, v_scale, scale_stride, device_error)
-    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    args = _describe(b"ttcct", key, value, k_cache, v_cache, slot_mapping)
     rc = lib().pa_reshape_and_cache_opt(*args, int(kv_dtype), o,
                                         _stream(stream))
     _check(rc, "pa_reshape_and_cache_opt")
@@ -299,7 +315,7 @@ def pa_gather_cache(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_
     from a cache of key's type, code * scale from an E4M3 or 4-bit cache (scales as
     pa_reshape_and_cache_opt).  A negative slot leaves its row as it was."""
     o = _write_options(k_scale, v_scale, scale_stride, device_error)
-    args = (_desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
+    args = _describe(b"ttcct", key, value, k_cache, v_cache, slot_mapping)
     rc = lib().pa_gather_cache(*args, o, _stream(stream))
     _check(rc, "pa_gather_cache")
 
@@ -313,17 +329,13 @@ def pa_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int =
     return table
 
 
-def _desc_or_none(t):
-    return None if t is None else _desc(t)
-
-
 def pa_rotary(q_out, q, k_out, key, positions, frequencies, q_weight=None, k_weight=None, eps: float = 1e-6,
               interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
     """Rows of queries q [T, Hq, D] and keys key [T, Hk, D] rotated by positions [T] (int64 or int32) into
     q_out and k_out (which may be q and key themselves; either pair may be None).  frequencies: int64 [R / 2]
     (pa_rotary_frequencies) or None.  With q_weight / k_weight [D] each head is normalised first."""
     o = _ROTARY_OPTIONS.pack(1 if interleaved else 0, magnitude, eps, 0, 0, 0, 0)
-    args = tuple(map(_desc_or_none, (q_out, q, k_out, key, positions, frequencies, q_weight, k_weight)))
+    args = _describe(b"tttttttt", q_out, q, k_out, key, positions, frequencies, q_weight, k_weight)
     rc = lib().pa_rotary(*args, o, _stream(stream))
     _check(rc, "pa_rotary")
 
@@ -336,10 +348,9 @@ def pa_rotary_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_
     slot_mapping, in one pass; scales and kv_dtype as pa_reshape_and_cache_opt."""
     o = _ROTARY_OPTIONS.pack(1 if interleaved else 0, magnitude, eps, _addr(k_scale), _addr(v_scale),
                              int(scale_stride), _addr(device_error))
-    args = (_desc_or_none(q_out), _desc_or_none(q), _desc(key), _desc(value), _cache(k_cache), _cache(v_cache))
-    rc = lib().pa_rotary_and_cache(*args, _desc_or_none(positions), _desc(slot_mapping), _desc_or_none(frequencies),
-                                   _desc_or_none(q_weight), _desc_or_none(k_weight), int(kv_dtype), o,
-                                   _stream(stream))
+    args = _describe(b"ttttccttttt", q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, frequencies,
+                     q_weight, k_weight)
+    rc = lib().pa_rotary_and_cache(*args, int(kv_dtype), o, _stream(stream))
     _check(rc, "pa_rotary_and_cache")
 
 
@@ -353,7 +364,7 @@ def pa_decode_opt(out, q, k_cache, v_cache, block_table, seq_lens, scale: float,
     no wait gives up)."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     rc = lib().pa_decode_opt(*args, float(scale), int(num_kv_heads), o,
                              _stream(stream))
     _check(rc, "pa_decode_opt")
@@ -370,9 +381,9 @@ def pa_decode_accumulate(out, q, k_cache, v_cache, block_table, seq_lens, scale:
     may be PA_PARTITION_BALANCED)."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     rc = lib().pa_decode_accumulate(*args, float(scale), int(num_kv_heads),
-                                    _desc(weights), o, _stream(stream))
+                                    *_describe(b"t", weights), o, _stream(stream))
     _check(rc, "pa_decode_accumulate")
 
 
@@ -391,7 +402,7 @@ def pa_decode_window(out, q, k_cache, v_cache, block_table, seq_lens, scale: flo
     of pages in between are not read.  A caller's workspace needs pa_decode_window_workspace_size bytes."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     rc = lib().pa_decode_window(*args, float(scale), int(num_kv_heads), int(window), int(sinks), o, _stream(stream))
     _check(rc, "pa_decode_window")
 
@@ -404,8 +415,7 @@ def pa_attention_window(out, q, k_cache, v_cache, query_start_loc, block_table, 
     and the first `sinks` ones.  Workspace as pa_decode_window."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(query_start_loc), _desc(block_table),
-            _desc(seq_lens))
+    args = _describe(b"ttccttt", out, q, k_cache, v_cache, query_start_loc, block_table, seq_lens)
     rc = lib().pa_attention_window(*args, float(scale), int(num_kv_heads), int(max_query_len), int(window), int(sinks),
                                    o, _stream(stream))
     _check(rc, "pa_attention_window")
@@ -424,8 +434,8 @@ def pa_evict(k_cache, v_cache, block_table, seq_lens, weights, budget: int, rece
     """Shorten every sequence to `budget` tokens per KV head, in place: its last `recent` ones and those of
     largest weights (fp32 [S, Hkv, W]).  Writes kept (int32 [S, Hkv, budget] positions, -1 padding),
     new_seq_lens (int32 [S]) and new_weights (as weights, zeros behind the kept ones)."""
-    args = (_cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens), _desc(weights))
-    outs = (_desc(kept), _desc(new_seq_lens), _desc(new_weights))
+    args = _describe(b"ccttt", k_cache, v_cache, block_table, seq_lens, weights)
+    outs = _describe(b"ttt", kept, new_seq_lens, new_weights)
     rc = lib().pa_evict(*args, int(budget), int(recent),
                         *outs, _ptr(device_error), _stream(stream))
     _check(rc, "pa_evict")
@@ -442,11 +452,9 @@ def pa_decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_tab
     the scales also quantise the rows written to an FP8 or 4-bit cache."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    nrs = None if new_rows_start is None else _desc(new_rows_start)
-    args = (_desc(out), _desc(q), _desc(key), _desc(value), _cache(k_cache), _cache(v_cache), _desc(slot_mapping))
-    rc = lib().pa_decode_step(*args, nrs, _desc(block_table),
-                              _desc(seq_lens), float(scale), int(num_kv_heads), o,
-                              _stream(stream))
+    args = _describe(b"ttttcctttt", out, q, key, value, k_cache, v_cache, slot_mapping, new_rows_start, block_table,
+                     seq_lens)
+    rc = lib().pa_decode_step(*args, float(scale), int(num_kv_heads), o, _stream(stream))
     _check(rc, "pa_decode_step")
 
 
@@ -460,8 +468,7 @@ def pa_attention_varlen(out, q, k_cache, v_cache, query_start_loc, block_table, 
     size is pa_decode_workspace_size with num_heads = Hq * max_query_len."""
     o = _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                         first_wait_limit)
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(query_start_loc), _desc(block_table),
-            _desc(seq_lens))
+    args = _describe(b"ttccttt", out, q, k_cache, v_cache, query_start_loc, block_table, seq_lens)
     rc = lib().pa_attention_varlen(*args, float(scale), int(num_kv_heads),
                                    int(max_query_len), o, _stream(stream))
     _check(rc, "pa_attention_varlen")
@@ -471,7 +478,7 @@ def pa_decode(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, num
               stream=None) -> None:
     """Paged decode attention: out/q [S, Hq, D], caches [NB, Hkv, 16, D], block_table [S, maxNB] int32,
     seq_lens [S] int32."""
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     rc = lib().pa_decode(*args, float(scale), int(num_kv_heads), _stream(stream))
     _check(rc, "pa_decode")
 
@@ -481,7 +488,7 @@ def pa_decode_ex(out, q, k_cache, v_cache, block_table, seq_lens, scale: float, 
                  stream=None) -> None:
     """pa_decode with FP8 scales, explicit partition size (0 heuristic, -1 unsplit), caller workspace
     (a zero-filled uint8 CUDA tensor, see pa_decode_workspace_size) and device error word (int32)."""
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().pa_decode_ex(*args, float(scale), int(num_kv_heads), _ptr(k_scale),
                             _ptr(v_scale), int(partition_size), _ptr(workspace), ws_bytes, _ptr(device_error),
@@ -495,7 +502,7 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_table, seq_lens, scale: fl
     where they run decode.  Split-KV scratch comes from a fixed 32 MiB buffer inside the library,
     shared by all calls on a device (calls that overlap on the GPU race on it); a problem needing
     more than that raises PAError(PA_ERR_WORKSPACE)."""
-    args = (_desc(out), _desc(q), _cache(k_cache), _cache(v_cache), _desc(block_table), _desc(seq_lens))
+    args = _describe(b"ttcctt", out, q, k_cache, v_cache, block_table, seq_lens)
     rc = lib().pa_decode_noalloc(*args, float(scale), int(num_kv_heads), _ptr(k_scale),
                                  _ptr(v_scale), int(partition_size), _ptr(device_error), _stream(stream))
     _check(rc, "pa_decode_noalloc")
@@ -608,6 +615,6 @@ class BlockManager:
 def pa_copy_blocks(k_cache, v_cache, block_pairs, device_error=None, stream=None) -> None:
     """Copy whole cache blocks: for each row (src, dst) of block_pairs (int64 [n, 2] on the
     device), block src of k_cache / v_cache is copied to block dst."""
-    args = (_cache(k_cache), _cache(v_cache), _desc(block_pairs))
+    args = _describe(b"cct", k_cache, v_cache, block_pairs)
     rc = lib().pa_copy_blocks(*args, _ptr(device_error), _stream(stream))
     _check(rc, "pa_copy_blocks")

@@ -1,7 +1,8 @@
 """Build libpa_gb300.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit compiles in parallel into ``_build/``; the objects are
-linked into ``libpa_gb300.so`` next to this file.  Rebuilds only when a source or
+linked into ``libpa_gb300.so`` next to this file.  Beside it, with the host compiler, the
+binding's descriptor code (``_marshal.so``, csrc/pa_marshal.cpp).  Rebuilds only when a source or
 header is newer than the library.
 """
 from __future__ import annotations
@@ -18,9 +19,14 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa_gb300.so")
-SOURCES = ["pa_api.cu", "pa_write.cu", "pa_decode.cu", "pa_decode_mma16.cu", "pa_decode_mma_fp8.cu", "pa_decode_mma_fp4.cu",
-           "pa_noalloc.cu", "pa_blocks.cu", "pa_fp4.cu", "pa_evict.cu", "pa_chunk_mma16.cu", "pa_rotary_f32.cu", "pa_rotary_bf16.cu", "pa_rotary_f16.cu",
-           "pa_decode_window_16.cu", "pa_decode_window_fp8.cu", "pa_decode_window_fp4.cu", "pa_chunk_window.cu"]
+# (the slowest to compile first)
+SOURCES = ["pa_decode_mma_fp4.cu", "pa_decode_mma16.cu", "pa_decode_mma_fp8.cu", "pa_decode_window_fp4.cu",
+           "pa_rotary_f32.cu", "pa_decode_window_16.cu", "pa_decode_window_fp8.cu", "pa_rotary_bf16.cu", "pa_rotary_f16.cu",
+           "pa_chunk_window.cu", "pa_chunk_mma16.cu", "pa_fp4.cu", "pa_decode.cu", "pa_evict.cu", "pa_write.cu", "pa_api.cu",
+           "pa_noalloc.cu", "pa_blocks.cu"]
+MARSHAL_SOURCE = os.path.join(CSRC, "pa_marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
+NO_MARSHAL = os.path.join(BUILD, "no_marshal")  # it could not be compiled here
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "-Xptxas", "-warn-spills"]
@@ -35,14 +41,36 @@ def _nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "pa.h"), __file__])
+            + glob.glob(os.path.join(CSRC, "*.h"))
+            + [MARSHAL_SOURCE, os.path.join(ROOT, "include", "pa.h"), __file__])
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not (os.path.exists(MARSHAL) or os.path.exists(NO_MARSHAL)):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _build_marshal() -> None:
+    """_marshal.so against the installed torch.  Without it the binding describes tensors in Python, so a
+    machine without torch's headers still builds."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = MARSHAL + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        open(NO_MARSHAL, "w").close()
+        sys.stderr.write("pa_marshal.cpp was not compiled (calls take longer on the host):\n%s\n" % (r.stdout + r.stderr)[-2000:])
+        return
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -62,8 +90,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -716,7 +716,11 @@ cudaError_t launch_chunk(const DecodeParams &p, int kind, const CUtensorMap &tmK
                          const CUtensorMap &tmQ, cudaStream_t st) {
   // head size 128 with more than one tile of query rows per KV head: two 128-row tiles per
   // CTA share each page (measured faster there; at head size 64 one tile per CTA is faster)
+#ifdef CHUNK_ONE
+  const bool two = !WIN && p.D == 128 && p.nq_max * p.G > kChunkTwoTileColumns;
+#else
   const bool two = p.D == 128 && p.nq_max * p.G > kChunkTwoTileColumns;
+#endif
   if (kind == KIND_BF16 && p.D == 64) return UmmaLaunch<KIND_BF16, 64, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
   if (kind == KIND_BF16 && p.D == 128)
     return two ? UmmaLaunch<KIND_BF16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)
