@@ -227,6 +227,7 @@ struct Plan {
   int flat;     // CTAs (with `warps`: warps) per head row of the balanced split (0 = none)
   int status;
   int warps;    // 1: the balanced split over warps (4-bit caches)
+  int narrow;   // 1: CTAs of half the warps (windows)
 };
 int balanced_ctas(int Hq, int Hkv, int D, int kind, int sm, bool device) {
   const int64_t rows = static_cast<int64_t>(Hkv) * ((Hq / Hkv + 7) / 8);
@@ -263,7 +264,7 @@ bool plan_fp4(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool d
 // varlen: several query tokens; plain: one, and no ALiBi
 Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool device, int request,
                bool varlen = false, bool plain = true) {
-  Plan pl{0, 0, 0, PA_OK, 0};
+  Plan pl{0, 0, 0, PA_OK, 0, 0};
   if (mma_fp4(kind) && request == 0 &&
       plan_fp4(S, Hq, Hkv, D, maxNB, kind, sm, device, varlen, plain, false, &pl))
     return pl;
@@ -295,29 +296,33 @@ int window_blocks(int maxNB, int64_t window, int64_t sinks, int G, int nq) {
 // The plan of a call under a window, of `pages` a unit by window_blocks (nearly what every longer sequence
 // reads, where a plan by the table's width has to guess).  Units that leave half of the resident CTA slots
 // empty are cut into 2, 4 or 8 parts a cluster, as long as the slots hold them all and a warp keeps two
-// pages; the cluster costs about 2 us, which fewer than eight pages a warp do not repay.  Units that
-// fill the slots once and a little more run as the balanced split where they are long.  Else whole units.
+// pages; the cluster costs about 2 us, which fewer than eight pages a warp do not repay.  Whole units run in
+// CTAs of half the warps, twice as many to an SM, where that brings all of them in at once (a second
+// wave of CTAs costs 5 us before its first page) or where they are so short that their own start weighs most
+// (`plain`: one query and no ALiBi, the only kernels built so).
 // Measured on GB300, 8 KV heads of 128, bf16 (us; unsplit / 2 / 4 / 8 parts / fixed partitions of the best
 // size / balanced): 1 sequence, window 1024, 65 pages: 14.0 / 11.4 / 8.4 / 7.2 / 9.3 / 29.0; 1 x 128: 5.3 / 6.6 /
 // 5.6 / 5.8 / - / 10.5; 4 x 4112: 43.9 / 26.4 / 17.4 / 16.1 / 18.2 / 26.0; 8 x 1024: 14.4 / 12.5 / 11.3 / 19.2 / 12.8 /
-// 17.8; 16 x 256: 7.5 / 9.7 / 16.2 / 22.0 / 10.8 / 17.6; 32 x 1024: 24.3 / 36.3 / 36.3 / 51.6 / 31.2 / 29.8; 64 x 512,
-// 1.1 waves: 32.0 / 39.5 / - / - / 32.3 / 31.6; 64 x 2048: 96.3 / 95.0 / - / - / 89.1 / 87.3; 128 x 2048, E4M3, 1.7 waves:
-// 91.0 / 110 / - / - / 115 / 93.2.
-Plan make_window_plan(int S, int Hq, int Hkv, int D, int pages, int kind, int sm, bool device, int request, bool varlen) {
+// 17.8; 16 x 256: 7.5 / 9.7 / 16.2 / 22.0 / 10.8 / 17.6; 32 x 1024: 24.3 / 36.3 / 36.3 / 51.6 / 31.2 / 29.8.
+// Unsplit in whole / half CTAs (and balanced): 64 x 512, 1.1 waves: 32.0 / 26.3 (32.2); 64 x 2048: 96.3 / 82.7
+// (88.8); 128 x 2048, E4M3, 1.7 waves: 92.5 / 90.0 (94.8); 128 x 256, 2.2 waves: 34.1 / 36.1; 256 x 1024, 4.5 waves:
+// 153 / 159; 256 x 128 (10 pages): 36.8 / 34.7, head size 64: 24.1 / 20.5.
+Plan make_window_plan(int S, int Hq, int Hkv, int D, int pages, int kind, int sm, bool device, int request, bool varlen,
+                      bool plain) {
   if (request != 0) return make_plan(S, Hq, Hkv, D, pages, kind, sm, device, request, varlen, false);
-  Plan pl{0, 0, 0, PA_OK, 0};
+  Plan pl{0, 0, 0, PA_OK, 0, 0};
   const int64_t units = static_cast<int64_t>(S) * Hkv * ((Hq / Hkv + 7) / 8);
   const int64_t slots = static_cast<int64_t>(std::max(sm, 1)) * ctas_per_sm(kind, D, device);
   const int warps = kind == KIND_F32 ? (D == 256 ? 2 : 4) : mma_warps(kind, D);
   if (pages >= 8 * warps) {
     for (const int C : {8, 4, 2}) {
       if (units * C > slots || pages < 2 * C * warps) continue;
+      if (C == 2 && mma_fp4(kind) && pages < 16 * warps) continue;  // (16 x 1024: 10.6 us, in two parts 13.5)
       pl.cluster = C;
       return pl;
     }
-    if (units > slots && units * 3 < slots * 4 && pages >= 64 && !varlen && kind != KIND_F32)
-      return make_plan(S, Hq, Hkv, D, pages, kind, sm, device, S <= kFlatMaxSeqs ? PA_PARTITION_BALANCED : -1, varlen, false);
   }
+  if (plain && kind != KIND_F32) pl.narrow = units > slots && (units <= 2 * slots || 2 * pages <= 5 * warps) ? 1 : 0;
   return pl;
 }
 
@@ -922,7 +927,7 @@ PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_h
     int flat = std::max(balanced_ctas(num_heads, num_kv_heads, head_size, kind, sm, false),
                         balanced_ctas(num_heads, num_kv_heads, head_size, kind4, sm, false));
     // 4-bit caches: split over warps, or (ALiBi, several query tokens) into fixed partitions
-    Plan pl{0, 0, 0, PA_OK, 0};
+    Plan pl{0, 0, 0, PA_OK, 0, 0};
     if (plan_fp4(num_seqs, num_heads, num_kv_heads, head_size, max_blocks_per_seq, kind4, sm, false, false, true, true,
                  &pl))
       flat = std::max(flat, pl.flat);
@@ -961,7 +966,7 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
       continue;
     }
     NB = window_blocks(NB, window, sinks, num_heads / num_kv_heads, max_query_len);
-    pl = make_window_plan(num_seqs, Hqv, num_kv_heads, head_size, NB, kind, sm, true, partition_size, varlen);
+    pl = make_window_plan(num_seqs, Hqv, num_kv_heads, head_size, NB, kind, sm, true, partition_size, varlen, true);
     if (pl.status == PA_OK && pl.cluster == 0 && (pl.flat > 0 || (pl.P > 0 && pl.P < NB * kBlock)))
       need = std::max(need, workspace_layout(num_seqs, Hqv, num_kv_heads, head_size, NB, pl.P, pl.flat).total);
   }
@@ -1078,7 +1083,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   // shared by 64 rows, no split) unless a split was asked for.
   const bool chunk = varlen && (kind == KIND_BF16 || kind == KIND_F16) && (D == 64 || D == 128) &&
                      (partition_size == 0 || partition_size == -1) && VH >= chunk_min_columns(D);
-  const Plan pl = window > 0 ? make_window_plan(S, Hqv, Hkv, D, NBw, kind, sm, true, chunk ? -1 : partition_size, varlen)
+  const Plan pl = window > 0 ? make_window_plan(S, Hqv, Hkv, D, NBw, kind, sm, true, chunk ? -1 : partition_size, varlen,
+                                                !varlen && !o.alibi_slopes)
                              : make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,
                                          !varlen && !o.alibi_slopes);
   if (pl.status != PA_OK) return pl.status;
@@ -1114,6 +1120,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   p.scale_stride = o.scale_stride;
   p.alibi = o.alibi_slopes;
   p.window = static_cast<int>(window);
+  p.narrow = pl.narrow;
   p.sinks = static_cast<int>(sinks);
   p.pages_per_part = P > 0 ? P / kBlock : std::max(maxNB, 1);
   p.max_parts = max_parts;
@@ -1128,7 +1135,8 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     // with every CTA resident from the start the order buys nothing and the ranking
     // (a read of every length plus two block barriers) sits on each CTA's critical path.
     const int64_t ctas = static_cast<int64_t>(S) * Hkv * p.HG * max_parts;
-    p.lpt = (pl.flat == 0 && longest_first(kind, S) && ctas > static_cast<int64_t>(sm) * ctas_per_sm(kind, D, true))
+    const int64_t slots = static_cast<int64_t>(sm) * ctas_per_sm(kind, D, true) * (pl.narrow ? 2 : 1);
+    p.lpt = (pl.flat == 0 && longest_first(kind, S) && ctas > slots)
                 ? 1
                 : 0;
   }

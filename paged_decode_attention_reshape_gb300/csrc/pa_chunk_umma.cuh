@@ -473,6 +473,20 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     const int pos = valid ? pos0 + row / G : -1;
     const float ab = (p.alibi && valid) ? __ldg(p.alibi + g * G + row % G) * 1.4426950408889634f : 0.f;
     float m = kUmmaEmpty;
+    // WIN, one tile a CTA: groups that every row of the warp sees in full, k < first_whole and from_whole <= k <
+    // to_whole, worked out once, and masks of 16 bits a page (64 x 256..512 new tokens, 32/8 heads of 64, window
+    // 1024: 566 us; a vote in each group and three compares a token 668).  With two tiles the same took longer
+    // (heads of 128, window 4096: 2232 us against 1957), so those vote and compare.
+    constexpr bool BITS = WIN && T == 1;
+    int first_whole = 0, from_whole = 0, to_whole = 0;
+    if constexpr (BITS) {
+      constexpr int GT = C::GP * kBlock;  // tokens of a group
+      first_whole = min(wg.ns / C::GP, win.sinks / GT);
+      const int t1 = wg.first * kBlock;  // the window's run starts here
+      const int from = valid ? max(0, pos - p.window + 1 - t1 + GT - 1) / GT : 0, to = valid ? max(0, pos + 1 - t1) / GT : ngr;
+      from_whole = wg.sinks_groups + __reduce_max_sync(0xffffffffu, from);
+      to_whole = wg.sinks_groups + __reduce_min_sync(0xffffffffu, to);
+    }
     for (int k = 0; k < ngr && ok; ++k) {
       const int b = k & 1;
       if (!__all_sync(0xffffffffu, umma_wait(sfull(tile, b), (k >> 1) & 1, abort))) {
@@ -493,9 +507,14 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
       // ---- logits in log2 units, masked past the row's position; a group the whole warp
       // sees in full (or rows without a query) skips the mask
       const int t0 = group_base(k) * kBlock;
-      bool mine = t0 + 63 <= pos;
-      if constexpr (WIN) mine = mine && group_pages(k) == C::GP && (t0 > pos - p.window || t0 + 64 <= p.sinks);
-      const bool whole = __all_sync(0xffffffffu, mine || !valid);
+      bool whole;
+      if constexpr (BITS) {
+        whole = k < first_whole || (k >= from_whole && k < to_whole);
+      } else {
+        bool mine = t0 + 63 <= pos;
+        if constexpr (WIN) mine = mine && group_pages(k) == C::GP && (t0 > pos - p.window || t0 + 64 <= p.sinks);
+        whole = __all_sync(0xffffffffu, mine || !valid);
+      }
       const float base = ab * static_cast<float>(t0 - pos);  // ALiBi bias of token t0
       // raw: the scores stay unscaled (scale > 0 keeps their order) and the scale is folded
       // into the exponent below; otherwise x holds the biased / masked log2 logits
@@ -506,12 +525,24 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
           for (int i = 0; i < 64; ++i) x[i] = fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base));
         }
       } else {
-        const int lim = WIN ? min(pos - t0, group_pages(k) * kBlock - 1) : pos - t0;  // tokens i <= lim are visible
-        const int lo = WIN ? pos - p.window - t0 : -1, hi = WIN ? p.sinks - t0 : 0;  // and, of those, i > lo and i < hi
+        if constexpr (BITS) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          x[i] = i <= lim && (!WIN || i > lo || i < hi) ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base))
-                                                        : -INFINITY;
+          for (int j = 0; j < C::GP; ++j) {
+            const int at = t0 + j * kBlock;  // the page's first token; bits of the tokens that are seen
+            const uint32_t old = Window::below(pos + 1 - p.window - at) & ~Window::below(p.sinks - at);
+            const uint32_t seen = j < group_pages(k) ? Window::below(pos + 1 - at) & ~old : 0u;
+#pragma unroll
+            for (int i = kBlock * j; i < kBlock * j + kBlock; ++i)
+              x[i] = (seen >> (i % kBlock)) & 1u ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base)) : -INFINITY;
+          }
+        } else {
+          const int lim = WIN ? min(pos - t0, group_pages(k) * kBlock - 1) : pos - t0;  // tokens i <= lim are visible
+          const int lo = WIN ? pos - p.window - t0 : -1, hi = WIN ? p.sinks - t0 : 0;  // and, of those, i > lo and i < hi
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            x[i] = i <= lim && (!WIN || i > lo || i < hi) ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base))
+                                                          : -INFINITY;
+        }
       }
       // row max of the group: a tree of three-input max instructions
       float lm;
@@ -716,11 +747,7 @@ cudaError_t launch_chunk(const DecodeParams &p, int kind, const CUtensorMap &tmK
                          const CUtensorMap &tmQ, cudaStream_t st) {
   // head size 128 with more than one tile of query rows per KV head: two 128-row tiles per
   // CTA share each page (measured faster there; at head size 64 one tile per CTA is faster)
-#ifdef CHUNK_ONE
-  const bool two = !WIN && p.D == 128 && p.nq_max * p.G > kChunkTwoTileColumns;
-#else
   const bool two = p.D == 128 && p.nq_max * p.G > kChunkTwoTileColumns;
-#endif
   if (kind == KIND_BF16 && p.D == 64) return UmmaLaunch<KIND_BF16, 64, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
   if (kind == KIND_BF16 && p.D == 128)
     return two ? UmmaLaunch<KIND_BF16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)

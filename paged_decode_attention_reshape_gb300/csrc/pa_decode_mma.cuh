@@ -672,7 +672,7 @@ __device__ __forceinline__ void zero_rows(const DecodeParams &p, const Cols &cm,
 // variants about 1.4 us on a 30 us decode, so only this one carries it.
 // ACC: scores stored for pa_decode_accumulate.  WIN: under a window.
 template <int KIND, int D, int W, int STAGES, bool PLAIN, bool EARLY, bool ACC, bool WIN>
-__global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
+__global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D) * (mma_warps(KIND, D) / W))
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
   using C = MmaCfg<KIND, D, W, STAGES>;
@@ -965,12 +965,12 @@ __global__ void __launch_bounds__(W * 32, mma_min_ctas(KIND, D))
 
 // Host side of one (kind, head size) instantiation: function attributes, launch and
 // resident CTAs per SM.
-template <int KIND, int D>
+template <int KIND, int D, int WARPS = mma_warps(KIND, D)>
 struct MmaLaunch {
   static constexpr int kKind = KIND, kD = D;
-  static constexpr int W = mma_warps(KIND, D), ST = mma_stages(KIND, D);
+  static constexpr int W = WARPS, ST = mma_stages(KIND, D);
   using C = MmaCfg<KIND, D, W, ST>;
-  static_assert(C::SMEM == mma_smem(KIND, D), "shape table out of sync");
+  static_assert(W != mma_warps(KIND, D) || C::SMEM == mma_smem(KIND, D), "shape table out of sync");
 
   template <bool PLAIN, bool EARLY, bool ACC, bool WIN>
   static cudaError_t attrs() {
@@ -1001,8 +1001,9 @@ struct MmaLaunch {
     return p.early ? launch_variant<true, true, false>(p, tmK, tmV, st) : launch_variant<true, false, false>(p, tmK, tmV, st);
   }
   static cudaError_t launch_window(const DecodeParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
-    return !p.qsl && !p.alibi ? launch_variant<true, false, false, true>(p, tmK, tmV, st)
-                              : launch_variant<false, false, false, true>(p, tmK, tmV, st);
+    if (p.qsl || p.alibi) return launch_variant<false, false, false, true>(p, tmK, tmV, st);
+    if (p.narrow) return MmaLaunch<KIND, D, mma_warps(KIND, D) / 2>::template launch_variant<true, false, false, true>(p, tmK, tmV, st);
+    return launch_variant<true, false, false, true>(p, tmK, tmV, st);
   }
   static int occupancy() {  // 0 when it cannot be queried
     int n = 0;

@@ -159,6 +159,7 @@ struct DecodeParams {
   // pa_decode_window / pa_attention_window (0: everything is seen): a query at position P sees the
   // tokens t <= P with t > P - window or t < sinks.  Both at most max_blocks * 16.
   int window, sinks;
+  int narrow;  // 1 (one query, no ALiBi, under a window): CTAs of half the warps, twice as many per SM
 };
 
 // The pages that a work item under a window reads, numbered without the gap between the first tokens'
