@@ -521,10 +521,12 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  * pages and the window's (its start is max(0, P + 1 - window), of the sequence's first query) may hold any
  * value, so their blocks can be given back.  Cost and workspace go by the window, not by the length.
  * Tokens of a page that is read which no query of the sequence sees never reach the output, whatever
- * they hold; a key or value that some query sees has to be finite for the other queries of its sequence
- * in the same call (they are multiplied by a weight of zero).
+ * they hold.  A value row (V) that some query sees is multiplied by a weight of zero for the other queries of
+ * its sequence in the same call, as in pa_attention_varlen: an infinity or NaN in it reaches them too.
  * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen).
- * Under a window a partition_size counts the visible tokens' pages, so it can be small.
+ * Under a window a partition_size counts the visible tokens' pages, so it can be small; 0 chooses whole
+ * units or a cluster split (no workspace).  A step's rows are written before (pa_rotary_and_cache,
+ * pa_reshape_and_cache): pa_decode_step and pa_decode_accumulate see the whole history.
  */
 int pa_decode_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
                      const pa_tensor *block_table, const pa_tensor *seq_lens, float scale, int num_kv_heads, int window,

@@ -202,3 +202,19 @@ def test_side_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     wc.check(gc.out, wc.reference(later))
+
+
+def test_calls_of_different_shapes_follow_each_other():
+    """The library's workspace between windowed, plain and accumulating calls of other shapes and splits."""
+    cases = [wc.make([3000, 20, 1500], 8, 2, 128, 900, 4, BF, seed=1), wc.make([700] * 9, 32, 4, 64, 333, 0, F16, seed=2),
+             wc.make([400, 2000], 8, 8, 128, 1000, 20, BF, "e4m3", seed=3, k_scale=0.05, v_scale=0.07)]
+    on = [wc.on_gpu(c) for c in cases]
+    want = [wc.reference(c) for c in cases]
+    for part in (64, BAL, 0, 32, 512, BAL, 16):
+        for c, g, w in zip(cases, on, want):
+            wc.check(wc.run(c, g, part, ws=False), w, "partition %d" % part)
+            full = wc.make([50, 300], 8, 2, 128, 10 ** 6, 0, BF, seed=4)
+            gf = wc.on_gpu(full)
+            pa.pa_decode_opt(gf.out, gf.q, gf.k_cache, gf.v_cache, gf.block_table, gf.seq_lens, full.scale, 2, partition_size=32)
+            wc.check(gf.out, wc.reference(full))
+

@@ -130,3 +130,58 @@ def test_keys_moved_to_new_positions():
     pair = torch.hypot(k[..., :64], k[..., 64:]).repeat(1, 1, 2).double().cpu()
     assert bool(((rows.double().cpu() - want).abs() <= 18 * 2.0 ** -24 * pair).all())
     assert torch.equal(vals, k)
+
+
+@pytest.mark.parametrize("kind,nhd", [("same", False), ("same", True), ("e4m3", False), ("fp4", False)])
+def test_blocks_past_4_gib(kind, nhd):
+    """The write and both windowed calls over blocks whose byte offsets pass 2^32."""
+    Hkv, Hq, D, W, K, lens = 2, 8, 128, 100, 4, [300, 257, 40]
+    per = {"same": Hkv * 16 * D * 2, "e4m3": Hkv * 16 * D, "fp4": Hkv * 9 * D}[kind]
+    base = (1 << 32) // per + 77
+    need = [(n + 15) // 16 for n in lens]
+    NB = base + sum(need) + 5
+    if kind == "fp4":
+        caches = [torch.empty(NB, Hkv, 9 * D, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    else:
+        shape = (NB, 16, Hkv, D) if nhd else (NB, Hkv, 16, D)
+        caches = [torch.empty(shape, dtype=torch.bfloat16 if kind == "same" else torch.uint8, device=DEV) for _ in range(2)]
+        if nhd:
+            caches = [c.permute(0, 2, 1, 3) for c in caches]
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)) + base
+    table = torch.full((3, max(need)), -1, dtype=torch.int32)
+    at = 0
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n].int()
+        at += n
+    slots = torch.cat([table[s][torch.arange(n) // 16].long() * 16 + torch.arange(n) % 16 for s, n in enumerate(lens)]).to(DEV)
+    pos = torch.cat([torch.arange(n) for n in lens]).to(DEV)
+    T = sum(lens)
+    x = torch.randn(T, Hq + 2 * Hkv, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    q, k, v = x[:, :Hq].contiguous(), x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    mode = {"same": pa.PA_KV_AUTO, "e4m3": pa.PA_KV_FP8_E4M3, "fp4": pa.PA_KV_FP4_E2M1}[kind]
+    sc = None if kind == "same" else torch.full((1,), 0.05 if kind == "e4m3" else 1.0, device=DEV)
+    kv = dict(k_scale=sc, v_scale=sc)
+    f = pa.pa_rotary_frequencies(D).to(DEV)
+    pa.pa_rotary_and_cache(q, q, k, v, *caches, pos, slots, f, mode, **kv)
+    back = torch.bfloat16 if kind == "same" else torch.float32
+    kb, vb = [torch.empty(T, Hkv, D, dtype=back, device=DEV) for _ in range(2)]
+    pa.pa_gather_cache(kb, vb, *caches, slots, **kv)
+    if kind == "same":
+        model.assert_rows(kb, *model.rows(k, pos, f))
+        assert torch.equal(vb, v)
+    ends = np.cumsum(lens)
+    c = wc.Case()
+    c.dtype, c.lens, c.Hkv, c.Hq, c.D, c.W, c.K, c.scale, c.alibi = torch.bfloat16, lens, Hkv, Hq, D, W, K, D ** -0.5, None
+    c.vals = [[y[e - n:e].double().cpu().numpy() for e, n in zip(ends, lens)] for y in (kb, vb)]
+    bt, sl = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for nq in (None, [70, 3, 20]):
+        c.nq = nq
+        rows = [e - 1 for e in ends] if nq is None else [i for e, n in zip(ends, nq) for i in range(e - n, e)]
+        c.q = q[rows].cpu()
+        out = torch.full((len(rows), Hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+        if nq is None:
+            pa.pa_decode_window(out, q[rows].contiguous(), *caches, bt, sl, c.scale, Hkv, W, K, **kv)
+        else:
+            starts = torch.from_numpy(np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)).to(DEV)
+            pa.pa_attention_window(out, q[rows].contiguous(), *caches, starts, bt, sl, c.scale, Hkv, max(nq), W, K, **kv)
+        wc.check(out, wc.reference(c), "new tokens %s" % nq)
