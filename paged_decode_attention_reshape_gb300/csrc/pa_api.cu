@@ -786,6 +786,14 @@ int rotary_impl(pa_tensor *q_out, const pa_tensor *q, pa_tensor *k_out, const pa
   if (T == 0 || Hq + Hk + Hv == 0) return PA_OK;
   for (const pa_tensor *t : {q, static_cast<const pa_tensor *>(q_out), key, static_cast<const pa_tensor *>(k_out), value})
     if (t && (r = check_row_pointers(t))) return r;
+  // outputs that overlap an input other than in place, or each other
+  const int row_eb = elem_bytes(dt);
+  for (const pa_tensor *out : {static_cast<const pa_tensor *>(q_out), static_cast<const pa_tensor *>(k_out)}) {
+    if (!out) continue;
+    const pa_tensor *own = out == q_out ? q : key;
+    for (const pa_tensor *x : {q, key, value, out == q_out ? static_cast<const pa_tensor *>(k_out) : nullptr})
+      if (x && !(x == own && x->data == out->data) && rows_shared(x, out, row_eb)) return PA_ERR_INVALID_ARG;
+  }
   if (pairs > 0 && !positions->data) return PA_ERR_INVALID_ARG;
   if (pairs > 0 && !on_elements(positions)) return PA_ERR_ALIGNMENT;
   if (cached && !slot_mapping->data) return PA_ERR_INVALID_ARG;

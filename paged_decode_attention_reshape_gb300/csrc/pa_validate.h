@@ -41,6 +41,25 @@ inline bool rows_overlap(const pa_tensor *t, int64_t len) {
   return (n > 1 && a < len) || (m > 1 && b < (n > 1 ? (n - 1) * a : 0) + len);
 }
 
+// Whether a row of one tensor [T, H, D] shares memory with a row of another of the same strides (elements of
+// eb bytes; views of one buffer, like heads side by side, do not).  Tensors of other strides are not looked at.
+inline bool rows_shared(const pa_tensor *a, const pa_tensor *b, int eb) {
+  const int64_t ts = a->stride[0] * eb, hs = a->stride[1] * eb, row = a->shape[2] * eb;
+  if (a->stride[0] != b->stride[0] || a->stride[1] != b->stride[1] || !a->data || !b->data) return false;
+  const int64_t away = static_cast<int64_t>(reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data));
+  auto near = [](int64_t x, int64_t step, int i) { return step > 0 ? x / step + i : 0; };
+  // b's row (0, 0) against a's rows (t, h) around it; t < 0, h < 0: b's rows against a's first
+  for (int i = -1; i <= 1; ++i) {
+    const int64_t t = near(away, ts, i), left = away - t * ts;
+    if (t >= a->shape[0] || -t >= b->shape[0]) continue;
+    for (int j = -1; j <= 1; ++j) {
+      const int64_t h = near(left, hs, j), apart = left - h * hs;
+      if (h < a->shape[1] && -h < b->shape[1] && apart < row && -apart < row) return true;
+    }
+  }
+  return false;
+}
+
 // Rows [T, H, D] whose every 32-byte piece is 32-byte aligned (element size eb).
 inline bool rows_aligned32(const pa_tensor *t, int eb) {
   return (reinterpret_cast<uintptr_t>(t->data) & 31u) == 0 && (t->stride[0] * eb) % 32 == 0 && (t->stride[1] * eb) % 32 == 0;

@@ -197,3 +197,54 @@ def test_option_struct_layout_matches_the_header(tmp_path):
     got = list(map(int, subprocess.check_output([str(exe)]).split()))
     assert got == [ctypes.sizeof(pa.PaRotaryOptions)] + [getattr(pa.PaRotaryOptions, f).offset for f in fields]
     assert len(pa._ROTARY_OPTIONS.pack(1, 2.0, 3.0, 0, 0, 0, 0)) == ctypes.sizeof(pa.PaRotaryOptions)
+
+
+@pytest.mark.parametrize("cached", [False, True])
+@pytest.mark.parametrize("what,by,status", [
+    ("q_out", HQ * D * 2, -1), ("q_out", -HQ * D * 2, -1),        # a token on, or back
+    ("q_out", D * 2, -1), ("q_out", -D * 2, -1), ("q_out", 16, -1),  # a head on or back, or inside a row
+    ("q_out", 3 * HQ * D * 2 + 32, -1), ("q_out", -(T - 1) * HQ * D * 2, -1)])
+def test_outputs_that_overlap_their_input(L, cached, what, by, status):
+    a = _args(cached)
+    a["q_out"].data = a["q"].data + by
+    assert _call(L, a) == status
+
+
+def test_views_of_one_buffer_do_not_overlap():
+    """The check itself over every pair of views of one buffer, against the rows' own bytes."""
+    import itertools
+
+    def shared(x, y):  # (start, strides, heads) in elements; as rows_shared in pa_validate.h
+        rows = lambda v: {(v[0] + t * v[1] + h * v[2] + d) for t in range(3) for h in range(v[3]) for d in range(16)}  # noqa: E731
+        return bool(rows(x) & rows(y))
+
+    def check(x, y):
+        ts, hs, row, away = x[1], x[2], 16, y[0] - x[0]
+        trunc = lambda p, q: int(p / q) if q else 0  # noqa: E731
+        for i in (-1, 0, 1):
+            t = trunc(away, ts) + i if ts else 0
+            left = away - t * ts
+            if t >= 3 or -t >= 3:
+                continue
+            for j in (-1, 0, 1):
+                h = trunc(left, hs) + j if hs else 0
+                apart = left - h * hs
+                if h < x[3] and -h < y[3] and -row < apart < row:
+                    return True
+        return False
+
+    for ts, hs in ((96, 16), (96, 32), (200, 48), (64, 16)):
+        heads = [n for n in (1, 2, 3) if (n - 1) * hs + 16 <= ts]
+        for hx, hy in itertools.product(heads, heads):
+            for off in range(-3 * ts - 20, 3 * ts + 20, 4):
+                x, y = (1000, ts, hs, hx), (1000 + off, ts, hs, hy)
+                assert check(x, y) == shared(x, y), (x, y)
+
+
+def test_refused_side_by_side_outputs(L):
+    a = _args(False)
+    a["k_out"] = _t([T, HKV, D], B16, a["q"].data + D * 2, strides=[HQ * D, D, 1])
+    assert _call(L, a) == -1                  # keys' output over queries
+    a = _args(False)
+    a["k_out"] = _t([T, HKV, D], B16, a["q_out"].data, strides=[HQ * D, D, 1])
+    assert _call(L, a) == -1                  # both outputs in one place
