@@ -525,6 +525,8 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  * they hold.  A value row (V) that some query sees is multiplied by a weight of zero for the other queries of
  * its sequence in the same call, as in pa_attention_varlen: an infinity or NaN in it reaches them too.
  * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen).
+ * pa_attention_window's kernels are pa_attention_varlen's; on 16-bit caches of head size 256, too, chunks of 40
+ * or more query columns per KV head run on the query-tile kernel (partition_size 0 or -1).
  * Under a window a partition_size counts the visible tokens' pages, so it can be small; 0 chooses whole
  * units or a cluster split (no workspace).  A step's rows are written before (pa_rotary_and_cache,
  * pa_reshape_and_cache): pa_decode_step and pa_decode_accumulate see the whole history.

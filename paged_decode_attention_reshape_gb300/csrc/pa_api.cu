@@ -288,9 +288,9 @@ Plan make_plan(int S, int Hq, int Hkv, int D, int maxNB, int kind, int sm, bool 
 
 // Chunks of query tokens run on the query-tile kernel (rows in the MMA M dimension, pages shared by 64
 // rows, no split) unless a split was asked for; columns: query columns per KV head.
-bool on_query_tiles(int kind, int D, int partition_size, int columns) {
-  return (kind == KIND_BF16 || kind == KIND_F16) && (D == 64 || D == 128) && (partition_size == 0 || partition_size == -1) &&
-         columns >= chunk_min_columns(D);
+bool on_query_tiles(int kind, int D, int partition_size, int columns, bool windowed) {
+  return (kind == KIND_BF16 || kind == KIND_F16) && (D == 64 || D == 128 || (D == 256 && windowed)) &&
+         (partition_size == 0 || partition_size == -1) && columns >= chunk_min_columns(D);
 }
 
 // Under a window: the most pages that a work item of the decode kernels reads (its numbers of Window),
@@ -966,14 +966,15 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
   const int sm = device_sm_count();
   if (sm <= 0) return 0;
   const int Hqv = num_heads * max_query_len;
-  if (max_query_len > 1 && on_query_tiles(kind, head_size, partition_size, Hqv / num_kv_heads)) return 0;
+  const bool whole = static_cast<int64_t>(window) + sinks >= static_cast<int64_t>(max_blocks_per_seq) * kBlock;
+  if (max_query_len > 1 && on_query_tiles(kind, head_size, partition_size, Hqv / num_kv_heads, !whole)) return 0;
   size_t need = 0;
   for (const bool varlen : {false, true}) {  // (a call of pa_attention_window may have one query each, too)
     if (!varlen && max_query_len > 1) continue;
     if (varlen && partition_size == PA_PARTITION_BALANCED) continue;
     int NB = max_blocks_per_seq;
     Plan pl;
-    if (static_cast<int64_t>(window) + sinks >= static_cast<int64_t>(NB) * kBlock) {
+    if (whole) {
       for (const bool plain : {false, true}) {
         pl = make_plan(num_seqs, Hqv, num_kv_heads, head_size, NB, kind, sm, true, partition_size, varlen, plain);
         if (pl.status == PA_OK && pl.cluster == 0 && (pl.flat > 0 || (pl.P > 0 && pl.P < NB * kBlock)))
@@ -1095,7 +1096,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   const int NBw = window > 0 ? window_blocks(maxNB, window, sinks, Hq / Hkv, varlen ? max_query_len : 1) : maxNB;
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
-  const bool chunk = varlen && on_query_tiles(kind, D, partition_size, VH);
+  const bool chunk = varlen && on_query_tiles(kind, D, partition_size, VH, window > 0);
   const Plan pl = window > 0 ? make_window_plan(S, Hqv, Hkv, D, NBw, kind, sm, true, chunk ? -1 : partition_size, varlen,
                                                 !varlen && !o.alibi_slopes)
                              : make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,

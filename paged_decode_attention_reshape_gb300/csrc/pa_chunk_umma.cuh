@@ -177,7 +177,7 @@ constexpr float kUmmaSlack = 8.f;              // lazy running max, log2 units (
 constexpr float kUmmaEmpty = -1e30f;           // running max of a row with no visible token yet
 
 // T row tiles of 128 rows per CTA.  T = 1: 6 warps, two CTAs per SM (their softmax and
-// MMA phases interleave).  T = 2: 10 warps, one CTA per SM; both tiles consume every K/V
+// MMA phases interleave; one at head size 256, whose output alone takes 256 of a tile's TMEM columns).  T = 2: 10 warps, one CTA per SM; both tiles consume every K/V
 // page that is loaded once, and the ring is deeper.
 template <int KIND, int D, int T>
 struct UmmaCfg {
@@ -185,7 +185,7 @@ struct UmmaCfg {
   static constexpr int TILES = T, ROWS = 128 * T;
   // warps 0 .. 4T-1 softmax, 4T .. 5T-1 one MMA issuer per tile, 5T the TMA producer
   static constexpr int MMA_WARP = 4 * T, TMA_WARP = 5 * T, THREADS = (5 * T + 1) * 32;
-  static constexpr int MIN_CTAS = T == 1 ? 2 : 1;
+  static constexpr int MIN_CTAS = T == 1 && D <= 128 ? 2 : 1;
   static constexpr int NBOX = D / 64;                 // 64-element (128-byte) boxes per row
   static constexpr int GP = 4;                        // pages per group: 64 tokens
   static constexpr int R = T == 1 ? (D == 64 ? 16 : 8) : (D == 64 ? 40 : 20);  // page slots of the ring
@@ -199,9 +199,9 @@ struct UmmaCfg {
   // q_full, v_tail, v_gap x2 (under a window)
   static constexpr int TBAR = 2 * NS * 8, NBARS = 2 * NS + 6 * T + 4;
   static constexpr size_t SMEM = 1024 + BAR_OFF + NBARS * 8 + 16;
-  static constexpr uint32_t TMEM_COLS = 256 * T;      // tile t: S/P buffers at 256 t + 0 / 64, O at 256 t + 128
+  static constexpr uint32_t TMEM_COLS = D == 256 ? 512 : 256 * T;  // tile t: S/P buffers at 256 t + 0 / 64, O at 256 t + 128
   static constexpr uint32_t OCOL = 128;
-  static_assert(D % 64 == 0 && D <= 128, "head size 64 or 128");
+  static_assert(D == 64 || D == 128 || (D == 256 && T == 1), "head size");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -752,6 +752,10 @@ cudaError_t launch_chunk(const DecodeParams &p, int kind, const CUtensorMap &tmK
   if (kind == KIND_BF16 && p.D == 128)
     return two ? UmmaLaunch<KIND_BF16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)
                : UmmaLaunch<KIND_BF16, 128, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
+  if constexpr (WIN) {
+    if (kind == KIND_BF16 && p.D == 256) return UmmaLaunch<KIND_BF16, 256, 1, true>::launch(p, tmK, tmV, tmQ, st);
+    if (kind == KIND_F16 && p.D == 256) return UmmaLaunch<KIND_F16, 256, 1, true>::launch(p, tmK, tmV, tmQ, st);
+  }
   if (kind == KIND_F16 && p.D == 64) return UmmaLaunch<KIND_F16, 64, 1, WIN>::launch(p, tmK, tmV, tmQ, st);
   if (kind == KIND_F16 && p.D == 128)
     return two ? UmmaLaunch<KIND_F16, 128, 2, WIN>::launch(p, tmK, tmV, tmQ, st)

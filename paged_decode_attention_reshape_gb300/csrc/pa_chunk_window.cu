@@ -1,5 +1,6 @@
 // pa_chunk_window.cu -- instantiations of the tensor-memory query-tile kernel (see
-// pa_chunk_umma.cuh) for bf16 and f16 caches, head sizes 64 and 128, one or two row tiles, under a window.
+// pa_chunk_umma.cuh) for bf16 and f16 caches, head sizes 64, 128 and 256, one or two row tiles, under a
+// window.
 #include "pa_chunk_umma.cuh"
 
 namespace pa {

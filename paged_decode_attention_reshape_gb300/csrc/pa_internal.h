@@ -302,8 +302,10 @@ cudaError_t launch_chunk_window(const DecodeParams &p, int kind, const CUtensorM
                                 const CUtensorMap &tmQ, cudaStream_t st);
 // Query columns per KV head (max_query_len x G) from which varlen attention uses it: below
 // that the column-group kernels are as fast or faster (256 sequences of 512-4096 tokens, 32/8
-// heads: at 32 columns 644 vs 737 us at head size 128, but 453 vs 325 us at head size 64).
-constexpr int chunk_min_columns(int D) { return D == 64 ? 32 : 64; }
+// heads: at 32 columns 644 vs 737 us at head size 128, but 453 vs 325 us at head size 64).  Head size 256,
+// under a window alone (64 x 1k..8k tokens, 32/8 heads, window 1024, columns / tile): 16 columns 138 / 249 us, 32 247 /
+// 250, 40 300 / 251, 64 465 / 247, 2048 14424 / 2185.
+constexpr int chunk_min_columns(int D) { return D == 256 ? 40 : D == 64 ? 32 : 64; }
 // Query columns per KV head above which the query-tile kernel takes two 128-row tiles per
 // CTA (head size 128).
 constexpr int kChunkTwoTileColumns = 128;

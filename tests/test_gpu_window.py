@@ -74,7 +74,8 @@ def test_columns(cache, dtype, D, G, W, K):
 
 
 @pytest.mark.parametrize("W,K", [(1, 0), (1, 20), (16, 16), (63, 1), (64, 64), (100, 4), (130, 70), (300, 0), (700, 200), (5, 300)])
-@pytest.mark.parametrize("dtype,D,G", [(BF, 64, 4), (F16, 64, 8), (BF, 128, 4), (F16, 128, 8), (BF, 128, 1), (BF, 128, 3)])
+@pytest.mark.parametrize("dtype,D,G", [(BF, 64, 4), (F16, 64, 8), (BF, 128, 4), (F16, 128, 8), (BF, 128, 1), (BF, 128, 3), (BF, 256, 4), (F16, 256, 1),
+                                       (F16, 256, 12)])
 def test_chunks(dtype, D, G, W, K):
     """Long chunks on the query-tile kernel: one and two tiles a CTA, chunks that end inside a tile, sequences
     without history, and of a single new token."""
@@ -91,7 +92,7 @@ def test_chunks(dtype, D, G, W, K):
         assert pa.pa_check_device_error(g.err) == (0, 0)
 
 
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_chunks_alibi_and_nhd(D):
     Hkv, G = 2, 4
     c = wc.make([300, 170, 600], Hkv * G, Hkv, D, 90, 20, BF, nq=[64, 170, 129], seed=8, alibi=np.linspace(0.01, 0.3, Hkv * G),
@@ -148,9 +149,9 @@ def test_bad_blocks_and_lengths(nq):
             wc.check(wc.run(c, g2, part), want)
 
 
-@pytest.mark.parametrize("nq", [None, [70, 64, 65], [200, 130, 1]])
-def test_a_wait_that_gives_up(nq):
-    c = wc.make([400, 300, 350], 8, 2, 128, 100, 4, BF, nq=nq, seed=4)
+@pytest.mark.parametrize("nq,D", [(None, 128), ([70, 64, 65], 128), ([200, 130, 1], 128), ([70, 64, 65], 256), ([200, 130, 1], 64)])
+def test_a_wait_that_gives_up(nq, D):
+    c = wc.make([400, 300, 350], 8, 2, D, 100, 4, BF, nq=nq, seed=4)
     g = wc.on_gpu(c)
     out = wc.run(c, g, 0, first_wait_limit=-1)
     assert pa.pa_check_device_error(g.err) == (-8, pa.PA_DEVERR_WAIT_TIMEOUT)

@@ -108,7 +108,7 @@ def on_gpu(c):
     g.stride = 0 if c.k_scale.ndim == 0 else 1
     g.alibi = None if c.alibi is None else torch.from_numpy(c.alibi).cuda()
     g.err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    g.ws = torch.zeros(128 << 20, dtype=torch.uint8, device="cuda")
+    g.ws = torch.zeros(320 << 20, dtype=torch.uint8, device="cuda")
     if c.nq is not None:
         g.starts = torch.from_numpy(np.concatenate([[0], np.cumsum(c.nq)]).astype(np.int32)).cuda()
     return g
