@@ -526,7 +526,10 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  * its sequence in the same call, as in pa_attention_varlen: an infinity or NaN in it reaches them too.
  * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen).
  * pa_attention_window's kernels are pa_attention_varlen's; on 16-bit caches of head size 256, too, chunks of 40
- * or more query columns per KV head run on the query-tile kernel (partition_size 0 or -1).
+ * or more query columns per KV head run on the query-tile kernel (partition_size 0 or -1).  Over E4M3 and 4-bit
+ * caches, calls of 128 or more columns a sequence on average, and of 16384 or more in all KV heads, run there too
+ * where the workspace (the library's, or a caller's of pa_decode_window_workspace_size bytes) holds the pages that
+ * the chunks see as 16-bit ones, up to 1 GiB; the values are exact.  Else they run in columns, without a workspace.
  * Under a window a partition_size counts the visible tokens' pages, so it can be small; 0 chooses whole
  * units or a cluster split (no workspace).  A step's rows are written before (pa_rotary_and_cache,
  * pa_reshape_and_cache): pa_decode_step and pa_decode_accumulate see the whole history.

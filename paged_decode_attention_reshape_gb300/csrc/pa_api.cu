@@ -293,6 +293,41 @@ bool on_query_tiles(int kind, int D, int partition_size, int columns, bool windo
          (partition_size == 0 || partition_size == -1) && columns >= chunk_min_columns(D);
 }
 
+// Long chunks over E4M3 and 4-bit caches under a window: the pages that the chunk sees, bounded by the window and
+// not by the length, are widened into the workspace first and run on the query tiles, where a sequence has
+// this many query columns per KV head on average, the columns' kernels (which widen every page once for 8 columns)
+// had this many work items, and the scratch stays below its limit.  Measured on GB300, 8 KV heads of 4 x 128
+// (4 x 256), columns / widened in us: E4M3, 64 sequences, window 1024: 64 columns 137 / 164 (244 / 372), 96
+// 208 / 170 (371 / 383), 128 275 / 171 (490 / 388), 256 543 / 208 (973 / 567), 2048 4100 / 740.  With few items
+// a query tile's walk over the window lasts longer than all the columns' (window 4096, 128 columns: 1024 items
+// 105 / 174 (178 / 262), 2048 items 179 / 209 (313 / 325); 256 columns: 2048 183 / 132 (315 / 264)).  4-bit pages
+// gain more (64 sequences, 128 columns: 296 / 160 (420 / 362); 64-wide heads 246 / 82).
+constexpr int kWidenColumns = 128;
+constexpr int kWidenItems = 2048;
+constexpr int64_t kWidenBytes = 1ll << 30;
+struct WidenPlan {
+  int pages;       // of a sequence, 0: not this way
+  size_t table, total;  // bytes of one cache's pages (K's, V's behind, then the table), bytes in all
+};
+// (rows: the query rows of all sequences, columns: those of the longest chunk)
+WidenPlan widen_plan(int S, int Hkv, int D, int maxNB, int kind, int partition_size, int columns, int nq, int64_t rows,
+                     int64_t window, int64_t sinks) {
+  WidenPlan w{0, 0, 0};
+  const int64_t all = std::min(rows, static_cast<int64_t>(S) * nq) * (columns / std::max(nq, 1));  // columns per KV head
+  if (!(mma_fp8(kind) || mma_fp4(kind)) || window <= 0 || nq < 2 ||
+      all < static_cast<int64_t>(S) * kWidenColumns || all * Hkv < kWidenItems * 8 ||
+      !on_query_tiles(KIND_BF16, D, partition_size, columns, true))
+    return w;
+  const int64_t pages = std::min<int64_t>(maxNB, (window + nq - 1 + kBlock - 2) / kBlock + 1 + (sinks + kBlock - 1) / kBlock);
+  const int64_t one = static_cast<int64_t>(S) * pages * Hkv * kBlock * D * 2;
+  const int64_t total = 2 * one + static_cast<int64_t>(S) * maxNB * 4;
+  if (total > kWidenBytes || pages > INT32_MAX / std::max(S, 1)) return w;
+  w.pages = static_cast<int>(pages);
+  w.table = static_cast<size_t>(2 * one);
+  w.total = static_cast<size_t>(total);
+  return w;
+}
+
 // Under a window: the most pages that a work item of the decode kernels reads (its numbers of Window),
 // for 8 columns of G heads a query and at most nq queries.  Windows and first tokens as given by the caller.
 int window_blocks(int maxNB, int64_t window, int64_t sinks, int G, int nq) {
@@ -967,6 +1002,10 @@ PA_API size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int n
   if (sm <= 0) return 0;
   const int Hqv = num_heads * max_query_len;
   const bool whole = static_cast<int64_t>(window) + sinks >= static_cast<int64_t>(max_blocks_per_seq) * kBlock;
+  const WidenPlan wide = widen_plan(num_seqs, num_kv_heads, head_size, max_blocks_per_seq, kind, partition_size,
+                                    Hqv / num_kv_heads, max_query_len,
+                                    static_cast<int64_t>(num_seqs) * max_query_len, whole ? 0 : window, sinks);
+  if (wide.pages > 0) return arrival_counter_bytes(num_seqs, Hqv, num_kv_heads) + wide.total;
   if (max_query_len > 1 && on_query_tiles(kind, head_size, partition_size, Hqv / num_kv_heads, !whole)) return 0;
   size_t need = 0;
   for (const bool varlen : {false, true}) {  // (a call of pa_attention_window may have one query each, too)
@@ -1096,7 +1135,22 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   const int NBw = window > 0 ? window_blocks(maxNB, window, sinks, Hq / Hkv, varlen ? max_query_len : 1) : maxNB;
   const int sm = device_sm_count();
   if (sm <= 0) return PA_ERR_CUDA;
-  const bool chunk = varlen && on_query_tiles(kind, D, partition_size, VH, window > 0);
+  bool chunk = varlen && on_query_tiles(kind, D, partition_size, VH, window > 0);
+  // over a quantised cache: its seen pages widened first, where there is room for them
+  const WidenPlan wide = varlen ? widen_plan(S, Hkv, D, maxNB, kind, partition_size, VH, max_query_len, q->shape[0],
+                                             window, sinks)
+                                : WidenPlan{0, 0, 0};
+  char *scratch = nullptr;
+  if (wide.pages > 0 && !dry) {
+    if (internal_ws) {
+      DevWorkspace w;
+      if (internal_workspace(0, wide.total, static_cast<cudaStream_t>(stream), &w) == PA_OK)
+        scratch = static_cast<char *>(w.ptr) + w.counters;
+    } else if (workspace && aligned16(workspace) && workspace_bytes >= arrival_counter_bytes(S, Hqv, Hkv) + wide.total) {
+      scratch = static_cast<char *>(workspace) + arrival_counter_bytes(S, Hqv, Hkv);  // (the counters stay at zero)
+    }
+    chunk = scratch != nullptr;
+  }
   const Plan pl = window > 0 ? make_window_plan(S, Hqv, Hkv, D, NBw, kind, sm, true, chunk ? -1 : partition_size, varlen,
                                                 !varlen && !o.alibi_slopes)
                              : make_plan(S, Hqv, Hkv, D, maxNB, kind, sm, true, chunk ? -1 : partition_size, varlen,
@@ -1211,6 +1265,62 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
   }
 
   cudaError_t e;
+  int tile_kind = kind;  // of the query tiles
+  if (scratch) {
+    WidenParams w{};
+    const int eb = elem_bytes(k_cache->dtype);
+    const bool paged4 = mma_fp4(kind);
+    w.k_cache = static_cast<const char *>(k_cache->data);
+    w.v_cache = static_cast<const char *>(v_cache->data);
+    w.kc_s0 = k_cache->stride[0] * eb;
+    w.kc_s1 = k_cache->stride[1] * eb;
+    w.kc_s2 = paged4 ? 0 : k_cache->stride[2] * eb;
+    w.vc_s0 = v_cache->stride[0] * eb;
+    w.vc_s1 = v_cache->stride[1] * eb;
+    w.vc_s2 = paged4 ? 0 : v_cache->stride[2] * eb;
+    w.block_table = p.block_table;
+    w.bt_ss = p.bt_ss;
+    w.seq_lens = p.seq_lens;
+    w.qsl = p.qsl;
+    w.Tq = p.Tq;
+    w.S = S;
+    w.Hkv = Hkv;
+    w.D = D;
+    w.num_blocks = NB;
+    w.max_blocks = maxNB;
+    w.nq_max = p.nq_max;
+    w.window = p.window;
+    w.sinks = p.sinks;
+    w.pages = wide.pages;
+    w.k_out = scratch;
+    w.v_out = scratch + wide.table / 2;
+    w.table = reinterpret_cast<int32_t *>(scratch + wide.table);
+    w.err = device_error;
+    w.wide = (reinterpret_cast<uintptr_t>(scratch) & 31u) == 0;  // (each cache's pages are a multiple of 2 KiB)
+    pa_tensor pages{};
+    pages.dtype = q->dtype;
+    pages.ndim = 4;
+    const int64_t extents[4] = {static_cast<int64_t>(S) * wide.pages, Hkv, kBlock, D};
+    int64_t step = 1;
+    for (int i = 3; i >= 0; --i) {
+      pages.shape[i] = extents[i];
+      pages.stride[i] = step;
+      step *= extents[i];
+    }
+    pages.data = w.k_out;
+    if ((r = make_cache_map(&pages, &tmK, &p.nhd))) return r;
+    pages.data = w.v_out;
+    if ((r = make_cache_map(&pages, &tmV, &p.nhd))) return r;
+    {
+      ProfScope ps(PA_KERNEL_DECODE, st);
+      e = launch_widen(w, k_cache->dtype, q->dtype, st);
+    }
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    p.block_table = w.table;
+    p.bt_ss = maxNB;
+    p.num_blocks = S * wide.pages;
+    tile_kind = q->dtype == PA_BF16 ? KIND_BF16 : KIND_F16;
+  }
   if (kind == KIND_F32) {
     p.kc = static_cast<const float *>(k_cache->data);
     p.vc = static_cast<const float *>(v_cache->data);
@@ -1222,7 +1332,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     p.vc_s2 = v_cache->stride[2];
     ProfScope ps(PA_KERNEL_DECODE, st);
     e = launch_decode_f32(p, st);
-  } else if (mma_fp4(kind)) {
+  } else if (mma_fp4(kind) && !scratch) {
     p.k4 = static_cast<const char *>(k_cache->data);
     p.v4 = static_cast<const char *>(v_cache->data);
     p.kc_s0 = k_cache->stride[0];
@@ -1238,7 +1348,7 @@ int decode_impl(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, co
     if (chunk) {
       CUtensorMap tmQ{};
       p.q_tma = make_q_map(q, p.G, &tmQ) == PA_OK ? 1 : 0;
-      e = p.window > 0 ? launch_chunk_window(p, kind, tmK, tmV, tmQ, st) : launch_chunk_umma(p, kind, tmK, tmV, tmQ, st);
+      e = p.window > 0 ? launch_chunk_window(p, tile_kind, tmK, tmV, tmQ, st) : launch_chunk_umma(p, kind, tmK, tmV, tmQ, st);
     } else if (kind == KIND_BF16 || kind == KIND_F16) {
       e = p.window > 0 ? launch_decode_window_16(p, kind, tmK, tmV, st) : launch_decode_mma_16(p, kind, tmK, tmV, st);
     } else {

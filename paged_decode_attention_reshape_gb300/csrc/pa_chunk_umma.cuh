@@ -472,6 +472,16 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     // ------------------------------------------------------------ softmax (row = tid)
     const int pos = valid ? pos0 + row / G : -1;
     const float ab = (p.alibi && valid) ? __ldg(p.alibi + g * G + row % G) * 1.4426950408889634f : 0.f;
+    // the softmax scale in log2 units; over a widened cache times its KV head's K scale
+    auto scale = [&] {
+      if constexpr (WIN) return p.k_scale ? p.scale_log2 * __ldg(p.k_scale + g * p.scale_stride) : p.scale_log2;
+      else return 0.f;
+    };
+    const float win_scale = scale();
+    auto scale_log2 = [&] {
+      if constexpr (WIN) return win_scale;
+      else return p.scale_log2;
+    };
     float m = kUmmaEmpty;
     // WIN, one tile a CTA: groups that every row of the warp sees in full, k < first_whole and from_whole <= k <
     // to_whole, worked out once, and masks of 16 bits a page (64 x 256..512 new tokens, 32/8 heads of 64, window
@@ -518,11 +528,13 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
       const float base = ab * static_cast<float>(t0 - pos);  // ALiBi bias of token t0
       // raw: the scores stay unscaled (scale > 0 keeps their order) and the scale is folded
       // into the exponent below; otherwise x holds the biased / masked log2 logits
-      const bool raw = whole && !p.alibi;
+      bool scaled = p.alibi != nullptr;  // (a K scale may have any sign)
+      if constexpr (WIN) scaled = scaled || !(scale_log2() > 0.f);
+      const bool raw = whole && !scaled;
       if (whole) {
-        if (p.alibi) {
+        if (scaled) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base));
+          for (int i = 0; i < 64; ++i) x[i] = fmaf(x[i], scale_log2(), fmaf(ab, static_cast<float>(i), base));
         }
       } else {
         if constexpr (BITS) {
@@ -533,14 +545,14 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
             const uint32_t seen = j < group_pages(k) ? Window::below(pos + 1 - at) & ~old : 0u;
 #pragma unroll
             for (int i = kBlock * j; i < kBlock * j + kBlock; ++i)
-              x[i] = (seen >> (i % kBlock)) & 1u ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base)) : -INFINITY;
+              x[i] = (seen >> (i % kBlock)) & 1u ? fmaf(x[i], scale_log2(), fmaf(ab, static_cast<float>(i), base)) : -INFINITY;
           }
         } else {
           const int lim = WIN ? min(pos - t0, group_pages(k) * kBlock - 1) : pos - t0;  // tokens i <= lim are visible
           const int lo = WIN ? pos - p.window - t0 : -1, hi = WIN ? p.sinks - t0 : 0;  // and, of those, i > lo and i < hi
 #pragma unroll
           for (int i = 0; i < 64; ++i)
-            x[i] = i <= lim && (!WIN || i > lo || i < hi) ? fmaf(x[i], p.scale_log2, fmaf(ab, static_cast<float>(i), base))
+            x[i] = i <= lim && (!WIN || i > lo || i < hi) ? fmaf(x[i], scale_log2(), fmaf(ab, static_cast<float>(i), base))
                                                           : -INFINITY;
         }
       }
@@ -554,9 +566,9 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
 #pragma unroll
         for (int i = 0; i < 7; ++i) b[i] = fmax3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
         b[7] = a[21];
-        lm = fmax3(fmax3(b[0], b[1], b[2]), fmax3(b[3], b[4], b[5]), fmaxf(b[6], b[7])) * (raw ? p.scale_log2 : 1.f);
+        lm = fmax3(fmax3(b[0], b[1], b[2]), fmax3(b[3], b[4], b[5]), fmaxf(b[6], b[7])) * (raw ? scale_log2() : 1.f);
       }
-      const float sc = raw ? p.scale_log2 : 1.f;  // p = exp2(x sc - m)
+      const float sc = raw ? scale_log2() : 1.f;  // p = exp2(x sc - m)
       const bool need = lm > m + kUmmaSlack;
       const float mn = need ? lm : m;
       // P.V of the previous group must have completed before O is rescaled.  The wait is
@@ -675,7 +687,10 @@ __global__ void __launch_bounds__(UmmaCfg<KIND, D, T>::THREADS, UmmaCfg<KIND, D,
     if (ok && __all_sync(0xffffffffu, umma_wait(odone(tile), (ngr - 1) & 1, abort))) {
       umma::fence_after();
       const int rr = tid & 127;  // this thread's row within the tile
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      float inv = l > 0.f ? 1.f / l : 0.f;
+      if constexpr (WIN) {
+        if (p.v_scale) inv *= __ldg(p.v_scale + g * p.scale_stride);
+      }
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float o[32];

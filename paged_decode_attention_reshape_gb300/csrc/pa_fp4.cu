@@ -216,6 +216,42 @@ __global__ void __launch_bounds__(256, kGatherCtas) gather_kernel(const GatherPa
   }
 }
 
+// A CTA per (page number, sequence): every head's page of K and V, a group of 16 elements a thread.  Codes
+// (4-bit: times their group's scale, 6 bits) are 16-bit numbers exactly; the heads' scales go into the
+// attention's own.  Bound by the bytes, a third read and the rest written (to L2 for the most part).
+template <int CT, int OT>
+__global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int v = blockIdx.x, s = blockIdx.y;
+  const int len = __ldg(p.seq_lens + s), a = __ldg(p.qsl + s), b = __ldg(p.qsl + s + 1), nq = b - a;
+  // (sequences that the attention refuses, and those without a query)
+  if (len < 0 || len > p.max_blocks * kBlock || a < 0 || b > p.Tq || nq <= 0 || nq > p.nq_max || nq > len) return;
+  const Window win = make_window(p.window, p.sinks, len - nq);
+  if (v >= (len + kBlock - 1) / kBlock - win.skip || v >= p.pages) return;
+  const int page = win.page(v);
+  const int blk = __ldg(p.block_table + s * p.bt_ss + page);
+  const bool bad = blk < 0 || blk >= p.num_blocks;
+  if (threadIdx.x == 0) {
+    p.table[static_cast<int64_t>(s) * p.max_blocks + page] = bad ? -1 : s * p.pages + v;
+    if (bad && p.err) atomicOr(p.err, kErrBlock);
+  }
+  if (bad) return;
+  const int groups = p.D / 16, per = p.Hkv * kBlock * groups;  // groups of a block of K
+  char *const out0 = p.k_out + static_cast<int64_t>(s * static_cast<int64_t>(p.pages) + v) * per * 32;
+  char *const out1 = p.v_out + static_cast<int64_t>(s * static_cast<int64_t>(p.pages) + v) * per * 32;
+  for (int i = threadIdx.x; i < 2 * per; i += 256) {
+    const bool second = i >= per;
+    const int j = second ? i - per : i, gi = j % groups, t = j / groups % kBlock, h = j / groups / kBlock;
+    const char *src = second ? p.v_cache + blk * p.vc_s0 + h * p.vc_s1 + t * p.vc_s2
+                             : p.k_cache + blk * p.kc_s0 + h * p.kc_s1 + t * p.kc_s2;
+    Cached<CT> c;
+    c.load(src, p.D, t, gi);
+    float x[16];
+    c.values(1.f, x);
+    store_group<OT>((second ? out1 : out0) + static_cast<int64_t>(j) * 32, p.wide, x);
+  }
+}
+
 // Blocks of 256 threads or fewer: groups of a row, heads, tokens; at most `most` of them (0: any).
 template <auto kern, typename P>
 cudaError_t launch_tokens(const P &p, int64_t most, cudaStream_t st) {
@@ -276,6 +312,19 @@ cudaError_t launch_gather(const GatherParams &p, int cache_dtype, int out_dtype,
     case PA_F16: return launch_gather_one<PA_F16, PA_F16>(p, sm_count, st);
     default: return cudaErrorInvalidValue;
   }
+}
+
+cudaError_t launch_widen(const WidenParams &p, int cache_dtype, int out_dtype, cudaStream_t st) {
+  const dim3 grid(p.pages, p.S), block(256);
+  const bool fp4 = cache_dtype == PA_FP4_E2M1;
+  cudaError_t e;
+  if (out_dtype == PA_BF16)
+    e = fp4 ? launch_pdl(widen_kernel<PA_FP4_E2M1, PA_BF16>, grid, block, 0, st, 1, p)
+            : launch_pdl(widen_kernel<PA_FP8_E4M3, PA_BF16>, grid, block, 0, st, 1, p);
+  else
+    e = fp4 ? launch_pdl(widen_kernel<PA_FP4_E2M1, PA_F16>, grid, block, 0, st, 1, p)
+            : launch_pdl(widen_kernel<PA_FP8_E4M3, PA_F16>, grid, block, 0, st, 1, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace pa

@@ -162,6 +162,22 @@ struct DecodeParams {
   int narrow;  // 1 (one query, no ALiBi, under a window): CTAs of half the warps, twice as many per SM
 };
 
+// The pages that the queries of a chunk see, of an E4M3 or 4-bit cache, as 16-bit pages of their codes' values
+// (pa_fp4.cu): page number v of sequence s (Window of its first query) becomes block s * pages + v of k_out and
+// v_out, [S * pages, Hkv, 16, D], which `table` [S, max_blocks] names at the page's own place.  A bad block
+// becomes entry -1.  Strides of the caches in bytes.
+struct WidenParams {
+  const char *k_cache, *v_cache;
+  int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2;
+  const int32_t *block_table, *seq_lens, *qsl;
+  int64_t bt_ss, Tq;
+  int S, Hkv, D, num_blocks, max_blocks, nq_max, window, sinks, pages;
+  char *k_out, *v_out;
+  int32_t *table;
+  int *err;
+  bool wide;  // k_out and v_out are 32-byte aligned (else 16)
+};
+
 // The pages that a work item under a window reads, numbered without the gap between the first tokens'
 // pages and the window's: every split cuts these numbers.  `start` is the first token inside the window of
 // the item's first query (of all its queries the earliest); tokens of [sinks, start) are seen by none.
@@ -285,6 +301,7 @@ cudaError_t launch_decode_mma_16(const DecodeParams &p, int kind, const CUtensor
 cudaError_t launch_decode_mma_fp8(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   cudaStream_t st);  // KIND_FP8_*
 cudaError_t launch_decode_mma_fp4(const DecodeParams &p, int kind, cudaStream_t st);  // KIND_FP4_*
+cudaError_t launch_widen(const WidenParams &p, int cache_dtype, int out_dtype, cudaStream_t st);
 // The same kernels under a window (p.window > 0).
 cudaError_t launch_decode_window_16(const DecodeParams &p, int kind, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                     cudaStream_t st);

@@ -219,3 +219,117 @@ def test_calls_of_different_shapes_follow_each_other():
             pa.pa_decode_opt(gf.out, gf.q, gf.k_cache, gf.v_cache, gf.block_table, gf.seq_lens, full.scale, 2, partition_size=32)
             wc.check(gf.out, wc.reference(full))
 
+
+QUANT = [("e4m3", BF, 128, 4), ("e4m3", F16, 256, 8), ("fp4", BF, 64, 8), ("fp4", F16, 128, 4), ("fp4", BF, 256, 2)]
+CHUNK = ([130, 500, 300, 77, 900, 777, 101], [130, 1, 64, 0, 33, 200, 101])
+
+
+def chunk_workspace(c, part=0):
+    code = pa.PA_FP8_E4M3 if c.cache == "e4m3" else pa.PA_FP4_E2M1
+    return pa.pa_decode_window_workspace_size(c.S, c.Hq, c.Hkv, c.D, c.width, code, c.W, c.K, max(c.nq), part)
+
+
+@pytest.mark.parametrize("W,K", [(1, 0), (1, 20), (16, 16), (100, 4), (130, 70), (700, 200), (5, 300)])
+@pytest.mark.parametrize("cache,dtype,D,G", QUANT)
+def test_chunks_of_quantised_caches(cache, dtype, D, G, W, K):
+    """Long chunks over E4M3 and 4-bit caches: widened into the library's workspace or the caller's (at 16 bytes off
+    a 32-byte border too, which leaves the arrival counters at zero), and in columns where there is no room."""
+    Hkv = 32 // G
+    lens, news = CHUNK
+    c = wc.make(lens, 32, Hkv, D, W, K, dtype, cache, nq=news, seed=W + K, extra_rows=3, **scales(cache, Hkv))
+    g, want = wc.on_gpu(c), wc.reference(c)
+    n = sum(news)
+    want = want[0][:n], want[1][:n]
+    need = chunk_workspace(c)
+    assert need > 0 and chunk_workspace(c, -1) == need
+    big = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
+    for what, ws in (("library", None), ("exact", big[:need]), ("off by 16", big[16:]), ("columns", big[:need - 1])):
+        if ws is not None:
+            big.zero_()
+            g.ws = ws
+        for part in (0, -1):
+            out = wc.run(c, g, part, ws=ws is not None)
+            assert bool(torch.isnan(out[n:]).all())
+            wc.check(out[:n], want, "%s, partition %d" % (what, part))
+            assert pa.pa_check_device_error(g.err) == (0, 0)
+        if ws is not None:
+            counters = (c.S * Hkv * ((G * max(news) + 7) // 8) * 4 + 255) // 256 * 256
+            assert not ws[:counters].any()
+    wc.check(wc.run(c, g, 128, ws=False)[:n], want, "a split asked for")
+
+
+@pytest.mark.parametrize("cache,dtype,D,G", QUANT)
+def test_quantised_chunks_with_bias_layout_signs_and_bad_blocks(cache, dtype, D, G):
+    Hkv = 32 // G
+    lens, news = [300, 250, 600], [64, 250, 200]
+    sc = dict(k_scale=np.resize([0.05, -0.03], Hkv), v_scale=np.resize([-0.07, 0.02, 0.06], Hkv))  # of both signs
+    c = wc.make(lens, 32, Hkv, D, 90, 20, dtype, cache, nq=news, seed=8, alibi=np.linspace(0.01, 0.3, 32),
+                nhd=cache == "e4m3", **sc)
+    g = wc.on_gpu(c)
+    wc.check(wc.run(c, g, ws=False), wc.reference(c), "ALiBi")
+    c = wc.make(lens, 32, Hkv, D, 90, 20, dtype, cache, nq=news, seed=9, nhd=cache == "e4m3", **sc)
+    g, want = wc.on_gpu(c), wc.reference(c)
+    wc.check(wc.run(c, g, ws=False), want, "signs")
+    g.block_table[1, 5] = c.NB
+    out = wc.run(c, g, ws=False)
+    assert pa.pa_check_device_error(g.err) == (-6, pa.PA_DEVERR_BLOCK_RANGE)
+    assert bool(torch.isnan(out[64:314]).any())  # (its row tiles that see the page write nothing)
+    for a, b in ((0, 64), (314, 514)):
+        wc.check(out[a:b], (want[0][a:b], want[1][a:b]))
+    g = wc.on_gpu(c)
+    g.seq_lens[2] = -1
+    out = wc.run(c, g, ws=False)
+    assert pa.pa_check_device_error(g.err) == (-6, pa.PA_DEVERR_SEQLEN_RANGE)
+    assert bool(torch.isnan(out[314:]).all())
+    wc.check(out[:314], (want[0][:314], want[1][:314]))
+
+
+def test_quantised_chunks_captured():
+    """Captured with the library's workspace, replayed over other rows, tables and lengths, between other calls."""
+    c = wc.make([300, 570], 32, 8, 128, 90, 20, BF, "e4m3", nq=[200, 320], seed=1, k_scale=0.05, v_scale=0.07)
+    later = wc.make([303, 576], 32, 8, 128, 90, 20, BF, "e4m3", nq=[200, 320], seed=2, k_scale=0.05, v_scale=0.07)
+    other = wc.make([500] * 6, 32, 4, 128, 200, 0, BF, "fp4", nq=[100] * 6, seed=3)
+    assert (later.NB, later.width) == (c.NB, c.width)
+    g, gl, go = wc.on_gpu(c), wc.on_gpu(later), wc.on_gpu(other)
+    wc.run(c, g, ws=False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wc.run(c, g, ws=False)
+    wc.check(wc.run(other, go, ws=False), wc.reference(other))  # (the workspace grows)
+    for name in ("k_cache", "v_cache", "q", "block_table", "seq_lens"):
+        getattr(g, name).copy_(getattr(gl, name))
+    graph.replay()
+    torch.cuda.synchronize()
+    wc.check(g.out, wc.reference(later))
+    wc.check(wc.run(other, go, ws=False), wc.reference(other))
+
+
+def test_workspace_of_long_chunks_over_quantised_caches():
+    """The size covers every call of at most max_query_len queries a sequence, and bounds itself."""
+    size = lambda *a: pa.pa_decode_window_workspace_size(*a)
+    for code in (pa.PA_FP8_E4M3, pa.PA_FP4_E2M1):
+        a = size(64, 32, 8, 128, 512, code, 1024, 4, 512, 0)
+        pages = (1024 + 511 + 14) // 16 + 1 + 1
+        counters = (64 * 8 * (4 * 512 // 8) * 4 + 255) // 256 * 256
+        assert a == counters + 2 * 64 * pages * 8 * 16 * 128 * 2 + 64 * 512 * 4
+        assert size(64, 32, 8, 128, 512, code, 1024, 4, 512, -1) == a
+        assert size(64, 32, 8, 128, 512, code, 1024, 4, 256, 0) < a
+        assert size(256, 32, 8, 128, 4096, code, 8192, 4, 512, 0) < 1 << 28  # (past the limit: columns)
+    assert size(64, 32, 8, 128, 512, pa.PA_BF16, 1024, 4, 512, 0) == 0
+
+
+@pytest.mark.parametrize("cache,dtype,D,G", QUANT)
+def test_quantised_chunks_of_padded_and_mixed_batches(cache, dtype, D, G):
+    """A batch of one long chunk and many short ones (columns), and query rows padded far past the last sequence."""
+    Hkv = 32 // G
+    news = [200] + [1] * 30
+    c = wc.make([400] + [150 + 7 * i for i in range(30)], 32, Hkv, D, 60, 17, dtype, cache, nq=news, seed=4,
+                extra_rows=1100, **scales(cache, Hkv))
+    g, want = wc.on_gpu(c), wc.reference(c)
+    out = wc.run(c, g, ws=False)
+    n = sum(news)
+    wc.check(out[:n], (want[0][:n], want[1][:n]))
+    assert bool(torch.isnan(out[n:]).all())
+    c = wc.make([400] + [150 + 7 * i for i in range(30)], 32, Hkv, D, 60, 17, dtype, cache, nq=news, seed=4,
+                **scales(cache, Hkv))
+    wc.check(wc.run(c, wc.on_gpu(c), ws=False), wc.reference(c))
