@@ -1494,10 +1494,12 @@ PA_API int pa_decode_step(pa_tensor *out, const pa_tensor *q, const pa_tensor *k
   // they help, and the early variant's in-loop wait costs more (c2: 33.3 vs 33.5 us).  With
   // early reads the write takes two CTAs per SM, leaving the decode's CTAs room beside it
   // (same step, graph replay: 4 / 3 / 2 / 1 write CTAs per SM 195.5 / 192.7 / 191.0 / 194.9 us).
-  const int write_ctas = new_rows_start ? 2 : 0;
+  // Without a row there is no write to wait for, and what runs before may have let its dependents start.
+  const bool early = new_rows_start && key->shape[0] > 0;
+  const int write_ctas = early ? 2 : 0;
   if ((r = write_impl(key, value, k_cache, v_cache, slot_mapping, kv, &wo, stream, write_ctas))) return r;
   return decode_impl(out, q, k_cache, v_cache, block_table, seq_lens, scale, num_kv_heads, o, internal, stream,
-                     nullptr, 1, new_rows_start, new_rows_start != nullptr);
+                     nullptr, 1, new_rows_start, early);
 }
 
 PA_API int pa_check_device_error(int *device_error, int *bits_out, pa_stream_t stream) {

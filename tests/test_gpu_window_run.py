@@ -185,3 +185,34 @@ def test_blocks_past_4_gib(kind, nhd):
             starts = torch.from_numpy(np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)).to(DEV)
             pa.pa_attention_window(out, q[rows].contiguous(), *caches, starts, bt, sl, c.scale, Hkv, max(nq), W, K, **kv)
         wc.check(out, wc.reference(c), "new tokens %s" % nq)
+
+
+@pytest.mark.parametrize("rows", [0, 3])
+def test_rotation_right_before_a_step(rows):
+    """Queries rotated in place by a long kernel and read by the step right behind it, which starts early where it
+    writes rows and may not where it has none to write."""
+    S, Hq, Hkv, D, T = 3, 8, 2, 128, 40000
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(T, Hq, D, device=DEV, generator=gen).to(torch.bfloat16)
+    pos = torch.arange(T, device=DEV)
+    freq = pa.pa_rotary_frequencies(D).to(DEV)
+    kc, vc = [torch.randn(30, Hkv, 16, D, device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2)]
+    table = torch.arange(30, dtype=torch.int32, device=DEV).view(3, 10)
+    lens = torch.tensor([150, 7, 90], dtype=torch.int32, device=DEV)
+    key, value = [torch.randn(rows, Hkv, D, device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2)]
+    slots = torch.tensor([149, 160 + 6, 320 + 89], device=DEV)[:rows]
+    starts = torch.tensor([0, 1, 2, 3] if rows else [0] * 4, dtype=torch.int32, device=DEV)
+    rotated, want, got = x.clone(), torch.empty(S, Hq, D, dtype=x.dtype, device=DEV), torch.empty_like(x[:S])
+    ks, vs = kc.clone(), vc.clone()
+    pa.pa_rotary(rotated, rotated, None, None, pos, freq)
+    torch.cuda.synchronize()
+    if rows:
+        pa.pa_reshape_and_cache(key, value, ks, vs, slots)
+    pa.pa_decode_opt(want, rotated[T - S:], ks, vs, table, lens, D ** -0.5, Hkv, partition_size=-1)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        now = x.clone()
+        pa.pa_rotary(now, now, None, None, pos, freq)
+        pa.pa_decode_step(got, now[T - S:], key, value, kc, vc, slots, table, lens, D ** -0.5, Hkv, new_rows_start=starts,
+                          partition_size=-1)
+        assert torch.equal(got, want)
