@@ -175,9 +175,10 @@ def lib() -> ctypes.CDLL:
             L.pa_profile_read.restype = i32
             L.pa_profile_read.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]
             try:
-                from ._marshal import describe
-                _describe = describe
-            except ImportError:  # (not built, or for another torch: the Python form says the same)
+                from . import _marshal
+                if _marshal.torch == torch.__version__:
+                    _describe = _marshal.describe
+            except (ImportError, AttributeError):  # (not built, or for another torch: the Python form says the same)
                 pass
             _lib = L
     return _lib

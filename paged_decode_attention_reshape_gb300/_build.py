@@ -61,7 +61,7 @@ def _build_marshal() -> None:
     base = os.path.dirname(torch.__file__)
     tmp = MARSHAL + ".%d.tmp" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), '-DPA_TORCH="%s"' % torch.__version__,
            "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
            "-lc10", "-ltorch_cpu", "-ltorch_python"]

@@ -91,4 +91,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit__marshal(void) { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit__marshal(void) {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch", PA_TORCH) < 0) {  // whose tensors it reads
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

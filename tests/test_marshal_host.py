@@ -46,3 +46,10 @@ def test_refusals(native):
     for args in ((), (b"tt", torch.zeros(1)), ("t", torch.zeros(1))):
         with pytest.raises(TypeError):
             native(*args)
+
+
+def test_for_this_torch(native):
+    from paged_decode_attention_reshape_gb300 import _marshal
+    assert _marshal.torch == torch.__version__
+    pa.lib()
+    assert pa._describe is native
