@@ -531,7 +531,7 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  * where the workspace (the library's, or a caller's of pa_decode_window_workspace_size bytes) holds the pages that
  * the chunks see as 16-bit ones, up to 1 GiB; the values are exact.  Else they run in columns, without a workspace.
  * Under a window a partition_size counts the visible tokens' pages, so it can be small; 0 chooses whole
- * units or a cluster split (no workspace).  A step's rows are written before (pa_rotary_and_cache,
+ * units or a cluster split (no workspace but for widened pages).  A step's rows are written before (pa_rotary_and_cache,
  * pa_reshape_and_cache): pa_decode_step and pa_decode_accumulate see the whole history.
  */
 int pa_decode_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_cache, const pa_tensor *v_cache,
@@ -725,8 +725,9 @@ const char *pa_status_string(int status);
  * synchronises on the recorded events, returns the summed device time (ms) and
  * the launch count for one kernel kind since the last read, and clears them.
  *   kind: 0 = cache write, 1 = decode (attention with the fused split-KV merge; the second
- *   kernel of pa_decode_accumulate counts here too); pa_rotary_and_cache counts as a cache
- *   write.  pa_rotary, pa_gather_cache, pa_evict and pa_copy_blocks are not bracketed.
+ *   kernel of pa_decode_accumulate and the widening of pages in pa_attention_window count here
+ *   too); pa_rotary_and_cache counts as a cache write.  pa_rotary, pa_gather_cache, pa_evict and
+ *   pa_copy_blocks are not bracketed.
  */
 #define PA_KERNEL_WRITE 0
 #define PA_KERNEL_DECODE 1

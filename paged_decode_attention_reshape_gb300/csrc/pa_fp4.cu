@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(256, kGatherCtas) gather_kernel(const GatherPa
 
 // A CTA per (page number, sequence): every head's page of K and V, a group of 16 elements a thread.  Codes
 // (4-bit: times their group's scale, 6 bits) are 16-bit numbers exactly; the heads' scales go into the
-// attention's own.  Bound by the bytes, a third read and the rest written (to L2 for the most part).
+// attention's own.  Bound by the bytes, a third read and the rest written: 16 chunks of 256..512 tokens, window
+// 1024, 8 heads of 128, E4M3: 23 us for 132 MB, 5.7 TB/s (the attention behind it 188 us).
 template <int CT, int OT>
 __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
