@@ -307,7 +307,7 @@ constexpr int kWidenItems = 2048;
 constexpr int64_t kWidenBytes = 1ll << 30;
 struct WidenPlan {
   int pages;       // of a sequence, 0: not this way
-  size_t table, total;  // bytes of one cache's pages (K's, V's behind, then the table), bytes in all
+  size_t table, total;  // bytes of both caches' pages (K's, V's, then the block table), bytes in all
 };
 // (rows: the query rows of all sequences, columns: those of the longest chunk)
 WidenPlan widen_plan(int S, int Hkv, int D, int maxNB, int kind, int partition_size, int columns, int nq, int64_t rows,
@@ -319,9 +319,10 @@ WidenPlan widen_plan(int S, int Hkv, int D, int maxNB, int kind, int partition_s
       !on_query_tiles(KIND_BF16, D, partition_size, columns, true))
     return w;
   const int64_t pages = std::min<int64_t>(maxNB, (window + nq - 1 + kBlock - 2) / kBlock + 1 + (sinks + kBlock - 1) / kBlock);
-  const int64_t one = static_cast<int64_t>(S) * pages * Hkv * kBlock * D * 2;
-  const int64_t total = 2 * one + static_cast<int64_t>(S) * maxNB * 4;
-  if (total > kWidenBytes || pages > INT32_MAX / std::max(S, 1)) return w;
+  const int64_t page_bytes = static_cast<int64_t>(Hkv) * kBlock * D * 2;
+  if (pages > kWidenBytes / (2 * page_bytes) / S) return w;  // (S > 0: it has columns)
+  const int64_t one = S * pages * page_bytes, total = 2 * one + static_cast<int64_t>(S) * maxNB * 4;
+  if (total > kWidenBytes) return w;
   w.pages = static_cast<int>(pages);
   w.table = static_cast<size_t>(2 * one);
   w.total = static_cast<size_t>(total);

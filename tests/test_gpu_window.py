@@ -315,6 +315,8 @@ def test_workspace_of_long_chunks_over_quantised_caches():
         assert size(64, 32, 8, 128, 512, code, 1024, 4, 512, -1) == a
         assert size(64, 32, 8, 128, 512, code, 1024, 4, 256, 0) < a
         assert size(256, 32, 8, 128, 4096, code, 8192, 4, 512, 0) < 1 << 28  # (past the limit: columns)
+        for S in (1 << 17, 1 << 30):  # (products past 2^63)
+            assert size(S, 32, 8, 256, 1 << 22, code, 1 << 25, 1 << 24, 512, -1) == 0
     assert size(64, 32, 8, 128, 512, pa.PA_BF16, 1024, 4, 512, 0) == 0
 
 
