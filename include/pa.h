@@ -256,8 +256,9 @@ typedef struct {
  *   q, q_out      [T, Hq, D] and
  *   key, k_out    [T, Hk, D], PA_F32 / PA_BF16 / PA_F16 (one type for all), D = 64, 128 or 256; innermost
  *                 stride 1.  Either pair may be NULL.  An output may be its input's memory with the
- *                 same strides (in place), and may share no other memory with an input or the other
- *                 output (PA_ERR_INVALID_ARG where the strides are the same; else not checked).
+ *                 same strides (in place), and its rows may share no other memory with rows of an
+ *                 input or the other output (PA_ERR_INVALID_ARG, whatever the strides; caches are not
+ *                 compared with q_out).
  *   positions     PA_I64 or PA_I32 [T].
  *   frequencies   PA_I64 [R / 2], R <= D a multiple of 16 (see above); NULL or empty: no rotation, and
  *                 positions (may be NULL) is not read.

@@ -41,22 +41,70 @@ inline bool rows_overlap(const pa_tensor *t, int64_t len) {
   return (n > 1 && a < len) || (m > 1 && b < (n > 1 ? (n - 1) * a : 0) + len);
 }
 
-// Whether a row of one tensor [T, H, D] shares memory with a row of another of the same strides (elements of
-// eb bytes; views of one buffer, like heads side by side, do not).  Tensors of other strides are not looked at.
-inline bool rows_shared(const pa_tensor *a, const pa_tensor *b, int eb) {
-  const int64_t ts = a->stride[0] * eb, hs = a->stride[1] * eb, row = a->shape[2] * eb;
-  if (a->stride[0] != b->stride[0] || a->stride[1] != b->stride[1] || !a->data || !b->data) return false;
-  const int64_t away = static_cast<int64_t>(reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data));
-  auto near = [](int64_t x, int64_t step, int i) { return step > 0 ? x / step + i : 0; };
-  // b's row (0, 0) against a's rows (t, h) around it; t < 0, h < 0: b's rows against a's first
-  for (int i = -1; i <= 1; ++i) {
-    const int64_t t = near(away, ts, i), left = away - t * ts;
-    if (t >= a->shape[0] || -t >= b->shape[0]) continue;
-    for (int j = -1; j <= 1; ++j) {
-      const int64_t h = near(left, hs, j), apart = left - h * hs;
-      if (h < a->shape[1] && -h < b->shape[1] && apart < row && -apart < row) return true;
-    }
+// Whether a row of a tensor x [T, H, D] shares memory with a row of an output [T, H', D] (elements of eb bytes;
+// the output's own rows do not overlap, see rows_overlap).  Views of one buffer, like heads side by side, do not.
+// Equal strides take a few divisions; others a step for each run of x's rows, where the two spans meet at all.
+inline bool rows_shared(const pa_tensor *x, const pa_tensor *out, int eb) {
+  struct Axis {
+    int64_t n, step;  // (step 0: one row, wherever it would go on)
+  };
+  struct Rows {
+    Axis big, small;
+    int64_t row;
+    int64_t span() const { return (big.n - 1) * big.step + (small.n - 1) * small.step + row; }
+  };
+  const int64_t row = x->shape[2] * eb;
+  if (!x->data || !out->data || row < 1) return false;
+  auto rows = [&](const pa_tensor *t) {
+    Rows r{{t->shape[0], t->stride[0] * eb}, {t->shape[1], t->stride[1] * eb}, row};
+    for (Axis *a : {&r.big, &r.small})
+      if (a->n <= 1) a->step = 0;
+    if (r.big.step < r.small.step) std::swap(r.big, r.small);
+    return r;
+  };
+  const Rows a = rows(x), b = rows(out);
+  if (a.big.n < 1 || a.small.n < 1 || b.big.n < 1 || b.small.n < 1) return false;
+  // where x's rows start, seen from the output's first
+  const int64_t away = static_cast<int64_t>(reinterpret_cast<intptr_t>(x->data) - reinterpret_cast<intptr_t>(out->data));
+  if (away >= b.span() || -away >= a.span()) return false;
+  auto floor_div = [](int64_t p, int64_t q) { return p >= 0 ? p / q : -((-p + q - 1) / q); };
+
+  const bool alike = x->stride[0] == out->stride[0] && x->stride[1] == out->stride[1];
+  if (alike && !rows_overlap(x, x->shape[2])) {
+    // Some difference of (t, h) must bring the starts within a row.  Neither tensor's rows overlap, so its heads of
+    // a token (or tokens of a head) end within the larger step, and only the nearest multiples come into question.
+    const bool heads_big = x->stride[1] > x->stride[0];
+    const int big = heads_big ? 1 : 0, small = 1 - big;
+    auto axis = [&](int i, int64_t from, auto &&each) {  // every difference i of that axis near `from` bytes
+      const int64_t n = x->shape[i], m = out->shape[i], step = n > 1 || m > 1 ? x->stride[i] * eb : 0;
+      const int64_t at = step > 0 ? floor_div(from, step) : 0;
+      for (int64_t d = at - 1; d <= at + 2; ++d)  // d = (the output's index) - (x's)
+        if (d < m && -d < n && (step > 0 || d == 0) && each(from - d * step)) return true;
+      return false;
+    };
+    return axis(big, away, [&](int64_t left) {
+      return axis(small, left, [&](int64_t apart) { return apart < row && -apart < row; });
+    });
   }
+
+  // The first row of the output that ends behind `at`: whether it starts before at + len.
+  auto met = [&](int64_t at, int64_t len) {
+    const int64_t block = (b.small.n - 1) * b.small.step + row;
+    int64_t i = b.big.n > 1 ? floor_div(at - block, b.big.step) + 1 : at < block ? 0 : 1;
+    if (i < 0) i = 0;
+    if (i >= b.big.n) return false;
+    const int64_t left = at - i * b.big.step;
+    int64_t j = b.small.n > 1 ? floor_div(left - row, b.small.step) + 1 : 0;
+    if (j < 0) j = 0;
+    return i * b.big.step + j * b.small.step < at + len;
+  };
+  // x's rows in runs: those of the smaller step as one where they lie side by side (or are one and the same)
+  const bool joined = a.small.step <= row;
+  const int64_t run = joined ? (a.small.n - 1) * a.small.step + row : row;
+  const int64_t bigs = a.big.step > 0 ? a.big.n : 1, smalls = joined ? 1 : a.small.n;
+  for (int64_t i = 0; i < bigs; ++i)
+    for (int64_t j = 0; j < smalls; ++j)
+      if (met(away + i * a.big.step + j * a.small.step, run)) return true;
   return false;
 }
 
