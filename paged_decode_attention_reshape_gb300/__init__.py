@@ -247,15 +247,15 @@ def _write_options(k_scale, v_scale, scale_stride, device_error) -> bytes:
 
 
 @functools.lru_cache(maxsize=64)
-def _no_options(partition_size) -> bytes:
+def _no_options(partition_size: int) -> bytes:
     """The options of a call that gives none but its partition size."""
-    return _DECODE_OPTIONS.pack(0, 0, 0, 0, int(partition_size), 0, 0, 0, 0)
+    return _DECODE_OPTIONS.pack(0, 0, 0, 0, partition_size, 0, 0, 0, 0)
 
 
 def _decode_options(k_scale, v_scale, scale_stride, alibi_slopes, partition_size, workspace, device_error,
                     first_wait_limit) -> bytes:
     if k_scale is v_scale is alibi_slopes is workspace is device_error is None and not scale_stride and not first_wait_limit:
-        return _no_options(partition_size)
+        return _no_options(int(partition_size))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return _DECODE_OPTIONS.pack(_addr(k_scale), _addr(v_scale), int(scale_stride), _addr(alibi_slopes),
                                 int(partition_size), _addr(workspace), ws_bytes, _addr(device_error),
