@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(kRotaryWarps * 32, kRotaryCtas<DT>) rotary_ker
           }
         };
         float ms = fmaf(sum_of_squares(), 1.f / D, p.eps);
-        // squares that overflow, or vanish: those rows once more by a power of two
+        // squares that overflow, or vanish: those rows once more by a power of two (2^100: an fp32 row's largest
+        // element is then at most 2^56, its sum 2^120, and the square of the smallest number there is 2^-98)
         if (__any_sync(ALL, !(ms <= 0x1p120f) || ms < 0x1p-96f)) {
-          const float by = ms < 0x1p-96f ? 0x1p64f : ms <= 0x1p120f ? 1.f : 0x1p-70f;
+          const float by = ms < 0x1p-96f ? 0x1p100f : ms <= 0x1p120f ? 1.f : 0x1p-70f;
           times(by);
           ms = fmaf(sum_of_squares(), 1.f / D, p.eps * by * by);
         }
