@@ -65,10 +65,16 @@ def _build_marshal() -> None:
            "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-o", tmp, "-L", os.path.join(base, "lib"),
            "-lc10", "-ltorch_cpu", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stdout + r.stderr if r.returncode != 0 else None
+    except OSError as e:  # no such compiler
+        failed = str(e)
+    if failed is not None:
         open(NO_MARSHAL, "w").close()
-        sys.stderr.write("pa_marshal.cpp was not compiled (calls take longer on the host):\n%s\n" % (r.stdout + r.stderr)[-2000:])
+        if os.path.exists(MARSHAL):  # (of an earlier source: its descriptors may be others)
+            os.remove(MARSHAL)
+        sys.stderr.write("pa_marshal.cpp was not compiled (calls take longer on the host):\n%s\n" % failed[-2000:])
         return
     os.replace(tmp, MARSHAL)
 
