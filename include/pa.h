@@ -216,10 +216,11 @@ int pa_gather_cache(pa_tensor *key, pa_tensor *value, const pa_tensor *k_cache, 
  * the rotated part, at most the head size) turns by the angle position * theta_i:
  *     a' = m (a cos - b sin),  b' = m (b cos + a sin);   elements from R on stay.
  * The frequencies are a device table of int64 [R / 2]: theta_i / (2 pi), turns per position, in units of
- * 2^-64 (whole turns dropped).  The library multiplies positions into it in 64-bit integers, so an angle
- * is exact to a turn's 2^-64 per position, however far the position.  Positions may be negative (the
- * rotation back); a call with the differences of two position lists moves rotated rows from one to the
- * other.
+ * 2^-64 (whole turns dropped).  The library multiplies positions into it in 64-bit integers: the product is
+ * exact, however far the position, so an angle is off by what its table entry is off, times the position.
+ * pa_rotary_frequencies works in fp64: its entries are within 2^-52 of a turn (base and factor at least 1), an
+ * angle within 2^-32 of a turn at 2^20 tokens.  Positions may be negative (the rotation back); a call with the differences of two position lists
+ * moves rotated rows from one to the other.
  */
 typedef enum {
     PA_ROTARY_PLAIN = 0,  /* theta_i = base^(-2 i / R) */
@@ -228,12 +229,15 @@ typedef enum {
                              factor, the fastest stays); R > 2 */
     PA_ROTARY_PARTS = 3   /* by what a pair turns over original_len tokens, n = original_len theta_i / (2 pi):
                              theta_i from n >= high on, theta_i / factor up to n <= low, between them
-                             mixed linearly in n */
+                             mixed linearly in n.  Rules that mix linearly in the pair's index i, between the
+                             border pairs rounded to whole numbers, give other tables for the same low and
+                             high (base 150000, 4096 tokens, factor 32: middle pairs differ by up to 4.3
+                             times): models trained with such a rule need their own table */
 } pa_rotary_scaling;
 
 /* Host only: fills frequencies (host int64 [rotary_dim / 2]), ready for a host-to-device copy.  factor for
- * every scaling but PLAIN; original_len, low, high for PARTS (1 and 32 are usual, with the options'
- * magnitude 0.1 ln(factor) + 1).  Tables of other rules are filled by the caller.
+ * every scaling but PLAIN; original_len, low, high for PARTS, as the model's rule gives them (some
+ * rules come with the options' magnitude 0.1 ln(factor) + 1).  Tables of other rules are filled by the caller.
  * PA_ERR_INVALID_ARG: an odd rotary_dim, values that are not positive and finite, low >= high. */
 int pa_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, double original_len, double low,
                           double high, int64_t *frequencies);
@@ -525,12 +529,18 @@ int pa_attention_varlen(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
  * Tokens of a page that is read which no query of the sequence sees never reach the output, whatever
  * they hold.  A value row (V) that some query sees is multiplied by a weight of zero for the other queries of
  * its sequence in the same call, as in pa_attention_varlen: an infinity or NaN in it reaches them too.
- * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen).
+ * Where window + sinks reaches max_blocks_per_seq * 16 the call is pa_decode_opt (pa_attention_varlen), its
+ * kernels and its cost too: long chunks over heads of 256 and over quantised caches, which the query tile serves
+ * only under a window (below), then run in columns of 8, several times slower; a table wider than that keeps
+ * them on it.
  * pa_attention_window's kernels are pa_attention_varlen's; on 16-bit caches of head size 256, too, chunks of 40
  * or more query columns per KV head run on the query-tile kernel (partition_size 0 or -1).  Over E4M3 and 4-bit
  * caches, calls of 128 or more columns a sequence on average, and of 16384 or more in all KV heads, run there too
  * where the workspace (the library's, or a caller's of pa_decode_window_workspace_size bytes) holds the pages that
- * the chunks see as 16-bit ones, up to 1 GiB; the values are exact.  Else they run in columns, without a workspace.
+ * the chunks see as 16-bit ones, up to 1 GiB; the values are exact.  Else they run in columns, without a workspace:
+ * a library-held one that cannot grow, or a caller's that is smaller, is no error (and what a stream capture takes
+ * stays in its graph).  The library keeps what it has grown to; calls, and replays of captured ones, that use its
+ * workspace on different streams must not overlap (see pa_decode).
  * Under a window a partition_size counts the visible tokens' pages, so it can be small; 0 chooses whole
  * units or a cluster split (no workspace but for widened pages).  A step's rows are written before (pa_rotary_and_cache,
  * pa_reshape_and_cache): pa_decode_step and pa_decode_accumulate see the whole history.
@@ -543,9 +553,13 @@ int pa_attention_window(pa_tensor *out, const pa_tensor *q, const pa_tensor *k_c
                         float scale, int num_kv_heads, int max_query_len, int window, int sinks,
                         const pa_decode_options *opt, pa_stream_t stream);
 
-/* Bytes of workspace that either call needs for this shape and partition_size on the current device (0 when
- * it does not split, for invalid arguments, or when no device can be queried).  kv_dtype_code: pa_dtype of
- * the cache; max_query_len: 1 for pa_decode_window.  Host-only. */
+/* Bytes of workspace for either call of this shape and partition_size on the current device (0 when it needs
+ * none, for invalid arguments, or when no device can be queried): what a split call needs, and what a long chunk
+ * over a quantised cache (split or not asked for: partition_size 0 and -1) can use for its widened pages, up to about
+ * 1 GiB; with less a split call is refused (PA_ERR_WORKSPACE), and such a chunk runs in columns.
+ * kv_dtype_code: pa_dtype of the cache; max_query_len: 1 for pa_decode_window.  Zero-filled once before its first
+ * use, and again between calls of which one splits and which differ in sequences, heads or max_query_len: those have
+ * their counters elsewhere (see pa_decode_ex).  Host-only. */
 size_t pa_decode_window_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                        int max_blocks_per_seq, int kv_dtype_code, int window, int sinks,
                                        int max_query_len, int partition_size);

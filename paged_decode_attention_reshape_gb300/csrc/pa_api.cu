@@ -302,7 +302,9 @@ bool on_query_tiles(int kind, int D, int partition_size, int columns, bool windo
 // 208 / 170 (371 / 383), 128 275 / 171 (490 / 388), 256 543 / 208 (973 / 567), 2048 4100 / 740.  With few items
 // a query tile's walk over the window lasts longer than all the columns' (window 4096, 128 columns: 1024 items
 // 105 / 174 (178 / 262), 2048 items 179 / 209 (313 / 325); 256 columns: 2048 183 / 132 (315 / 264)).  4-bit pages
-// gain more (64 sequences, 128 columns: 296 / 160 (420 / 362); 64-wide heads 246 / 82).
+// gain more (64 sequences, 128 columns: 296 / 160 (420 / 362); 64-wide heads 246 / 82).  The thresholds know neither the
+// window nor the cache: at 96 columns and window 1024 they take the slower side (heads of 128), and at 2048 items
+// and window 4096 with 128 columns as well.
 constexpr int kWidenColumns = 128;
 constexpr int kWidenItems = 2048;
 constexpr int64_t kWidenBytes = 1ll << 30;

@@ -319,7 +319,8 @@ cudaError_t launch_chunk_window(const DecodeParams &p, int kind, const CUtensorM
                                 const CUtensorMap &tmQ, cudaStream_t st);
 // Query columns per KV head (max_query_len x G) from which varlen attention uses it: below
 // that the column-group kernels are as fast or faster (256 sequences of 512-4096 tokens, 32/8
-// heads: at 32 columns 644 vs 737 us at head size 128, but 453 vs 325 us at head size 64).  Head size 256,
+// heads, no window: at 32 columns 644 vs 737 us at head size 128, but 453 vs 325 us at head size 64; the same
+// borders hold under a window, where they have not been measured).  Head size 256,
 // under a window alone (64 x 1k..8k tokens, 32/8 heads, window 1024, columns / tile): 16 columns 138 / 249 us, 32 247 /
 // 250, 40 300 / 251, 64 465 / 247, 2048 14424 / 2185.
 constexpr int chunk_min_columns(int D) { return D == 256 ? 40 : D == 64 ? 32 : 64; }
